@@ -634,6 +634,152 @@ int dopt_state_to_model(const dopt_shard_map* map, int32_t buffer, int32_t rank,
 int dopt_state_from_model(const dopt_shard_map* map, int32_t buffer, int32_t rank, int32_t layout,
                           const void* model, void* state, dopt_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * The optimizer step over a list of tensors.
+ *
+ * The same step -- global grad norm, clip, skip, AdamW, cast into the param
+ * -- for params that are not laid out in a sharded buffer: a list of
+ * separate tensors, each with its own param, grad and state arrays (views
+ * of larger buffers, a model's params as its framework allocated them, the
+ * tensors of one rank).  A list is an array of dopt_tensor in host memory,
+ * read during the call only (the pointers it holds are used until the
+ * call's work on the stream has run).  Every array of a tensor is contiguous
+ * and has `numel` elements; it needs only its own elements' alignment (4
+ * bytes for fp32, 2 for bf16/fp16, 1 for codes) -- a tensor whose arrays
+ * all start on 32-byte boundaries takes the vector path.  Arrays of one
+ * call must not overlap, but for the list's read-only grads.
+ *
+ * Moments are held in fp32, or in 8 bits per element (DOPT_MOMENTS_8BIT,
+ * per tensor; one list may hold both).  The 8-bit moments of a tensor are
+ * cut into blocks of DOPT_MOMENT_BLOCK consecutive elements (the last may
+ * be shorter), each with one scale byte per moment, s:
+ *   exp_avg    : e4m3 code x 2^(s - 127), rounded to nearest even, with
+ *                s = max(E - 8, 8), E = (bits(max |m|) + 0x1FFFFF) >> 23:
+ *                the smallest power of two that keeps the largest at most
+ *                448 = the largest e4m3 value.
+ *   exp_avg_sq : code 0 is zero; code c > 0 is the fp32 number with bits
+ *                (s << 23) + (c << 20): five exponent and three mantissa
+ *                bits, no sign (a second moment has none), with
+ *                s = max(E - 31, 0), E = (bits(max v) + 0x0FFFFF) >> 23.
+ *                c = (bits(v) + R - (s << 23)) >> 20, at least 1 for v > 0,
+ *                so a moment that is not zero never divides like zero.
+ *   bits(x) is the fp32 pattern of x as an integer.  Where E >= 255 (a
+ *   moment that is infinite, NaN or above the largest value) the block's
+ *   codes are 0 and its scale byte is 255, and all of it reads as NaN.
+ * R is 0x80000 (nearest) in dopt_state8_pack.  In the step it is r << 4, r
+ * 16 pseudo-random bits of (seed, step, tensor, element), so that exp_avg_sq
+ * is right in the mean: it moves by about 1 - beta2 per step, far less
+ * than the 3 to 6 % of half a code, and nearest rounding would freeze it.
+ * (exp_avg moves by 1 - beta1, which nearest rounding follows.)  For
+ * element i of the list's tensor number k in step t, all in 32 bits unless
+ * said:
+ *   x = (i / 2) * 0x9E3779B9 + seed + k * 0x510E527F + t * 0x6A09E667;
+ *   p = x * 0xBB67AE85 (64 bits); x = low(p) ^ high(p);
+ *   p = x * 0xA54FF53B (64 bits); x = low(p) ^ high(p);
+ *   r = the low half of x for even i, the high half for odd i.
+ * The values of 8-bit moments are exact in bf16.
+ */
+typedef enum {
+  DOPT_MOMENTS_F32 = 0, /* exp_avg, exp_avg_sq: float; no scales            */
+  DOPT_MOMENTS_8BIT = 1 /* uint8 codes, and one scale byte per block each   */
+} dopt_moments;
+
+#define DOPT_MOMENT_BLOCK 256
+
+/* One tensor of a list.  Pointers of a tensor with numel 0 are ignored. */
+typedef struct {
+  int64_t numel;      /* >= 0                                                */
+  int32_t param_dtype, grad_dtype; /* dopt_dtype; the grad's is the param's
+                                      or fp32                               */
+  int32_t moments;    /* dopt_moments                                        */
+  int32_t reserved;
+  double wd_mult;     /* weight-decay multiplier of this tensor              */
+  void* param;
+  const void* grad;
+  float* master;      /* bf16/fp16 params: the fp32 weights; fp32 params are
+                         stepped in place: NULL                             */
+  void* exp_avg;      /* float, or codes                                     */
+  void* exp_avg_sq;
+  uint8_t* exp_avg_scale;    /* 8-bit moments: dopt_moment_blocks(numel)     */
+  uint8_t* exp_avg_sq_scale; /* bytes each; else NULL                        */
+} dopt_tensor;
+
+/* ceil(numel / DOPT_MOMENT_BLOCK); DOPT_E_INVALID for a negative numel. */
+int64_t dopt_moment_blocks(int64_t numel);
+
+/* Workspace bytes of dopt_tensors_grad_norm and dopt_tensors_step for a
+ * list of n_tensors tensors (0 on a negative count). */
+size_t dopt_tensors_workspace_bytes(int32_t n_tensors);
+
+/*
+ * Global norm, clip coefficient and non-finite flag of a list's grads, as
+ * dopt_grad_norm gives them for a sharded buffer: with g = fp32(grad) *
+ * inv_loss_scale over every element of every tensor,
+ *   *d_norm      = sqrt(sum g^2) as fp32, NaN when found_inf;
+ *   *d_clip_coef = max_norm / (norm + 1e-6) when max_norm > 0 and that is
+ *                  < 1, else 1;
+ *   *d_found_inf = 1 if any g is non-finite.
+ * Any of the three may be NULL.  Only grad, grad_dtype and numel of the
+ * tensors are used.  Squares are added in fp32 over 8 or 16 elements of a
+ * thread, then in fp64 in a fixed order: the same list gives the same bits
+ * on the same kind of GPU.  Elements whose squares would leave the fp32 range
+ * are squared in fp64.  dopt_read_step_stats reads the statistics (with
+ * the count of zero grads) from the workspace.
+ * An empty list (n_tensors 0) has norm 0.
+ */
+int dopt_tensors_grad_norm(const dopt_tensor* tensors, int32_t n_tensors, float inv_loss_scale,
+                           double max_norm, void* workspace, size_t workspace_bytes, float* d_norm,
+                           float* d_clip_coef, int32_t* d_found_inf, dopt_stream stream);
+
+/*
+ * AdamW over a list of tensors: per element the arithmetic of
+ * dopt_adam_step (each operation rounded once in fp32), with
+ *   g = (fp32(grad) * inv_loss_scale) * (*d_clip_coef)
+ * and, for 8-bit moments, the stored values widened before the update and
+ * the new ones rounded to codes after it (the weight is stepped with the
+ * new moments before that rounding).  `seed` is the stochastic rounding's.
+ * d_clip_coef NULL: 1.  If d_found_inf is given and *d_found_inf is nonzero,
+ * nothing is written.
+ */
+int dopt_tensors_adam_step(const dopt_tensor* tensors, int32_t n_tensors,
+                           const dopt_adamw_hparams* hp, float inv_loss_scale, uint32_t seed,
+                           const float* d_clip_coef, const int32_t* d_found_inf,
+                           dopt_stream stream);
+
+/*
+ * The whole step over a list: dopt_tensors_grad_norm, then
+ * dopt_tensors_adam_step with its clip coefficient and skip flag, without
+ * waiting for either.  d_found_inf and d_norm (either may be NULL) receive
+ * the results.  d_step and d_lr as in dopt_step_args: with d_step the step
+ * number lives in device memory (hp->step is ignored, a skipped step does
+ * not count), so a captured step can be replayed from a CUDA graph once it
+ * has run on the device.
+ */
+int dopt_tensors_step(const dopt_tensor* tensors, int32_t n_tensors, const dopt_adamw_hparams* hp,
+                      float inv_loss_scale, double max_norm, uint32_t seed, int64_t* d_step,
+                      const double* d_lr, void* workspace, size_t workspace_bytes,
+                      int32_t* d_found_inf, float* d_norm, dopt_stream stream);
+
+/* The moments of one tensor as values (fp32 or bf16) and as 8-bit codes.
+ * Either moment may be left out by a NULL values pointer (its code and
+ * scale pointers are then ignored). */
+typedef struct {
+  int64_t numel;
+  int32_t values_dtype; /* DOPT_F32 or DOPT_BF16                             */
+  int32_t reserved;
+  void* exp_avg;        /* values                                            */
+  void* exp_avg_sq;
+  uint8_t* exp_avg_codes;
+  uint8_t* exp_avg_sq_codes;
+  uint8_t* exp_avg_scale;    /* dopt_moment_blocks(numel) bytes              */
+  uint8_t* exp_avg_sq_scale;
+} dopt_moment_tensor;
+
+/* Values to 8-bit codes and scales (rounded to nearest; a negative
+ * exp_avg_sq is taken as NaN), and back (exact in both value types). */
+int dopt_state8_pack(const dopt_moment_tensor* tensors, int32_t n_tensors, dopt_stream stream);
+int dopt_state8_unpack(const dopt_moment_tensor* tensors, int32_t n_tensors, dopt_stream stream);
+
 #if defined(DOPT_BOUNDS_CHECK) && DOPT_BOUNDS_CHECK
 /* Debug builds only (DOPT_BOUNDS_CHECK=1): the release library neither
  * exports this hook nor tests for it in its kernels.  Test hook for the

@@ -26,6 +26,8 @@ F32, BF16, F16 = 0, 1, 2
 OK, E_INVALID, E_ALIGN, E_SIZE, E_CUDA, E_NOMEM = 0, -1, -2, -3, -4, -5
 GROUP_FP32_FROM_FLOAT16, GROUP_FP32 = 0, 1
 LAYOUT_FULL_BUFFER, LAYOUT_SHARD_ONLY, LAYOUT_BUCKET = 0, 1, 2
+MOMENTS_F32, MOMENTS_8BIT = 0, 1
+MOMENT_BLOCK = 256
 ALL_RANKS = -1
 MAX_REPLICAS = 64
 
@@ -90,6 +92,18 @@ class dopt_loss_scaler(ctypes.Structure):
                 ("growth_tracker", _I32), ("hysteresis_tracker", _I32)]
 
 
+class dopt_tensor(ctypes.Structure):
+    _fields_ = [("numel", _I64), ("param_dtype", _I32), ("grad_dtype", _I32), ("moments", _I32),
+                ("reserved", _I32), ("wd_mult", _D), ("param", _P), ("grad", _P), ("master", _P),
+                ("exp_avg", _P), ("exp_avg_sq", _P), ("exp_avg_scale", _P), ("exp_avg_sq_scale", _P)]
+
+
+class dopt_moment_tensor(ctypes.Structure):
+    _fields_ = [("numel", _I64), ("values_dtype", _I32), ("reserved", _I32), ("exp_avg", _P),
+                ("exp_avg_sq", _P), ("exp_avg_codes", _P), ("exp_avg_sq_codes", _P),
+                ("exp_avg_scale", _P), ("exp_avg_sq_scale", _P)]
+
+
 def _proto(name, res, *args):
     fn = getattr(_lib, name)
     fn.restype = res
@@ -150,6 +164,17 @@ _c = {
                                       ctypes.POINTER(dopt_loss_scaler), _I32),
     "dopt_kernel_launches": _proto("dopt_kernel_launches", ctypes.c_uint64),
     "dopt_step_local_stats": _proto("dopt_step_local_stats", ctypes.c_int, ctypes.POINTER(dopt_step_args), _P, _P),
+    "dopt_moment_blocks": _proto("dopt_moment_blocks", _I64, _I64),
+    "dopt_tensors_workspace_bytes": _proto("dopt_tensors_workspace_bytes", _SZ, _I32),
+    "dopt_tensors_grad_norm": _proto("dopt_tensors_grad_norm", ctypes.c_int, _P, _I32, _F, _D, _P, _SZ,
+                                     _P, _P, _P, _P),
+    "dopt_tensors_adam_step": _proto("dopt_tensors_adam_step", ctypes.c_int, _P, _I32,
+                                     ctypes.POINTER(dopt_adamw_hparams), _F, ctypes.c_uint32, _P, _P, _P),
+    "dopt_tensors_step": _proto("dopt_tensors_step", ctypes.c_int, _P, _I32,
+                                ctypes.POINTER(dopt_adamw_hparams), _F, _D, ctypes.c_uint32, _P, _P, _P,
+                                _SZ, _P, _P, _P),
+    "dopt_state8_pack": _proto("dopt_state8_pack", ctypes.c_int, _P, _I32, _P),
+    "dopt_state8_unpack": _proto("dopt_state8_unpack", ctypes.c_int, _P, _I32, _P),
     "dopt_debug_bounds_record": _proto("dopt_debug_bounds_record", ctypes.c_int, ctypes.POINTER(_I64)),
     "dopt_read_step_stats": _proto("dopt_read_step_stats", ctypes.c_int, _P,
                                    ctypes.POINTER(dopt_step_stats), _P),
@@ -536,10 +561,161 @@ def dopt_loss_scaler_update(s, found_inf):
     return s.scale
 
 
+def _array(entry, name, numel, dtypes, where):
+    """(pointer, numel, dtype name) of a list entry's array: a pointer, or a
+    torch tensor, which must be contiguous, of one of `dtypes` (torch dtype
+    names) and of `numel` elements (None: any)."""
+    x = entry.get(name)
+    if x is None or not hasattr(x, "data_ptr"):
+        return _ptr(x), numel, None
+    dt = str(x.dtype).replace("torch.", "")
+    if not x.is_contiguous():
+        raise DoptError(E_INVALID, f"{where}: {name} is not contiguous")
+    if dt not in dtypes:
+        raise DoptError(E_INVALID, f"{where}: {name} is {dt}, not {' or '.join(dtypes)}")
+    if numel is not None and x.numel() != numel:
+        raise DoptError(E_INVALID, f"{where}: {name} has {x.numel()} elements, not {numel}")
+    return x.data_ptr(), x.numel(), dt
+
+
+_DTYPE = {"float32": F32, "bfloat16": BF16, "float16": F16}
+
+
+class TensorList:
+    """A marshalled list of dopt_tensor (and the owner of its arrays'
+    references).  entries: one dict per tensor with grad and, to step it,
+    param, exp_avg, exp_avg_sq and, for bf16/fp16 params, master; 8-bit
+    moments (uint8 codes) also take exp_avg_scale and exp_avg_sq_scale
+    (uint8, dopt_moment_blocks(numel) each); optional wd_mult (1.0).  Arrays
+    are contiguous torch tensors, whose sizes and dtypes are checked and
+    used, or device pointers; an entry of pointers also gives numel,
+    param_dtype, grad_dtype and moments."""
+
+    def __init__(self, entries):
+        self.n = len(entries)
+        self.c = (dopt_tensor * max(1, self.n))()
+        self._keep = [dict(e) for e in entries]
+        for k, e in enumerate(entries):
+            where = f"tensor {k}"
+            t = self.c[k]
+            param, n, pdt = _array(e, "param", e.get("numel"), _DTYPE, where)
+            t.grad, n, gdt = _array(e, "grad", n, _DTYPE, where)
+            if n is None:
+                raise DoptError(E_INVALID, f"{where}: numel is not given")
+            t.numel, t.param = int(n), param
+            t.grad_dtype = _DTYPE[gdt] if gdt else int(e.get("grad_dtype", F32))
+            t.param_dtype = _DTYPE[pdt] if pdt else int(e.get("param_dtype", t.grad_dtype))
+            t.master = _array(e, "master", n, ("float32",), where)[0]
+            t.exp_avg, _, mdt = _array(e, "exp_avg", n, ("float32", "uint8"), where)
+            t.exp_avg_sq, _, vdt = _array(e, "exp_avg_sq", n, ("float32", "uint8"), where)
+            if mdt != vdt:
+                raise DoptError(E_INVALID, f"{where}: exp_avg and exp_avg_sq differ in format")
+            eight = e.get("exp_avg_scale") is not None
+            if mdt and (mdt == "uint8") != eight:
+                raise DoptError(E_INVALID, f"{where}: uint8 moments, and only they, come with scales")
+            t.moments = int(e.get("moments", MOMENTS_8BIT if eight else MOMENTS_F32))
+            blocks = dopt_moment_blocks(max(0, t.numel))
+            t.exp_avg_scale = _array(e, "exp_avg_scale", blocks, ("uint8",), where)[0]
+            t.exp_avg_sq_scale = _array(e, "exp_avg_sq_scale", blocks, ("uint8",), where)[0]
+            t.wd_mult = float(e.get("wd_mult", 1.0))
+
+    def set_grads(self, grads):
+        """Points the tensors at other grads (same sizes and dtypes)."""
+        if len(grads) != self.n:
+            raise DoptError(E_INVALID, f"{len(grads)} grads for {self.n} tensors")
+        ptrs = []
+        for k, g in enumerate(grads):
+            ptr, _, dt = _array(dict(grad=g), "grad", self.c[k].numel, _DTYPE, f"tensor {k}")
+            if dt and _DTYPE[dt] != self.c[k].grad_dtype:
+                raise DoptError(E_INVALID, f"tensor {k}: grad is {dt}, unlike before")
+            ptrs.append(ptr)
+        for k, (g, ptr) in enumerate(zip(grads, ptrs)):
+            self.c[k].grad = ptr
+            self._keep[k]["grad"] = g
+
+
+class MomentList:
+    """A marshalled list of dopt_moment_tensor.  entries: one dict per tensor
+    with exp_avg and/or exp_avg_sq (values: float32 or bfloat16), and for each
+    its codes (exp_avg_codes, uint8) and scales (exp_avg_scale, uint8,
+    dopt_moment_blocks(numel)); contiguous torch tensors, or device pointers
+    with numel and values_dtype."""
+
+    def __init__(self, entries):
+        self.n = len(entries)
+        self.c = (dopt_moment_tensor * max(1, self.n))()
+        self._keep = [dict(e) for e in entries]
+        values = ("float32", "bfloat16")
+        for k, e in enumerate(entries):
+            where = f"tensor {k}"
+            t = self.c[k]
+            t.exp_avg, n, mdt = _array(e, "exp_avg", e.get("numel"), values, where)
+            t.exp_avg_sq, n, vdt = _array(e, "exp_avg_sq", n, values, where)
+            if n is None:
+                raise DoptError(E_INVALID, f"{where}: numel is not given")
+            if mdt and vdt and mdt != vdt:
+                raise DoptError(E_INVALID, f"{where}: exp_avg and exp_avg_sq differ in dtype")
+            t.numel = int(n)
+            t.values_dtype = _DTYPE[mdt or vdt] if mdt or vdt else int(e.get("values_dtype", F32))
+            blocks = dopt_moment_blocks(max(0, t.numel))
+            for name in ("exp_avg", "exp_avg_sq"):
+                setattr(t, name + "_codes", _array(e, name + "_codes", t.numel, ("uint8",), where)[0])
+                setattr(t, name + "_scale", _array(e, name + "_scale", blocks, ("uint8",), where)[0])
+
+
+def dopt_moment_blocks(numel):
+    """Scale bytes of one 8-bit moment of numel elements."""
+    return _check(_c["dopt_moment_blocks"](numel))
+
+
+def dopt_tensors_workspace_bytes(n_tensors):
+    v = _c["dopt_tensors_workspace_bytes"](n_tensors)
+    if v == 0:
+        raise DoptError(E_INVALID, dopt_last_error())
+    return v
+
+
+def dopt_tensors_grad_norm(tensors, inv_loss_scale, max_norm, workspace, workspace_bytes, d_norm,
+                           d_clip_coef, d_found_inf, stream=None):
+    """Grad norm, clip coefficient and non-finite flag (device scalars) of a
+    TensorList."""
+    _check(_c["dopt_tensors_grad_norm"](tensors.c, tensors.n, inv_loss_scale, max_norm, _ptr(workspace),
+                                        workspace_bytes, _ptr(d_norm), _ptr(d_clip_coef), _ptr(d_found_inf),
+                                        _stream(stream)))
+
+
+def dopt_tensors_adam_step(tensors, hp, step, inv_loss_scale=1.0, seed=0, d_clip_coef=None,
+                           d_found_inf=None, stream=None):
+    """AdamW over a TensorList; seed: of the 8-bit second moments' rounding."""
+    h = _hparams(hp, step)
+    _check(_c["dopt_tensors_adam_step"](tensors.c, tensors.n, ctypes.byref(h), inv_loss_scale,
+                                        seed & 0xFFFFFFFF, _ptr(d_clip_coef), _ptr(d_found_inf),
+                                        _stream(stream)))
+
+
+def dopt_tensors_step(tensors, hp, step, workspace, workspace_bytes, *, inv_loss_scale=1.0, max_norm=1.0,
+                      seed=0, d_step=None, d_lr=None, d_found_inf=None, d_norm=None, stream=None):
+    """Grad norm, clip, skip and AdamW over a TensorList, without waiting."""
+    h = _hparams(hp, step)
+    _check(_c["dopt_tensors_step"](tensors.c, tensors.n, ctypes.byref(h), inv_loss_scale, max_norm,
+                                   seed & 0xFFFFFFFF, _ptr(d_step), _ptr(d_lr), _ptr(workspace),
+                                   workspace_bytes, _ptr(d_found_inf), _ptr(d_norm), _stream(stream)))
+
+
+def dopt_state8_pack(moments, stream=None):
+    """The values of a MomentList into its 8-bit codes and scales."""
+    _check(_c["dopt_state8_pack"](moments.c, moments.n, _stream(stream)))
+
+
+def dopt_state8_unpack(moments, stream=None):
+    """The codes and scales of a MomentList into its values."""
+    _check(_c["dopt_state8_unpack"](moments.c, moments.n, _stream(stream)))
+
+
 def exported_symbols():
     """Names of the C entry points this binding resolved in the library."""
     return sorted(_c)
 
 
 __all__ = [n for n in dir() if n.startswith("dopt_")] + [
-    "ShardMap", "StepArgs", "DoptError", "exported_symbols"]
+    "ShardMap", "StepArgs", "TensorList", "MomentList", "DoptError", "exported_symbols"]

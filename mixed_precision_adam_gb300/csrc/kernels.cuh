@@ -4,6 +4,7 @@
 // helpers.  Included by every CUDA translation unit of the library:
 //   k1_f32.cu, k1_bf16.cu, k1_f16.cu -- K1 reduce/prepare, one grad dtype each
 //   k3.cu                             -- K3 AdamW + cast back
+//   tensors*.cu                       -- the step over a list of tensors (tensors.cuh)
 //   dopt_cuda.cu                      -- K2 finalize and the C entry points
 //
 // The step is three HBM-bound passes over the selected shard(s):

@@ -1,0 +1,215 @@
+// tensors.cuh -- what the kernels over a list of tensors share: the launch
+// tables (a tensor's pointers, length and first tile, by value in the kernel
+// parameters, as the run tables of the sharded step), typed loads and
+// stores, the AdamW arithmetic, and the 8-bit moments' encoding.
+//   tensors.cu        -- the C entry points: checks, tables, launches
+//   tensors_norm.cu   -- the grad norm (with the finalize in its last CTA)
+//   tensors_adamw.cu  -- AdamW with fp32 moments
+//   tensors_adamw8.cu -- AdamW with 8-bit moments, and their pack / unpack
+#pragma once
+
+#include "kernels.cuh"
+
+namespace dopt {
+
+constexpr int kMomentBlock = DOPT_MOMENT_BLOCK;
+
+// ------------------------------------------------------------ launch tables --
+
+// One tensor's grad in a norm launch.
+struct NormSeg {
+  const void* grad;
+  int64_t len;
+  int32_t tile0;  // first tile of this tensor in the launch
+  int32_t dtype;  // dopt_dtype of the grad
+};
+constexpr int kNormCap = 1280, kNormSmallCap = 64;
+constexpr int kNormTile = 8192;  // elements per tile
+
+struct NormHead {
+  Partial* partials;      // one slot per CTA of this launch
+  float inv_scale;
+  uint32_t* fin_counter;  // last launch of a call: the finalize's ticket counter, else NULL
+  FinalizeArgs fin;
+  int32_t n_seg, n_tiles;
+};
+template <int CAP>
+struct NormParamsT : NormHead {
+  NormSeg seg[CAP];
+};
+static_assert(sizeof(NormParamsT<kNormCap>) <= 32764, "kernel parameter limit");
+
+// One tensor in an AdamW launch.
+struct AdamSeg {
+  void* param;
+  const void* grad;
+  float* weight;  // the fp32 weights: the master copy, or the fp32 param itself
+  void* m;
+  void* v;
+  uint8_t* m_scale;
+  uint8_t* v_scale;
+  int64_t len;
+  union {
+    double wd_mult;  // device step scalars: the decay is formed on the device
+    float decay;     // host step scalars: (float)(1 - lr * wd * wd_mult)
+  };
+  int32_t tile0;
+  uint32_t key;  // 8-bit moments: the tensor's term of the rounding hash
+};
+constexpr int kAdamCap = 400, kAdamSmallCap = 40;
+constexpr int kAdamTile = 2048;  // elements per tile
+
+struct AdamHead {
+  const float* coef;        // device scalar, or NULL: 1
+  const int32_t* found_inf; // device flag, or NULL: never skipped
+  const DevStep* dev;       // step scalars from the finalize pass, or NULL: the fields below
+  const int64_t* d_step;    // with dev: the step number (already advanced to this step's)
+  double lr_wd;
+  float b1, b2, omb1, omb2, eps, step_size, bc2_sqrt;
+  float inv_scale;
+  uint32_t key;    // seed (+ the step's term, unless d_step)
+  int32_t early;   // 1: this launch follows a kernel of the same call that writes none of its state
+  int32_t n_seg, n_tiles;
+};
+template <int CAP>
+struct AdamParamsT : AdamHead {
+  AdamSeg seg[CAP];
+};
+static_assert(sizeof(AdamParamsT<kAdamCap>) <= 32764, "kernel parameter limit");
+static_assert(sizeof(AdamParamsT<kAdamSmallCap>) <= 4096, "compact parameters");
+
+// One tensor in a pack or unpack launch.
+struct MomentSeg {
+  void* m;  // values
+  void* v;
+  uint8_t* mc;  // codes
+  uint8_t* vc;
+  uint8_t* ms;  // scales
+  uint8_t* vs;
+  int64_t len;
+  int32_t tile0;
+  int32_t reserved;
+};
+constexpr int kMomentCap = 500, kMomentSmallCap = 60;
+template <int CAP>
+struct MomentParamsT {
+  int32_t n_seg, n_tiles;
+  MomentSeg seg[CAP];
+};
+static_assert(sizeof(MomentParamsT<kMomentCap>) <= 32764, "kernel parameter limit");
+
+// The rounding hash's terms, as the header states them.
+constexpr uint32_t kHashPair = 0x9E3779B9u, kHashTensor = 0x510E527Fu, kHashStep = 0x6A09E667u;
+constexpr uint32_t kHashMul1 = 0xBB67AE85u, kHashMul2 = 0xA54FF53Bu;
+
+// The tensor holding tile t, by bisection (a CTA's first tile).
+template <typename P>
+__device__ __forceinline__ int find_seg(const P& p, int t) {
+  int lo = 0, hi = p.n_seg - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.seg[mid].tile0 <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+// The same for a later tile, from the one before.
+template <typename P>
+__device__ __forceinline__ int next_seg(const P& p, int si, int t) {
+  while (si + 1 < p.n_seg && p.seg[si + 1].tile0 <= t) ++si;
+  return si;
+}
+
+// ------------------------------------------------------- elements by type --
+
+template <typename T>
+__device__ __forceinline__ float widen(T x);
+template <>
+__device__ __forceinline__ float widen<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float widen<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <>
+__device__ __forceinline__ float widen<__half>(__half x) { return __half2float(x); }
+
+template <typename T>
+__device__ __forceinline__ T narrow(float x);
+template <>
+__device__ __forceinline__ float narrow<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half narrow<__half>(float x) { return __float2half_rn(x); }
+
+// One element of AdamW, each operation rounded once in fp32: the arithmetic
+// of the sharded step's AdamW pass.
+struct AdamScalars {
+  float c, decay, step_size, bc2_sqrt;
+};
+__device__ __forceinline__ void adamw_element(float g, const AdamHead& p, const AdamScalars& s, float& w, float& m,
+                                              float& v) {
+  g = __fmul_rn(__fmul_rn(g, p.inv_scale), s.c);
+  w = __fmul_rn(w, s.decay);
+  m = __fadd_rn(__fmul_rn(p.b1, m), __fmul_rn(p.omb1, g));
+  v = __fadd_rn(__fmul_rn(p.b2, v), __fmul_rn(__fmul_rn(p.omb2, g), g));
+  const float denom = __fadd_rn(__fdiv_rn(__fsqrt_rn(v), s.bc2_sqrt), p.eps);
+  w = __fsub_rn(w, __fmul_rn(s.step_size, __fdiv_rn(m, denom)));
+}
+
+// The decoupled weight-decay factor of a tensor; in fp64, so out of line and
+// once per tensor only when the step scalars live on the device.
+static __device__ __noinline__ float tensor_decay(double lr_wd, double wd_mult) {
+  return (float)(1.0 - lr_wd * wd_mult);
+}
+__device__ __forceinline__ float decay_of_seg(const AdamHead& p, const AdamSeg& sg) {
+  return p.dev ? tensor_decay(p.dev->lr_wd, sg.wd_mult) : sg.decay;
+}
+
+// ----------------------------------------------------------- host launches --
+
+// Launch of one kernel over a table; `early` tables may start under the
+// kernel before them (programmatic stream serialization): each CTA waits
+// for that grid before it reads or writes anything it may share with it.
+template <typename K, typename P>
+int launch_table(K kern, const P& params, int n_tiles, cudaStream_t s, const char* what, int* grid_out = nullptr,
+                 bool programmatic = false) {
+  int grid = 0;
+  int st = grid_for(kern, n_tiles, &grid);
+  if (st) return st;
+  if (grid_out) *grid_out = grid;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = programmatic ? 1 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, params);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();  // reported here, not left for the next call to find
+    return fail(DOPT_E_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+  }
+  return check_launch(what);
+}
+
+// One launch each; the table's own count picks the compact parameter block.
+int launch_tensors_norm(const NormParamsT<kNormCap>& p, cudaStream_t s, int* grid);
+int tensors_norm_grid(int n_seg, int n_tiles, int* grid);
+int launch_tensors_adamw(int32_t param_dtype, int32_t grad_dtype, const AdamParamsT<kAdamCap>& p, cudaStream_t s);
+int launch_tensors_adamw8(int32_t param_dtype, int32_t grad_dtype, const AdamParamsT<kAdamCap>& p, cudaStream_t s);
+int launch_state8_pack(int32_t values_dtype, const MomentParamsT<kMomentCap>& p, cudaStream_t s);
+int launch_state8_unpack(int32_t values_dtype, const MomentParamsT<kMomentCap>& p, cudaStream_t s);
+
+// A table's parameters with room for CAP entries only.
+template <typename Small, typename Head, typename Big>
+Small compact_table(const Big& b) {
+  Small out{};
+  static_cast<Head&>(out) = static_cast<const Head&>(b);
+  for (int i = 0; i < b.n_seg; ++i) out.seg[i] = b.seg[i];
+  return out;
+}
+
+}  // namespace dopt
