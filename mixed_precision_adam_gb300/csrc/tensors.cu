@@ -16,10 +16,10 @@ std::string at(const char* fn, int32_t k) { return std::string(fn) + ": tensor "
 
 int64_t tiles_of(int64_t numel, int tile) { return numel / tile + (numel % tile != 0); }
 
-// Adds a tensor's tiles to a list's count; false when a launch could not
-// number them (about 4e12 elements).
+// Adds a tensor's tiles (of the smallest size used, with one to spare) to a
+// list's count; false when a launch could not number them (2e12 elements).
 bool count_tiles(int64_t numel, int64_t* total) {
-  *total += tiles_of(numel, std::min(kAdamTile, kNormTile));
+  *total += tiles_of(numel, 1024) + 1;
   return *total <= INT32_MAX;
 }
 
@@ -124,8 +124,10 @@ int run_norm(const dopt_tensor* ts, int32_t n, float inv_scale, FinalizeArgs fin
     for (; k < n; ++k) {
       if (ts[k].numel == 0) continue;
       if (p.n_seg == kNormCap) break;
-      p.seg[p.n_seg++] = NormSeg{ts[k].grad, ts[k].numel, p.n_tiles, ts[k].grad_dtype};
-      p.n_tiles += (int32_t)tiles_of(ts[k].numel, kNormTile);
+      const size_t elem = dtype_bytes(ts[k].grad_dtype);
+      const int16_t shift = (int16_t)((reinterpret_cast<uintptr_t>(ts[k].grad) & 15u) / elem);
+      p.seg[p.n_seg++] = NormSeg{ts[k].grad, ts[k].numel, p.n_tiles, (int16_t)ts[k].grad_dtype, shift};
+      p.n_tiles += (int32_t)tiles_of(ts[k].numel + shift, kNormTileBytes / (int)elem);
     }
     int grid = 0;
     int st = tensors_norm_grid(p.n_seg, p.n_tiles, &grid);
@@ -139,6 +141,17 @@ int run_norm(const dopt_tensor* ts, int32_t n, float inv_scale, FinalizeArgs fin
     if (last) return DOPT_OK;
     p.n_seg = p.n_tiles = 0;
   }
+}
+
+// AdamSeg::shift of a tensor with fp32 moments: its first element's index
+// within the groups of four that its arrays are read in, when they agree
+// (separate allocations, or views of buffers at one element offset).
+int32_t common_shift(const AdamSeg& g, int32_t pd, int32_t gd) {
+  auto index = [](const void* p, size_t elem) { return (int32_t)(reinterpret_cast<uintptr_t>(p) / elem & 3); };
+  const int32_t at = index(g.weight, 4);
+  const bool same = index(g.m, 4) == at && index(g.v, 4) == at && index(g.grad, dtype_bytes(gd)) == at &&
+                    index(g.param, dtype_bytes(pd)) == at;
+  return same ? at : -1;
 }
 
 struct AdamJob {
@@ -204,7 +217,12 @@ int run_adamw(const dopt_tensor* ts, int32_t n, const AdamJob& j, cudaStream_t s
             g.decay = (float)(1.0 - p.lr_wd * t.wd_mult);
           g.tile0 = p.n_tiles;
           g.key = (uint32_t)k * kHashTensor;
-          p.n_tiles += (int32_t)tiles_of(t.numel, kAdamTile);
+          if (moments == DOPT_MOMENTS_F32) {
+            g.shift = common_shift(g, pd, gd);
+            p.n_tiles += (int32_t)tiles_of(t.numel + std::max(g.shift, 0), kAdamTile32);
+          } else {
+            p.n_tiles += (int32_t)tiles_of(t.numel, kAdamTile);
+          }
         }
         if (int st = flush()) return st;
       }

@@ -21,10 +21,11 @@ struct NormSeg {
   const void* grad;
   int64_t len;
   int32_t tile0;  // first tile of this tensor in the launch
-  int32_t dtype;  // dopt_dtype of the grad
+  int16_t dtype;  // dopt_dtype of the grad
+  int16_t shift;  // elements from the 16-byte boundary below the first one to it
 };
 constexpr int kNormCap = 1280, kNormSmallCap = 64;
-constexpr int kNormTile = 8192;  // elements per tile
+constexpr int kNormTileBytes = 16384;  // grads per tile
 
 struct NormHead {
   Partial* partials;      // one slot per CTA of this launch
@@ -55,9 +56,15 @@ struct AdamSeg {
   };
   int32_t tile0;
   uint32_t key;  // 8-bit moments: the tensor's term of the rounding hash
+  // Where the arrays have a common vector boundary: fp32 moments, elements
+  // from the boundary below the tensor's first element to it (0 to 3);
+  // 8-bit moments, 0 when the first element is one; -1: none.
+  int32_t shift;
+  int32_t reserved;
 };
-constexpr int kAdamCap = 400, kAdamSmallCap = 40;
-constexpr int kAdamTile = 2048;  // elements per tile
+constexpr int kAdamCap = 360, kAdamSmallCap = 40;
+constexpr int kAdamTile32 = 1024;  // elements per tile, fp32 moments
+constexpr int kAdamTile = 2048;    // elements per tile, 8-bit moments
 
 struct AdamHead {
   const float* coef;        // device scalar, or NULL: 1

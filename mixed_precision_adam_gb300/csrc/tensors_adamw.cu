@@ -1,36 +1,156 @@
 // tensors_adamw.cu -- AdamW over a list of tensors, moments in fp32.
+//
+// One pass: reads grad, weight, m and v of every element once, writes
+// weight, m, v and the 16-bit param once (28 bytes per element with bf16
+// grads and params, 30 with fp32 grads, 28 for fp32 params): bound by
+// memory.  A CTA strides over the list's tiles; a thread has four elements
+// of a tile, and loads its next tile's before it computes and stores this
+// one's, so the memory pipe stays busy under the arithmetic.
 #include "tensors.cuh"
 
 namespace dopt {
 
+// Four elements of a type, as loaded and stored at once.
+template <typename T>
+struct Four;
+template <>
+struct Four<float> {
+  using Raw = float4;
+  static __device__ __forceinline__ void widen4(const Raw& r, float* x) {
+    x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w;
+  }
+};
+template <>
+struct Four<__nv_bfloat16> {
+  using Raw = uint2;
+  static __device__ __forceinline__ void widen4(const Raw& r, float* x) {
+    x[0] = __uint_as_float(r.x << 16); x[1] = __uint_as_float(r.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(r.y << 16); x[3] = __uint_as_float(r.y & 0xFFFF0000u);
+  }
+  static __device__ __forceinline__ Raw narrow4(const float* x) {
+    const unsigned a = __bfloat16_as_ushort(__float2bfloat16_rn(x[0])), b = __bfloat16_as_ushort(__float2bfloat16_rn(x[1]));
+    const unsigned c = __bfloat16_as_ushort(__float2bfloat16_rn(x[2])), d = __bfloat16_as_ushort(__float2bfloat16_rn(x[3]));
+    return make_uint2(a | (b << 16), c | (d << 16));
+  }
+};
+template <>
+struct Four<__half> {
+  using Raw = uint2;
+  static __device__ __forceinline__ float h(unsigned bits) { return __half2float(__ushort_as_half((unsigned short)bits)); }
+  static __device__ __forceinline__ void widen4(const Raw& r, float* x) {
+    x[0] = h(r.x & 0xFFFFu); x[1] = h(r.x >> 16);
+    x[2] = h(r.y & 0xFFFFu); x[3] = h(r.y >> 16);
+  }
+  static __device__ __forceinline__ Raw narrow4(const float* x) {
+    const unsigned a = __half_as_ushort(__float2half_rn(x[0])), b = __half_as_ushort(__float2half_rn(x[1]));
+    const unsigned c = __half_as_ushort(__float2half_rn(x[2])), d = __half_as_ushort(__float2half_rn(x[3]));
+    return make_uint2(a | (b << 16), c | (d << 16));
+  }
+};
+
+// A thread's part of a tile.  `e` is its first element; `full`: its four
+// elements are in the tensor and every array has them on a vector boundary.
+template <typename GT>
+struct AdamPart {
+  typename Four<GT>::Raw g;
+  float4 w, m, v;
+  int64_t first;
+  int64_t e;
+  int si;
+  float decay;
+  bool full;
+};
+
+template <typename GT, typename P>
+__device__ __forceinline__ void place_part(const P& p, int t, int si, AdamPart<GT>& a) {
+  const AdamSeg& sg = p.seg[si];
+  a.si = si;
+  // tiles are cut `shift` elements below the first one, where every array
+  // that can be read in vectors has a vector boundary
+  a.first = (int64_t)(t - sg.tile0) * kAdamTile32 - max(sg.shift, 0);
+  a.e = a.first + threadIdx.x * 4;
+  a.full = sg.shift >= 0 && a.e >= 0 && a.e + 4 <= sg.len;
+}
+template <typename GT, typename P>
+__device__ __forceinline__ void load_state(const P& p, AdamPart<GT>& a) {
+  if (!a.full) return;
+  const AdamSeg& sg = p.seg[a.si];
+  a.w = __ldcs(reinterpret_cast<const float4*>(sg.weight + a.e));
+  a.m = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(sg.m) + a.e));
+  a.v = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(sg.v) + a.e));
+}
+template <typename GT, typename P>
+__device__ __forceinline__ void load_grad(const P& p, AdamPart<GT>& a) {
+  if (a.full)
+    a.g = __ldcs(reinterpret_cast<const typename Four<GT>::Raw*>(static_cast<const GT*>(p.seg[a.si].grad) + a.e));
+}
+
 template <typename PT, typename GT, int CAP>
-__global__ void __launch_bounds__(kThreads) tensors_adamw(const __grid_constant__ AdamParamsT<CAP> p) {
+__global__ void __launch_bounds__(kThreads, 4) tensors_adamw(const __grid_constant__ AdamParamsT<CAP> p) {
+  int t = blockIdx.x;
+  const bool work = t < p.n_tiles;
+  AdamPart<GT> cur;
+  if (work) {
+    place_part<GT>(p, t, find_seg(p, t), cur);
+    if (p.early) load_state<GT>(p, cur);  // the launch before writes none of it
+  }
   wait_for_prior_grids();
-  if (p.found_inf && *p.found_inf) return;
+  if (!work || (p.found_inf && *p.found_inf)) return;
   AdamScalars s;
   s.c = p.coef ? *p.coef : 1.f;
   s.step_size = p.dev ? p.dev->step_size : p.step_size;
   s.bc2_sqrt = p.dev ? p.dev->bc2_sqrt : p.bc2_sqrt;
-  int si = -1;
-  for (int t = blockIdx.x; t < p.n_tiles; t += gridDim.x) {
-    const int k = si < 0 ? find_seg(p, t) : next_seg(p, si, t);
-    const AdamSeg& sg = p.seg[k];
-    if (k != si) s.decay = decay_of_seg(p, sg);
-    si = k;
-    const int64_t off = (int64_t)(t - sg.tile0) * kAdamTile;
-    const int n = (int)min((int64_t)kAdamTile, sg.len - off);
-    const GT* g = static_cast<const GT*>(sg.grad) + off;
-    float* w = sg.weight + off;
-    float* m = static_cast<float*>(sg.m) + off;
-    float* v = static_cast<float*>(sg.v) + off;
-    for (int e = threadIdx.x; e < n; e += kThreads) {
-      float ww = w[e], mm = m[e], vv = v[e];
-      adamw_element(widen<GT>(g[e]), p, s, ww, mm, vv);
-      w[e] = ww;
-      m[e] = mm;
-      v[e] = vv;
-      if constexpr (sizeof(PT) == 2) static_cast<PT*>(sg.param)[off + e] = narrow<PT>(ww);
+  load_grad<GT>(p, cur);
+  if (!p.early) load_state<GT>(p, cur);
+  cur.decay = decay_of_seg(p, p.seg[cur.si]);
+  for (;;) {
+    AdamPart<GT> nxt;
+    const int tn = t + (int)gridDim.x;
+    const bool more = tn < p.n_tiles;
+    if (more) {
+      place_part<GT>(p, tn, next_seg(p, cur.si, tn), nxt);
+      load_grad<GT>(p, nxt);
+      load_state<GT>(p, nxt);
+      nxt.decay = nxt.si == cur.si ? cur.decay : decay_of_seg(p, p.seg[nxt.si]);
     }
+    const AdamSeg& sg = p.seg[cur.si];
+    s.decay = cur.decay;
+    float* const wp = sg.weight;
+    float* const mp = static_cast<float*>(sg.m);
+    float* const vp = static_cast<float*>(sg.v);
+    if (cur.full) {
+      float g[4];
+      Four<GT>::widen4(cur.g, g);
+      float w[4] = {cur.w.x, cur.w.y, cur.w.z, cur.w.w};
+      float m[4] = {cur.m.x, cur.m.y, cur.m.z, cur.m.w};
+      float v[4] = {cur.v.x, cur.v.y, cur.v.z, cur.v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) adamw_element(g[j], p, s, w[j], m[j], v[j]);
+      __stcs(reinterpret_cast<float4*>(wp + cur.e), make_float4(w[0], w[1], w[2], w[3]));
+      __stcs(reinterpret_cast<float4*>(mp + cur.e), make_float4(m[0], m[1], m[2], m[3]));
+      __stcs(reinterpret_cast<float4*>(vp + cur.e), make_float4(v[0], v[1], v[2], v[3]));
+      if constexpr (sizeof(PT) == 2)
+        __stcs(reinterpret_cast<uint2*>(static_cast<PT*>(sg.param) + cur.e), Four<PT>::narrow4(w));
+    } else {
+      // a tensor's ragged ends (its own four elements), or a tensor whose
+      // arrays have no common vector boundary (consecutive threads take
+      // consecutive elements)
+      const bool ends = sg.shift >= 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t e = ends ? cur.e + j : cur.first + j * kThreads + threadIdx.x;
+        if (e < 0 || e >= sg.len) continue;
+        float w = wp[e], m = mp[e], v = vp[e];
+        adamw_element(widen<GT>(static_cast<const GT*>(sg.grad)[e]), p, s, w, m, v);
+        wp[e] = w;
+        mp[e] = m;
+        vp[e] = v;
+        if constexpr (sizeof(PT) == 2) static_cast<PT*>(sg.param)[e] = narrow<PT>(w);
+      }
+    }
+    if (!more) break;
+    cur = nxt;
+    t = tn;
   }
 }
 
