@@ -95,7 +95,7 @@ struct MomentSeg {
   uint8_t* vs;
   int64_t len;
   int32_t tile0;
-  int32_t reserved;
+  int32_t vec;  // 1: every array has the first element on a vector boundary
 };
 constexpr int kMomentCap = 500, kMomentSmallCap = 60;
 template <int CAP>
