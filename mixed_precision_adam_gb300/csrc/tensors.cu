@@ -155,10 +155,10 @@ int32_t common_shift(const AdamSeg& g, int32_t pd, int32_t gd) {
 }
 
 // Whether a tensor with 8-bit moments has its first element on a vector
-// boundary of every array (16 bytes, 8 for codes): the blocks start there.
-bool block_vectors(const AdamSeg& g) {
-  return aligned_to(g.weight, 16) && aligned_to(g.m, 8) && aligned_to(g.v, 8) && aligned_to(g.grad, 16) &&
-         aligned_to(g.param, 16);
+// boundary of every array (eight elements): the blocks start there.
+bool block_vectors(const AdamSeg& g, int32_t pd, int32_t gd) {
+  return aligned_to(g.weight, 32) && aligned_to(g.m, 8) && aligned_to(g.v, 8) &&
+         aligned_to(g.grad, 8 * dtype_bytes(gd)) && aligned_to(g.param, 8 * dtype_bytes(pd));
 }
 
 struct AdamJob {
@@ -228,7 +228,7 @@ int run_adamw(const dopt_tensor* ts, int32_t n, const AdamJob& j, cudaStream_t s
             g.shift = common_shift(g, pd, gd);
             p.n_tiles += (int32_t)tiles_of(t.numel + std::max(g.shift, 0), kAdamTile32);
           } else {
-            g.shift = block_vectors(g) ? 0 : -1;
+            g.shift = block_vectors(g, pd, gd) ? 0 : -1;
             p.n_tiles += (int32_t)tiles_of(t.numel, kAdamTile);
           }
         }
@@ -277,8 +277,9 @@ int run_moments(const dopt_moment_tensor* ts, int32_t n, bool pack, cudaStream_t
       if (t.numel == 0 || t.values_dtype != dt || (!t.exp_avg && !t.exp_avg_sq)) continue;
       if (p.n_seg == kMomentCap)
         if (int st = flush()) return st;
-      const bool vec = (!t.exp_avg || (aligned_to(t.exp_avg, 16) && aligned_to(t.exp_avg_codes, 8))) &&
-                       (!t.exp_avg_sq || (aligned_to(t.exp_avg_sq, 16) && aligned_to(t.exp_avg_sq_codes, 8)));
+      const size_t elem = dtype_bytes(t.values_dtype);
+      const bool vec = (!t.exp_avg || (aligned_to(t.exp_avg, 8 * elem) && aligned_to(t.exp_avg_codes, 8))) &&
+                       (!t.exp_avg_sq || (aligned_to(t.exp_avg_sq, 8 * elem) && aligned_to(t.exp_avg_sq_codes, 8)));
       p.seg[p.n_seg++] = MomentSeg{t.exp_avg,          t.exp_avg_sq,    t.exp_avg_codes,    t.exp_avg_sq_codes,
                                    t.exp_avg_scale,    t.exp_avg_sq_scale, t.numel,         p.n_tiles, vec ? 1 : 0};
       p.n_tiles += (int32_t)tiles_of(t.numel, kAdamTile);

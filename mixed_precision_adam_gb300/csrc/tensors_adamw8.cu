@@ -31,43 +31,50 @@ __device__ __forceinline__ uint32_t v_scale_of(uint32_t top) {
   const uint32_t e = exponent_of(top, 0x0FFFFFu);
   return e >= 255u ? 255u : (uint32_t)max((int)e - 31, 0);
 }
-// Eight consecutive elements of a type, as loaded and stored at once.
+// Eight consecutive fp32 elements in one 32-byte access (streaming: read
+// once, written once).
+__device__ __forceinline__ void load8(const float* p, float2* x) {
+  asm volatile("ld.global.cs.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(x[0].x), "=f"(x[0].y), "=f"(x[1].x), "=f"(x[1].y), "=f"(x[2].x), "=f"(x[2].y), "=f"(x[3].x), "=f"(x[3].y)
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void store8(float* p, const float2* x) {
+  asm volatile("st.global.cs.v8.f32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(x[0].x), "f"(x[0].y), "f"(x[1].x),
+               "f"(x[1].y), "f"(x[2].x), "f"(x[2].y), "f"(x[3].x), "f"(x[3].y), "l"(p)
+               : "memory");
+}
+
+// Eight consecutive elements of a type as four pairs: what a load leaves in
+// registers until it is widened, and the store.
 template <typename T>
 struct Eight;
 template <>
 struct Eight<float> {
   struct Raw {
-    float4 a, b;
+    float2 x[4];
   };
-  static __device__ __forceinline__ Raw load(const float* p) {
-    return Raw{__ldcs(reinterpret_cast<const float4*>(p)), __ldcs(reinterpret_cast<const float4*>(p) + 1)};
+  static __device__ __forceinline__ void load(const float* p, Raw& r) { load8(p, r.x); }
+  static __device__ __forceinline__ void widen8(const Raw& r, float2* x) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = r.x[k];
   }
-  static __device__ __forceinline__ void widen8(const Raw& r, float* x) {
-    x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
-    x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
-  }
-  static __device__ __forceinline__ void store(float* p, const float* x) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
-    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
-  }
+  static __device__ __forceinline__ void store(float* p, const float2* x) { store8(p, x); }
 };
 template <>
 struct Eight<__nv_bfloat16> {
   using Raw = uint4;
-  static __device__ __forceinline__ Raw load(const __nv_bfloat16* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
-  static __device__ __forceinline__ void widen8(const Raw& r, float* x) {
+  static __device__ __forceinline__ void load(const __nv_bfloat16* p, Raw& r) { r = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  static __device__ __forceinline__ void widen8(const Raw& r, float2* x) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x[2 * k] = __uint_as_float(w[k] << 16);
-      x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-    }
+    for (int k = 0; k < 4; ++k) x[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* x) {
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float2* x) {
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+      const __nv_bfloat162 h = __float22bfloat162_rn(x[k]);
       w[k] = *reinterpret_cast<const uint32_t*>(&h);
     }
     __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
@@ -76,86 +83,132 @@ struct Eight<__nv_bfloat16> {
 template <>
 struct Eight<__half> {
   using Raw = uint4;
-  static __device__ __forceinline__ Raw load(const __half* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
-  static __device__ __forceinline__ void widen8(const Raw& r, float* x) {
+  static __device__ __forceinline__ void load(const __half* p, Raw& r) { r = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  static __device__ __forceinline__ void widen8(const Raw& r, float2* x) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-      x[2 * k] = f.x;
-      x[2 * k + 1] = f.y;
-    }
+    for (int k = 0; k < 4; ++k) x[k] = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
   }
-  static __device__ __forceinline__ void store(__half* p, const float* x) {
+  static __device__ __forceinline__ void store(__half* p, const float2* x) {
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const __half2 h = __floats2half2_rn(x[2 * k], x[2 * k + 1]);
+      const __half2 h = __float22half2_rn(x[k]);
       w[k] = *reinterpret_cast<const uint32_t*>(&h);
     }
     __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
   }
 };
 
-// Two e4m3 codes as floats, and back.
-__device__ __forceinline__ float2 widen_e4m3x2(uint32_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
-  return __half22float2(__half2(h));
-}
-__device__ __forceinline__ uint32_t narrow_e4m3x2(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
+// Element j of four pairs.
+__device__ __forceinline__ float& elem(float2* x, int j) { return j & 1 ? x[j / 2].y : x[j / 2].x; }
 
-// A warp's block of moments: eight codes per lane in two words each.
-__device__ __forceinline__ void unpack_block(uint2 mc, uint2 vc, uint32_t ms, uint32_t vs, float* m, float* v) {
-  const float unit = m_unit(ms);
-  const uint32_t base = vs << 23;
+// exp_avg codes (two words, eight codes) as the numbers they are before
+// their block's unit.
+__device__ __forceinline__ void widen_m(uint2 mc, float2* m) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t mw = k < 2 ? mc.x : mc.y;
-    const float2 f = widen_e4m3x2((k & 1) ? mw >> 16 : mw & 0xFFFFu);
-    m[2 * k] = __fmul_rn(f.x, unit);
-    m[2 * k + 1] = __fmul_rn(f.y, unit);
+    const uint32_t w = k < 2 ? mc.x : mc.y;
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((k & 1) ? w >> 16 : w & 0xFFFFu), __NV_E4M3);
+    m[k] = __half22float2(__half2(h));
   }
+}
+// exp_avg_sq codes as values: base + the code at bits 20..27, and 0 for
+// code 0 (checked for all eight at once; rare but for blocks never touched).
+__device__ __forceinline__ void widen_v(uint2 vc, uint32_t s, float2* v) {
+  const uint32_t base = s << 23;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t w = j < 4 ? vc.x : vc.y;
-    const int at = 8 * (j & 3);  // the code's bits, moved to 20..27
-    const uint32_t c = (at <= 20 ? w << (20 - at) : w >> (at - 20)) & 0x0FF00000u;
-    v[j] = __uint_as_float(min(c, 1u) * base + c);  // code 0 is zero
-  }
-  if (vs == 255u) {
+  for (int j = 0; j < 8; ++j)
+    elem(v, j) = __uint_as_float(__byte_perm(j < 4 ? vc.x : vc.y, 0, 0x4440 + (j & 3)) * 0x100000u + base);
+  const uint32_t zero = ((vc.x - 0x01010101u) & ~vc.x) | ((vc.y - 0x01010101u) & ~vc.y);
+  if ((zero & 0x80808080u) || s == 255u) {  // a byte is 0 (or, harmlessly, 1 above a 0)
+    const float none = s == 255u ? __uint_as_float(0x7FC00000u) : 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(0x7FC00000u);
+    for (int j = 0; j < 8; ++j)
+      if (s == 255u || !(((j < 4 ? vc.x : vc.y) >> (8 * (j & 3))) & 0xFFu)) elem(v, j) = none;
   }
 }
 
-// The largest of a lane's eight |m| or v over the warp, as fp32 bits (the
-// order of non-negative floats, NaN above all).
-__device__ __forceinline__ uint32_t block_top(const float* x) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-  return __reduce_max_sync(0xFFFFFFFFu, top);
+// Largest of three magnitudes, NaN above all.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// The largest magnitude of the warp's elements, eight per lane, as fp32 bits
+// (their order is that of the magnitudes, NaN above all).
+__device__ __forceinline__ uint32_t block_top(const float2* x) {
+  float t = max3_abs(x[0].x, x[0].y, x[1].x);
+  t = max3_abs(t, x[1].y, x[2].x);
+  t = max3_abs(t, x[2].y, x[3].x);
+  t = max3_abs(t, x[3].y, x[3].y);
+  return __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(t));
 }
 
-__device__ __forceinline__ uint2 pack_m_block(const float* m, uint32_t s) {
+__device__ __forceinline__ uint2 narrow_m(const float2* m, uint32_t s) {
   const float up = __uint_as_float((254u - s) << 23);
+  const float2 up2 = make_float2(up, up);
   uint32_t h[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) h[k] = narrow_e4m3x2(__fmul_rn(m[2 * k], up), __fmul_rn(m[2 * k + 1], up));
-  return s == 255u ? make_uint2(0u, 0u) : make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  for (int k = 0; k < 4; ++k) h[k] = __nv_cvt_float2_to_fp8x2(__fmul2_rn(m[k], up2), __NV_SATFINITE, __NV_E4M3);
+  return s == 255u ? make_uint2(0u, 0u) : make_uint2(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
 }
-// r20: the elements' rounding addends.  The scale keeps codes at most 255.
-__device__ __forceinline__ uint2 pack_v_block(const float* v, uint32_t s, const uint32_t* r20) {
-  uint32_t w[2] = {0u, 0u};
+// r16: the elements' rounding bits, two per word (0x8000: nearest).  Two codes
+// at a time in the halves of a word: the fp32 patterns' upper halves, held
+// at the smallest code or above, less the base, shifted down to bytes.  The
+// scale keeps codes at most 255.
+__device__ __forceinline__ uint2 narrow_v(const float2* v, uint32_t s, const uint32_t* r16) {
+  const uint32_t base16 = s * 0x00800080u, least16 = base16 + 0x00100010u;
+  uint32_t h[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t b = __float_as_uint(v[j]);
-    const int c = max((int)(b + r20[j] - (s << 23)) >> 20, (int)min(b, 1u));  // at least 1 but for zero
-    w[j / 4] |= (uint32_t)c << (8 * (j & 3));
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t a = __float_as_uint(v[k].x) + ((r16[k] & 0xFFFFu) << 4);
+    const uint32_t b = __float_as_uint(v[k].y) + ((r16[k] >> 16) << 4);
+    h[k] = (__vmaxu2(__byte_perm(a, b, 0x7632), least16) - base16) >> 4;  // codes in bytes 0 and 2
   }
-  return s == 255u ? make_uint2(0u, 0u) : make_uint2(w[0], w[1]);
+  uint2 c = make_uint2(__byte_perm(h[0], h[1], 0x6420), __byte_perm(h[2], h[3], 0x6420));
+  const float least = fminf(fminf(fminf(v[0].x, v[0].y), fminf(v[1].x, v[1].y)),
+                            fminf(fminf(v[2].x, v[2].y), fminf(v[3].x, v[3].y)));
+  if (least == 0.f) {  // zeros have code 0
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if ((j & 1 ? v[j / 2].y : v[j / 2].x) == 0.f) (j < 4 ? c.x : c.y) &= ~(0xFFu << (8 * (j & 3)));
+    }
+  }
+  return s == 255u ? make_uint2(0u, 0u) : c;
+}
+
+// AdamW on eight elements.  The moments' arithmetic rounds each operation
+// once in fp32, two elements per instruction.  The weight's update takes
+// the hardware's approximate root and reciprocal (each within 2^-22 of the
+// exact; the update itself is a small part of the weight): correctly
+// rounded ones cost half of the kernel's instructions, which then bound it.
+struct Adam8 {
+  float2 inv_scale, c, decay, b1, b2, omb1, omb2, minus_size, inv_bc2, eps;
+};
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float root(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// m arrives without its block's unit, which b1 carries (a power of two:
+// the product is the same).
+__device__ __forceinline__ void adamw_pairs(const Adam8& a, float2 b1_unit, float2* g, float2* w, float2* m, float2* v) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 gk = __fmul2_rn(__fmul2_rn(g[k], a.inv_scale), a.c);
+    m[k] = __fadd2_rn(__fmul2_rn(b1_unit, m[k]), __fmul2_rn(a.omb1, gk));
+    v[k] = __fadd2_rn(__fmul2_rn(a.b2, v[k]), __fmul2_rn(__fmul2_rn(a.omb2, gk), gk));
+    const float2 denom = __ffma2_rn(make_float2(root(v[k].x), root(v[k].y)), a.inv_bc2, a.eps);
+    const float2 u = __fmul2_rn(m[k], make_float2(reciprocal(denom.x), reciprocal(denom.y)));
+    w[k] = __ffma2_rn(a.minus_size, u, __fmul2_rn(w[k], a.decay));
+  }
 }
 
 // A lane's part of a block.  `full`: its eight elements are consecutive, in
@@ -163,7 +216,7 @@ __device__ __forceinline__ uint2 pack_v_block(const float* v, uint32_t s, const 
 template <typename GT>
 struct Part8 {
   typename Eight<GT>::Raw g;
-  typename Eight<float>::Raw w;
+  float2 w[4];
   uint2 m, v;
   uint32_t ms, vs;
   int64_t block;  // the block's first element; < 0: none (past the tensor's end)
@@ -189,7 +242,7 @@ __device__ __forceinline__ void load_state(const P& p, Part8<GT>& a) {
   }
   if (a.full) {
     const int64_t e = a.block + (threadIdx.x % 32) * 8;
-    a.w = Eight<float>::load(sg.weight + e);
+    load8(sg.weight + e, a.w);
     a.m = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(sg.m) + e));
     a.v = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(sg.v) + e));
   }
@@ -197,13 +250,12 @@ __device__ __forceinline__ void load_state(const P& p, Part8<GT>& a) {
 template <typename GT, typename P>
 __device__ __forceinline__ void load_grad(const P& p, Part8<GT>& a) {
   if (a.full)
-    a.g = Eight<GT>::load(static_cast<const GT*>(p.seg[a.si].grad) + a.block + (threadIdx.x % 32) * 8);
+    Eight<GT>::load(static_cast<const GT*>(p.seg[a.si].grad) + a.block + (threadIdx.x % 32) * 8, a.g);
 }
 
 // Updates a lane's part (whole warps: the block's scales are reduced over it).
 template <typename PT, typename GT>
-__device__ __forceinline__ void step_part(const AdamHead& p, const AdamSeg& sg, const Part8<GT>& a,
-                                          const AdamScalars& s, uint32_t key) {
+__device__ __forceinline__ void step_part(const AdamSeg& sg, const Part8<GT>& a, const Adam8& ad, uint32_t key) {
   const int lane = threadIdx.x % 32;
   float* const wp = sg.weight + a.block;
   uint8_t* const mp = static_cast<uint8_t*>(sg.m) + a.block;
@@ -215,11 +267,11 @@ __device__ __forceinline__ void step_part(const AdamHead& p, const AdamSeg& sg, 
   const bool vec = sg.shift == 0;
   const int n = (int)min((int64_t)kMomentBlock, sg.len - a.block);
   const int first = vec ? lane * 8 : lane, stride = vec ? 1 : 32;
-  float g[8], w[8], m[8], v[8];
+  float2 g[4], w[4], m[4], v[4];
   uint2 mc, vc;
   if (a.full) {
     Eight<GT>::widen8(a.g, g);
-    Eight<float>::widen8(a.w, w);
+    Eight<float>::widen8(*reinterpret_cast<const Eight<float>::Raw*>(a.w), w);
     mc = a.m;
     vc = a.v;
   } else {
@@ -228,51 +280,48 @@ __device__ __forceinline__ void step_part(const AdamHead& p, const AdamSeg& sg, 
     for (int j = 0; j < 8; ++j) {
       const int e = first + j * stride;
       const bool in = e < n;
-      g[j] = in ? widen<GT>(gp[e]) : 0.f;
-      w[j] = in ? wp[e] : 0.f;
+      elem(g, j) = in ? widen<GT>(gp[e]) : 0.f;
+      elem(w, j) = in ? wp[e] : 0.f;
       mw[j / 4] |= (in ? (uint32_t)mp[e] : 0u) << (8 * (j & 3));
       vw[j / 4] |= (in ? (uint32_t)vp[e] : 0u) << (8 * (j & 3));
     }
     mc = make_uint2(mw[0], mw[1]);
     vc = make_uint2(vw[0], vw[1]);
   }
-  unpack_block(mc, vc, a.ms, a.vs, m, v);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) adamw_element(g[j], p, s, w[j], m[j], v[j]);
+  widen_m(mc, m);
+  widen_v(vc, a.vs, v);
+  adamw_pairs(ad, both(__fmul_rn(ad.b1.x, m_unit(a.ms))), g, w, m, v);
   if (a.full) {
-    Eight<float>::store(wp + first, w);
+    store8(wp + first, w);
     if constexpr (sizeof(PT) == 2) Eight<PT>::store(pp + first, w);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int e = first + j * stride;
       if (e < n) {
-        wp[e] = w[j];
-        if constexpr (sizeof(PT) == 2) pp[e] = narrow<PT>(w[j]);
+        wp[e] = elem(w, j);
+        if constexpr (sizeof(PT) == 2) pp[e] = narrow<PT>(elem(w, j));
       } else {
-        m[j] = v[j] = 0.f;  // past the end: no part in the scales (NaN blocks)
+        elem(m, j) = elem(v, j) = 0.f;  // past the end: no part in the scales (NaN blocks)
       }
     }
   }
   const uint32_t ms = m_scale_of(block_top(m)), vs = v_scale_of(block_top(v));
-  uint32_t r20[8];
+  uint32_t r16[4];
   const uint32_t at = (uint32_t)((uint64_t)a.block >> 1);
   if (vec) {
+    const uint32_t x = (at + lane * 4) * kHashPair + key;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t h = hash_pair((at + lane * 4 + k) * kHashPair + key);
-      r20[2 * k] = (h << 4) & 0xFFFF0u;
-      r20[2 * k + 1] = (h >> 12) & 0xFFFF0u;
-    }
+    for (int k = 0; k < 4; ++k) r16[k] = hash_pair(x + k * kHashPair);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t h = hash_pair((at + (lane >> 1) + j * 16) * kHashPair + key);
-      r20[j] = ((lane & 1) ? h >> 12 : h << 4) & 0xFFFF0u;
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t x = (at + (lane >> 1) + k * 32) * kHashPair + key;
+      r16[k] = __byte_perm(hash_pair(x), hash_pair(x + 16 * kHashPair), (lane & 1) ? 0x7632 : 0x5410);
     }
   }
-  mc = pack_m_block(m, ms);
-  vc = pack_v_block(v, vs, r20);
+  mc = narrow_m(m, ms);
+  vc = narrow_v(v, vs, r16);
   if (lane == 0) {
     sg.m_scale[a.block / kMomentBlock] = (uint8_t)ms;
     sg.v_scale[a.block / kMomentBlock] = (uint8_t)vs;
@@ -303,10 +352,16 @@ __global__ void __launch_bounds__(kThreads, 3) tensors_adamw8(const __grid_const
   }
   wait_for_prior_grids();
   if (!work || (p.found_inf && *p.found_inf)) return;
-  AdamScalars s;
-  s.c = p.coef ? *p.coef : 1.f;
-  s.step_size = p.dev ? p.dev->step_size : p.step_size;
-  s.bc2_sqrt = p.dev ? p.dev->bc2_sqrt : p.bc2_sqrt;
+  Adam8 ad;
+  ad.inv_scale = both(p.inv_scale);
+  ad.c = both(p.coef ? *p.coef : 1.f);
+  ad.b1 = both(p.b1);
+  ad.b2 = both(p.b2);
+  ad.omb1 = both(p.omb1);
+  ad.omb2 = both(p.omb2);
+  ad.minus_size = both(p.dev ? -p.dev->step_size : -p.step_size);
+  ad.inv_bc2 = both(__fdiv_rn(1.f, p.dev ? p.dev->bc2_sqrt : p.bc2_sqrt));
+  ad.eps = both(fmaxf(p.eps, 0x1p-126f));  // the reciprocal takes subnormals for 0
   const uint32_t key = p.key + (p.d_step ? (uint32_t)*p.d_step * kHashStep : 0u);
   load_grad<GT>(p, cur);
   if (!p.early) load_state<GT>(p, cur);
@@ -321,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, 3) tensors_adamw8(const __grid_const
       load_state<GT>(p, nxt);
       nxt.decay = nxt.si == cur.si ? cur.decay : decay_of_seg(p, p.seg[nxt.si]);
     }
-    s.decay = cur.decay;
-    if (cur.block >= 0) step_part<PT, GT>(p, p.seg[cur.si], cur, s, key + p.seg[cur.si].key);
+    ad.decay = both(cur.decay);
+    if (cur.block >= 0) step_part<PT, GT>(p.seg[cur.si], cur, ad, key + p.seg[cur.si].key);
     if (!more) break;
     cur = nxt;
     t = tn;
@@ -352,20 +407,22 @@ int launch_tensors_adamw8(int32_t param_dtype, int32_t grad_dtype, const AdamPar
 // where every array has its first element on a vector boundary, else 32
 // apart.  A lane's part of a moment's values and codes:
 template <typename VT>
-__device__ __forceinline__ void load_values(const VT* x, bool vec, int lane, int n, float* out) {
+__device__ __forceinline__ void load_values(const VT* x, bool vec, int lane, int n, float2* out) {
   if (vec && lane * 8 + 8 <= n) {
-    Eight<VT>::widen8(Eight<VT>::load(x + lane * 8), out);
+    typename Eight<VT>::Raw r;
+    Eight<VT>::load(x + lane * 8, r);
+    Eight<VT>::widen8(r, out);
     return;
   }
   const int first = vec ? lane * 8 : lane, stride = vec ? 1 : 32;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int e = first + j * stride;
-    out[j] = e < n ? widen<VT>(x[e]) : 0.f;
+    elem(out, j) = e < n ? widen<VT>(x[e]) : 0.f;
   }
 }
 template <typename VT>
-__device__ __forceinline__ void store_values(VT* x, bool vec, int lane, int n, const float* in) {
+__device__ __forceinline__ void store_values(VT* x, bool vec, int lane, int n, float2* in) {
   if (vec && lane * 8 + 8 <= n) {
     Eight<VT>::store(x + lane * 8, in);
     return;
@@ -374,7 +431,7 @@ __device__ __forceinline__ void store_values(VT* x, bool vec, int lane, int n, c
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int e = first + j * stride;
-    if (e < n) x[e] = narrow<VT>(in[j]);
+    if (e < n) x[e] = narrow<VT>(elem(in, j));
   }
 }
 __device__ __forceinline__ uint2 load_codes(const uint8_t* x, bool vec, int lane, int n) {
@@ -418,25 +475,25 @@ template <typename VT, int CAP>
 __global__ void __launch_bounds__(kThreads) state8_pack(const __grid_constant__ MomentParamsT<CAP> p) {
   const int lane = threadIdx.x % 32;
   each_block(p, [&](const MomentSeg& sg, int64_t off, int n, bool vec) {
-    float m[8], v[8];
+    float2 m[4], v[4];
     if (sg.m) load_values(static_cast<const VT*>(sg.m) + off, vec, lane, n, m);
     if (sg.v) load_values(static_cast<const VT*>(sg.v) + off, vec, lane, n, v);
     if (sg.m) {
       const uint32_t s = m_scale_of(block_top(m));
       if (lane == 0) sg.ms[off / kMomentBlock] = (uint8_t)s;
-      store_codes(sg.mc + off, vec, lane, n, pack_m_block(m, s));
+      store_codes(sg.mc + off, vec, lane, n, narrow_m(m, s));
     }
     if (sg.v) {
-      uint32_t nearest[8];
+      const uint32_t nearest[4] = {0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         // -0 is 0; what is below 0 is not a second moment: NaN
-        v[j] = v[j] < 0.f ? __uint_as_float(0x7FC00000u) : __fadd_rn(v[j], 0.f);
-        nearest[j] = 0x80000u;
+        float& x = elem(v, j);
+        x = x < 0.f ? __uint_as_float(0x7FC00000u) : __fadd_rn(x, 0.f);
       }
       const uint32_t s = v_scale_of(block_top(v));
       if (lane == 0) sg.vs[off / kMomentBlock] = (uint8_t)s;
-      store_codes(sg.vc + off, vec, lane, n, pack_v_block(v, s, nearest));
+      store_codes(sg.vc + off, vec, lane, n, narrow_v(v, s, nearest));
     }
   });
 }
@@ -455,8 +512,11 @@ __global__ void __launch_bounds__(kThreads) state8_unpack(const __grid_constant_
       vc = load_codes(sg.vc + off, vec, lane, n);
       vs = sg.vs[off / kMomentBlock];
     }
-    float m[8], v[8];
-    unpack_block(mc, vc, ms, vs, m, v);
+    float2 m[4], v[4];
+    widen_m(mc, m);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = __fmul2_rn(m[k], both(m_unit(ms)));
+    widen_v(vc, vs, v);
     if (sg.m) store_values(static_cast<VT*>(sg.m) + off, vec, lane, n, m);
     if (sg.v) store_values(static_cast<VT*>(sg.v) + off, vec, lane, n, v);
   });
