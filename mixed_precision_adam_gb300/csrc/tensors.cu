@@ -155,10 +155,10 @@ int32_t common_shift(const AdamSeg& g, int32_t pd, int32_t gd) {
 }
 
 // Whether a tensor with 8-bit moments has its first element on a vector
-// boundary of every array (eight elements): the blocks start there.
-bool block_vectors(const AdamSeg& g, int32_t pd, int32_t gd) {
-  return aligned_to(g.weight, 32) && aligned_to(g.m, 8) && aligned_to(g.v, 8) &&
-         aligned_to(g.grad, 8 * dtype_bytes(gd)) && aligned_to(g.param, 8 * dtype_bytes(pd));
+// boundary of every array (16 bytes, 32 for the weights): the blocks start there.
+bool block_vectors(const AdamSeg& g, int32_t pd) {
+  return aligned_to(g.weight, 32) && aligned_to(g.m, 16) && aligned_to(g.v, 16) &&
+         aligned_to(g.grad, 16) && aligned_to(g.param, 8 * dtype_bytes(pd));
 }
 
 struct AdamJob {
@@ -228,7 +228,7 @@ int run_adamw(const dopt_tensor* ts, int32_t n, const AdamJob& j, cudaStream_t s
             g.shift = common_shift(g, pd, gd);
             p.n_tiles += (int32_t)tiles_of(t.numel + std::max(g.shift, 0), kAdamTile32);
           } else {
-            g.shift = block_vectors(g, pd, gd) ? 0 : -1;
+            g.shift = block_vectors(g, pd) ? 0 : -1;
             p.n_tiles += (int32_t)tiles_of(t.numel, kAdamTile);
           }
         }

@@ -180,9 +180,9 @@ __device__ __forceinline__ float decay_of_seg(const AdamHead& p, const AdamSeg& 
 // for that grid before it reads or writes anything it may share with it.
 template <typename K, typename P>
 int launch_table(K kern, const P& params, int n_tiles, cudaStream_t s, const char* what, int* grid_out = nullptr,
-                 bool programmatic = false) {
+                 bool programmatic = false, size_t smem = 0) {
   int grid = 0;
-  int st = grid_for(kern, n_tiles, &grid);
+  int st = grid_for(kern, n_tiles, &grid, smem);
   if (st) return st;
   if (grid_out) *grid_out = grid;
   cudaLaunchAttribute attr[1];
@@ -191,6 +191,7 @@ int launch_table(K kern, const P& params, int n_tiles, cudaStream_t s, const cha
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

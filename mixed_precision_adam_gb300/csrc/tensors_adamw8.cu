@@ -1,11 +1,29 @@
 // tensors_adamw8.cu -- AdamW over a list of tensors with the moments in 8
 // bits, and the moments' conversion between values and 8-bit codes.
+//
+// The update reads grad, weight and both codes of every element once and
+// writes weight, 16-bit param and both codes once: 16 bytes per element with
+// bf16 or fp16 grads and params, or with both in fp32 (and 4 scale bytes per
+// block).  Against 28 to 30 bytes with fp32 moments that leaves the same
+// arithmetic and the encoding half the time, about 90 issue slots per element
+// at the memory's rate, so both count: the moments' arithmetic runs two
+// elements per instruction, codes are made two at a time, and the inputs
+// come through a ring in shared memory.  A warp has a block of 256 elements
+// at a time, so a block's largest moments are one warp reduction each.
+// Measured on 1.35e9 bf16 elements: 3325 us, 6.48 TB/s (0.96 of the copy
+// bandwidth); fp32 params and grads 6.59 TB/s.
 #include <cuda_fp8.h>
 
 #include "tensors.cuh"
+#include "tma.cuh"
 
 namespace dopt {
 
+// Three CTAs per SM and three slots per warp: 16 to 20 KB per slot and CTA,
+// 144 to 180 KB of the SM's shared memory.  Four CTAs (64 registers) were 7 %
+// slower, two slots 5 %; four slots with fp32 grads leave room for two CTAs
+// only (21 % slower).
+constexpr int kRing8 = 3, kCtas8 = 3;
 static_assert(kMomentBlock == 256 && kAdamTile % kMomentBlock == 0, "one warp per block, 8 elements per lane");
 
 __device__ __forceinline__ uint32_t exponent_of(uint32_t bits, uint32_t up) { return (bits + up) >> 23; }
@@ -189,7 +207,7 @@ struct Adam8 {
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float root(float x) {
   float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float reciprocal(float x) {
@@ -211,96 +229,154 @@ __device__ __forceinline__ void adamw_pairs(const Adam8& a, float2 b1_unit, floa
   }
 }
 
-// A lane's part of a block.  `full`: its eight elements are consecutive, in
-// the tensor, and every array has them on a vector boundary.
-template <typename GT>
-struct Part8 {
-  typename Eight<GT>::Raw g;
-  float2 w[4];
-  uint2 m, v;
-  uint32_t ms, vs;
-  int64_t block;  // the block's first element; < 0: none (past the tensor's end)
-  int si;
-  float decay;
-  bool full;
+// Where a tile lies.  All of it is the same for the whole CTA, so that
+// addresses are a uniform base plus a thread's constant offset.
+struct Place8 {
+  int si;         // the tensor
+  int64_t first;  // the tile's first element
+  int n;          // elements of the tensor from there, at most kAdamTile
 };
-
-template <typename GT, typename P>
-__device__ __forceinline__ void place_part(const P& p, int t, int si, Part8<GT>& a) {
+template <typename P>
+__device__ __forceinline__ Place8 place_tile(const P& p, int t, int si) {
   const AdamSeg& sg = p.seg[si];
+  Place8 a;
   a.si = si;
-  a.block = (int64_t)(t - sg.tile0) * kAdamTile + (threadIdx.x / 32) * kMomentBlock;
-  if (a.block >= sg.len) a.block = -1;
-  a.full = sg.shift == 0 && a.block >= 0 && a.block + (threadIdx.x % 32) * 8 + 8 <= sg.len;
-}
-template <typename GT, typename P>
-__device__ __forceinline__ void load_state(const P& p, Part8<GT>& a) {
-  const AdamSeg& sg = p.seg[a.si];
-  if (a.block >= 0) {
-    a.ms = sg.m_scale[a.block / kMomentBlock];
-    a.vs = sg.v_scale[a.block / kMomentBlock];
-  }
-  if (a.full) {
-    const int64_t e = a.block + (threadIdx.x % 32) * 8;
-    load8(sg.weight + e, a.w);
-    a.m = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(sg.m) + e));
-    a.v = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(sg.v) + e));
-  }
-}
-template <typename GT, typename P>
-__device__ __forceinline__ void load_grad(const P& p, Part8<GT>& a) {
-  if (a.full)
-    Eight<GT>::load(static_cast<const GT*>(p.seg[a.si].grad) + a.block + (threadIdx.x % 32) * 8, a.g);
+  a.first = (int64_t)(t - sg.tile0) * kAdamTile;
+  a.n = (int)min((int64_t)kAdamTile, sg.len - a.first);
+  return a;
 }
 
-// Updates a lane's part (whole warps: the block's scales are reduced over it).
+template <typename T>
+__device__ __forceinline__ T* at_offset(T* base, uint32_t elems) {
+  return reinterpret_cast<T*>(reinterpret_cast<char*>(base) + elems * (uint32_t)sizeof(T));
+}
+template <typename T>
+__device__ __forceinline__ const T* at_offset(const T* base, uint32_t elems) {
+  return reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + elems * (uint32_t)sizeof(T));
+}
+
+// A whole block's inputs reach its warp through a ring of kRing8 slots of
+// shared memory per warp, filled by asynchronous copies kRing8 - 1 tiles
+// ahead: the loads in flight then depend neither on registers nor on the
+// number of resident warps, both of which the update's arithmetic limits.
+// Each lane copies 16-byte pieces (grads, weights, then exp_avg's and
+// exp_avg_sq's codes); each warp waits for its own copies only.
+template <typename GT>
+struct Ring8 {
+  static constexpr int kGrad = kMomentBlock * (int)sizeof(GT), kWeight = kMomentBlock * 4, kCodes = kMomentBlock;
+  static constexpr int kSlot = kGrad + kWeight + 2 * kCodes;
+  static constexpr size_t kBytes = (size_t)kRing8 * (kThreads / 32) * kSlot;
+};
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Where 16-byte piece c of an fp32 array lies in its part of a slot: pieces 2i
+// and 2i + 1 are lane i's, and the swap of every second group of eight lets
+// eight lanes read theirs from eight different bank groups.
+__device__ __forceinline__ uint32_t piece_at(uint32_t c) { return (c ^ ((c >> 3) & 1u)) * 16u; }
+
+// Whether a warp's block comes through the ring: it is whole, and the
+// tensor's arrays start on 16-byte boundaries.
+__device__ __forceinline__ bool through_ring(const AdamSeg& sg, const Place8& a) {
+  return sg.shift == 0 && (int)(threadIdx.x / 32 + 1) * kMomentBlock <= a.n;
+}
+template <typename GT, typename P>
+__device__ __forceinline__ void fetch_block(const P& p, const Place8& a, uint32_t slot, uint32_t& scales) {
+  const AdamSeg& sg = p.seg[a.si];
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if ((int)(warp * kMomentBlock) < a.n)
+    scales = *at_offset(sg.m_scale + a.first / kMomentBlock, warp) |
+             ((uint32_t)*at_offset(sg.v_scale + a.first / kMomentBlock, warp) << 8);
+  if (!through_ring(sg, a)) return;
+  const char* g = reinterpret_cast<const char*>(static_cast<const GT*>(sg.grad) + a.first);
+  const char* w = reinterpret_cast<const char*>(sg.weight + a.first);
+#pragma unroll
+  for (int k = 0; k < Ring8<GT>::kGrad / 512; ++k) {
+    const uint32_t c = k * 32 + lane;
+    copy16(slot + (sizeof(GT) == 4 ? piece_at(c) : c * 16u), g + warp * Ring8<GT>::kGrad + c * 16u);
+  }
+  slot += Ring8<GT>::kGrad;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t c = k * 32 + lane;
+    copy16(slot + piece_at(c), w + warp * Ring8<GT>::kWeight + c * 16u);
+  }
+  slot += Ring8<GT>::kWeight;
+  const uint8_t* codes = static_cast<const uint8_t*>(lane < 16 ? sg.m : sg.v) + a.first;
+  copy16(slot + lane * 16u, codes + warp * kMomentBlock + (lane & 15u) * 16u);
+}
+
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint2 shared8(uint32_t at) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(at) : "memory");
+  return r;
+}
+__device__ __forceinline__ void shared_floats(uint32_t at, uint32_t lane, float2* x) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint4 r = shared16(at + piece_at(2 * lane + k));
+    x[2 * k] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+    x[2 * k + 1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
+  }
+}
+// A lane's eight elements of its warp's slot.
+template <typename GT>
+__device__ __forceinline__ void from_ring(uint32_t slot, uint32_t lane, float2* g, float2* w, uint2& mc, uint2& vc) {
+  if constexpr (sizeof(GT) == 4)
+    shared_floats(slot, lane, g);
+  else
+    Eight<GT>::widen8(shared16(slot + lane * 16u), g);
+  shared_floats(slot + Ring8<GT>::kGrad, lane, w);
+  mc = shared8(slot + Ring8<GT>::kGrad + Ring8<GT>::kWeight + lane * 8u);
+  vc = shared8(slot + Ring8<GT>::kGrad + Ring8<GT>::kWeight + Ring8<GT>::kCodes + lane * 8u);
+}
+
+// Updates a warp's block.  key: the hash's argument for the tile's first
+// pair.  Element j of a lane: consecutive ones for a block through the
+// ring; 32 apart (consecutive lanes, consecutive elements) in a tensor's
+// ragged last block, or where the arrays have no common vector boundary.
 template <typename PT, typename GT>
-__device__ __forceinline__ void step_part(const AdamSeg& sg, const Part8<GT>& a, const Adam8& ad, uint32_t key) {
-  const int lane = threadIdx.x % 32;
-  float* const wp = sg.weight + a.block;
-  uint8_t* const mp = static_cast<uint8_t*>(sg.m) + a.block;
-  uint8_t* const vp = static_cast<uint8_t*>(sg.v) + a.block;
-  const GT* const gp = static_cast<const GT*>(sg.grad) + a.block;
-  PT* const pp = static_cast<PT*>(sg.param) + a.block;
-  // element j of the lane: consecutive where the tensor is read in vectors,
-  // 32 apart (consecutive lanes, consecutive elements) where it is not
-  const bool vec = sg.shift == 0;
-  const int n = (int)min((int64_t)kMomentBlock, sg.len - a.block);
-  const int first = vec ? lane * 8 : lane, stride = vec ? 1 : 32;
+__device__ __forceinline__ void step_block(const AdamSeg& sg, const Place8& a, uint32_t slot, uint32_t scales,
+                                           const Adam8& ad, uint32_t key) {
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const bool ring = through_ring(sg, a);
   float2 g[4], w[4], m[4], v[4];
   uint2 mc, vc;
-  if (a.full) {
-    Eight<GT>::widen8(a.g, g);
-    Eight<float>::widen8(*reinterpret_cast<const Eight<float>::Raw*>(a.w), w);
-    mc = a.m;
-    vc = a.v;
+  const uint32_t at = threadIdx.x * 8, loose = warp * kMomentBlock + lane;
+  if (ring) {
+    from_ring<GT>(slot, lane, g, w, mc, vc);
   } else {
     uint32_t mw[2] = {0u, 0u}, vw[2] = {0u, 0u};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int e = first + j * stride;
-      const bool in = e < n;
-      elem(g, j) = in ? widen<GT>(gp[e]) : 0.f;
-      elem(w, j) = in ? wp[e] : 0.f;
-      mw[j / 4] |= (in ? (uint32_t)mp[e] : 0u) << (8 * (j & 3));
-      vw[j / 4] |= (in ? (uint32_t)vp[e] : 0u) << (8 * (j & 3));
+      const uint32_t e = loose + j * 32;
+      const bool in = (int)e < a.n;
+      elem(g, j) = in ? widen<GT>(static_cast<const GT*>(sg.grad)[a.first + e]) : 0.f;
+      elem(w, j) = in ? sg.weight[a.first + e] : 0.f;
+      mw[j / 4] |= (in ? (uint32_t) static_cast<const uint8_t*>(sg.m)[a.first + e] : 0u) << (8 * (j & 3));
+      vw[j / 4] |= (in ? (uint32_t) static_cast<const uint8_t*>(sg.v)[a.first + e] : 0u) << (8 * (j & 3));
     }
     mc = make_uint2(mw[0], mw[1]);
     vc = make_uint2(vw[0], vw[1]);
   }
   widen_m(mc, m);
-  widen_v(vc, a.vs, v);
-  adamw_pairs(ad, both(__fmul_rn(ad.b1.x, m_unit(a.ms))), g, w, m, v);
-  if (a.full) {
-    store8(wp + first, w);
-    if constexpr (sizeof(PT) == 2) Eight<PT>::store(pp + first, w);
+  widen_v(vc, scales >> 8, v);
+  adamw_pairs(ad, both(__fmul_rn(ad.b1.x, m_unit(scales & 0xFFu))), g, w, m, v);
+  if (ring) {
+    store8(at_offset(sg.weight + a.first, at), w);
+    if constexpr (sizeof(PT) == 2) Eight<PT>::store(at_offset(static_cast<PT*>(sg.param) + a.first, at), w);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int e = first + j * stride;
-      if (e < n) {
-        wp[e] = elem(w, j);
-        if constexpr (sizeof(PT) == 2) pp[e] = narrow<PT>(elem(w, j));
+      const uint32_t e = loose + j * 32;
+      if ((int)e < a.n) {
+        sg.weight[a.first + e] = elem(w, j);
+        if constexpr (sizeof(PT) == 2) static_cast<PT*>(sg.param)[a.first + e] = narrow<PT>(elem(w, j));
       } else {
         elem(m, j) = elem(v, j) = 0.f;  // past the end: no part in the scales (NaN blocks)
       }
@@ -308,50 +384,67 @@ __device__ __forceinline__ void step_part(const AdamSeg& sg, const Part8<GT>& a,
   }
   const uint32_t ms = m_scale_of(block_top(m)), vs = v_scale_of(block_top(v));
   uint32_t r16[4];
-  const uint32_t at = (uint32_t)((uint64_t)a.block >> 1);
-  if (vec) {
-    const uint32_t x = (at + lane * 4) * kHashPair + key;
+  if (ring) {
+    const uint32_t y = key + (at >> 1) * kHashPair;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) r16[k] = hash_pair(x + k * kHashPair);
+    for (int k = 0; k < 4; ++k) r16[k] = hash_pair(y + k * kHashPair);
   } else {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint32_t x = (at + (lane >> 1) + k * 32) * kHashPair + key;
-      r16[k] = __byte_perm(hash_pair(x), hash_pair(x + 16 * kHashPair), (lane & 1) ? 0x7632 : 0x5410);
+      const uint32_t y = key + (warp * (kMomentBlock / 2) + (lane >> 1) + k * 32) * kHashPair;
+      r16[k] = __byte_perm(hash_pair(y), hash_pair(y + 16 * kHashPair), (lane & 1) ? 0x7632 : 0x5410);
     }
   }
   mc = narrow_m(m, ms);
   vc = narrow_v(v, vs, r16);
   if (lane == 0) {
-    sg.m_scale[a.block / kMomentBlock] = (uint8_t)ms;
-    sg.v_scale[a.block / kMomentBlock] = (uint8_t)vs;
+    *at_offset(sg.m_scale + a.first / kMomentBlock, warp) = (uint8_t)ms;
+    *at_offset(sg.v_scale + a.first / kMomentBlock, warp) = (uint8_t)vs;
   }
-  if (a.full) {
-    __stcs(reinterpret_cast<uint2*>(mp + first), mc);
-    __stcs(reinterpret_cast<uint2*>(vp + first), vc);
+  if (ring) {
+    __stcs(reinterpret_cast<uint2*>(at_offset(static_cast<uint8_t*>(sg.m) + a.first, at)), mc);
+    __stcs(reinterpret_cast<uint2*>(at_offset(static_cast<uint8_t*>(sg.v) + a.first, at)), vc);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int e = first + j * stride;
-      if (e < n) {
-        mp[e] = (uint8_t)((j < 4 ? mc.x : mc.y) >> (8 * (j & 3)));
-        vp[e] = (uint8_t)((j < 4 ? vc.x : vc.y) >> (8 * (j & 3)));
+      const uint32_t e = loose + j * 32;
+      if ((int)e < a.n) {
+        static_cast<uint8_t*>(sg.m)[a.first + e] = (uint8_t)((j < 4 ? mc.x : mc.y) >> (8 * (j & 3)));
+        static_cast<uint8_t*>(sg.v)[a.first + e] = (uint8_t)((j < 4 ? vc.x : vc.y) >> (8 * (j & 3)));
       }
     }
   }
 }
 
 template <typename PT, typename GT, int CAP>
-__global__ void __launch_bounds__(kThreads, 3) tensors_adamw8(const __grid_constant__ AdamParamsT<CAP> p) {
+__global__ void __launch_bounds__(kThreads, kCtas8) tensors_adamw8(const __grid_constant__ AdamParamsT<CAP> p) {
+  extern __shared__ uint4 ring[];
+  uint32_t slot0;
+  asm("{.reg .u64 t; cvta.to.shared.u64 t, %1; cvt.u32.u64 %0, t;}" : "=r"(slot0) : "l"(ring));
+  slot0 += threadIdx.x / 32 * (kRing8 * Ring8<GT>::kSlot);
   int t = blockIdx.x;
-  const bool work = t < p.n_tiles;
-  Part8<GT> cur;
-  if (work) {
-    place_part<GT>(p, t, find_seg(p, t), cur);
-    if (p.early) load_state<GT>(p, cur);  // the launch before writes none of it
+  Place8 cur = {}, ahead;
+  uint32_t scales[kRing8];  // of the tiles in flight, this one's first
+  if (!p.early) wait_for_prior_grids();
+  // the first kRing8 - 1 tiles; the launch before this one, when it is of
+  // the same call, writes none of what they read
+  if (t < p.n_tiles) cur = place_tile(p, t, find_seg(p, t));
+  ahead = cur;
+  int ta = t;
+#pragma unroll
+  for (int k = 0; k < kRing8 - 1; ++k) {
+    if (ta < p.n_tiles) {
+      if (k) ahead = place_tile(p, ta, next_seg(p, ahead.si, ta));
+      fetch_block<GT>(p, ahead, slot0 + k * Ring8<GT>::kSlot, scales[k]);
+      ta += gridDim.x;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  wait_for_prior_grids();
-  if (!work || (p.found_inf && *p.found_inf)) return;
+  if (p.early) wait_for_prior_grids();
+  if (t >= p.n_tiles || (p.found_inf && *p.found_inf)) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
   Adam8 ad;
   ad.inv_scale = both(p.inv_scale);
   ad.c = both(p.coef ? *p.coef : 1.f);
@@ -362,34 +455,47 @@ __global__ void __launch_bounds__(kThreads, 3) tensors_adamw8(const __grid_const
   ad.minus_size = both(p.dev ? -p.dev->step_size : -p.step_size);
   ad.inv_bc2 = both(__fdiv_rn(1.f, p.dev ? p.dev->bc2_sqrt : p.bc2_sqrt));
   ad.eps = both(fmaxf(p.eps, 0x1p-126f));  // the reciprocal takes subnormals for 0
+  ad.decay = both(decay_of_seg(p, p.seg[cur.si]));
   const uint32_t key = p.key + (p.d_step ? (uint32_t)*p.d_step * kHashStep : 0u);
-  load_grad<GT>(p, cur);
-  if (!p.early) load_state<GT>(p, cur);
-  cur.decay = decay_of_seg(p, p.seg[cur.si]);
+  uint32_t slot = slot0, slot_ahead = slot0 + (kRing8 - 1) * Ring8<GT>::kSlot;
+  const uint32_t slot_end = slot0 + kRing8 * Ring8<GT>::kSlot;
   for (;;) {
-    Part8<GT> nxt;
-    const int tn = t + (int)gridDim.x;
-    const bool more = tn < p.n_tiles;
-    if (more) {
-      place_part<GT>(p, tn, next_seg(p, cur.si, tn), nxt);
-      load_grad<GT>(p, nxt);
-      load_state<GT>(p, nxt);
-      nxt.decay = nxt.si == cur.si ? cur.decay : decay_of_seg(p, p.seg[nxt.si]);
+    if (ta < p.n_tiles) {
+      ahead = place_tile(p, ta, next_seg(p, ahead.si, ta));
+      fetch_block<GT>(p, ahead, slot_ahead, scales[kRing8 - 1]);
+      ta += gridDim.x;
     }
-    ad.decay = both(cur.decay);
-    if (cur.block >= 0) step_part<PT, GT>(p.seg[cur.si], cur, ad, key + p.seg[cur.si].key);
-    if (!more) break;
-    cur = nxt;
-    t = tn;
+    asm volatile("cp.async.commit_group;\n cp.async.wait_group %0;" ::"n"(kRing8 - 1) : "memory");
+    __syncwarp();  // the warp's copies, not this lane's alone
+    if ((int)(threadIdx.x / 32 * kMomentBlock) < cur.n)
+      step_block<PT, GT>(p.seg[cur.si], cur, slot, scales[0], ad,
+                         key + p.seg[cur.si].key + (uint32_t)(cur.first >> 1) * kHashPair);
+    t += gridDim.x;
+    if (t >= p.n_tiles) break;
+    const Place8 next = place_tile(p, t, next_seg(p, cur.si, t));
+    if (next.si != cur.si) ad.decay = both(decay_of_seg(p, p.seg[next.si]));
+    cur = next;
+#pragma unroll
+    for (int k = 0; k + 1 < kRing8; ++k) scales[k] = scales[k + 1];
+    slot_ahead = slot;
+    slot = slot + Ring8<GT>::kSlot == slot_end ? slot0 : slot + Ring8<GT>::kSlot;
+    __syncwarp();  // every lane has read the slot before it is filled again
   }
+}
+
+template <typename PT, typename GT, int CAP>
+int launch_adamw8_cap(const AdamParamsT<CAP>& p, cudaStream_t s) {
+  static std::atomic<uint64_t> smem_set{0};
+  auto kern = tensors_adamw8<PT, GT, CAP>;
+  if (int st = allow_dynamic_smem(kern, Ring8<GT>::kBytes, smem_set, "tensors_adamw8")) return st;
+  return launch_table(kern, p, p.n_tiles, s, "tensors_adamw8 launch", nullptr, true, Ring8<GT>::kBytes);
 }
 
 template <typename PT, typename GT>
 int launch_adamw8_t(const AdamParamsT<kAdamCap>& p, cudaStream_t s) {
   if (p.n_seg <= kAdamSmallCap)
-    return launch_table(tensors_adamw8<PT, GT, kAdamSmallCap>, compact_table<AdamParamsT<kAdamSmallCap>, AdamHead>(p),
-                        p.n_tiles, s, "tensors_adamw8 launch", nullptr, true);
-  return launch_table(tensors_adamw8<PT, GT, kAdamCap>, p, p.n_tiles, s, "tensors_adamw8 launch", nullptr, true);
+    return launch_adamw8_cap<PT, GT>(compact_table<AdamParamsT<kAdamSmallCap>, AdamHead>(p), s);
+  return launch_adamw8_cap<PT, GT>(p, s);
 }
 
 int launch_tensors_adamw8(int32_t param_dtype, int32_t grad_dtype, const AdamParamsT<kAdamCap>& p, cudaStream_t s) {
