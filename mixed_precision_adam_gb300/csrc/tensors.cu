@@ -125,19 +125,19 @@ int run_norm(const dopt_tensor* ts, int32_t n, float inv_scale, FinalizeArgs fin
       if (ts[k].numel == 0) continue;
       if (p.n_seg == kNormCap) break;
       const size_t elem = dtype_bytes(ts[k].grad_dtype);
-      const int16_t shift = (int16_t)((reinterpret_cast<uintptr_t>(ts[k].grad) & 15u) / elem);
+      const int16_t shift = (int16_t)((reinterpret_cast<uintptr_t>(ts[k].grad) & (kNormVector - 1)) / elem);
       p.seg[p.n_seg++] = NormSeg{ts[k].grad, ts[k].numel, p.n_tiles, (int16_t)ts[k].grad_dtype, shift};
-      p.n_tiles += (int32_t)tiles_of(ts[k].numel + shift, kNormTileBytes / (int)elem);
+      p.n_tiles += (int32_t)tiles_of(ts[k].numel + shift, tensors_norm_tile_bytes() / (int)elem);
     }
     int grid = 0;
-    int st = tensors_norm_grid(p.n_seg, p.n_tiles, &grid);
+    int st = tensors_norm_grid(p, &grid);
     if (st) return st;
     p.partials = parts + fin.n_slots;
     fin.n_slots += grid;
     const bool last = k == n;
     p.fin_counter = last ? counter : nullptr;
     p.fin = fin;
-    if ((st = launch_tensors_norm(p, s, &grid))) return st;
+    if ((st = launch_tensors_norm(p, s))) return st;
     if (last) return DOPT_OK;
     p.n_seg = p.n_tiles = 0;
   }

@@ -22,10 +22,10 @@ struct NormSeg {
   int64_t len;
   int32_t tile0;  // first tile of this tensor in the launch
   int16_t dtype;  // dopt_dtype of the grad
-  int16_t shift;  // elements from the 16-byte boundary below the first one to it
+  int16_t shift;  // elements from the vector boundary below the first one to it
 };
 constexpr int kNormCap = 1280, kNormSmallCap = 64;
-constexpr int kNormTileBytes = 16384;  // grads per tile
+constexpr int kNormVector = 32;  // bytes: the grid tiles are cut on
 
 struct NormHead {
   Partial* partials;      // one slot per CTA of this launch
@@ -175,27 +175,47 @@ __device__ __forceinline__ float decay_of_seg(const AdamHead& p, const AdamSeg& 
 
 // ----------------------------------------------------------- host launches --
 
-// Launch of one kernel over a table; `early` tables may start under the
-// kernel before them (programmatic stream serialization): each CTA waits
-// for that grid before it reads or writes anything it may share with it.
-template <typename K, typename P>
-int launch_table(K kern, const P& params, int n_tiles, cudaStream_t s, const char* what, int* grid_out = nullptr,
-                 bool programmatic = false, size_t smem = 0) {
-  int grid = 0;
-  int st = grid_for(kern, n_tiles, &grid, smem);
+// CTAs of a kernel that the current device holds at once, at most kMaxGrid.
+// Asked once per device and kernel (its dynamic shared memory is allowed
+// then too), so that a later launch, in a stream capture say, is only a launch.
+template <auto Kern, size_t SMEM = 0>
+int resident_ctas(int* out, const char* what) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail(DOPT_E_CUDA, std::string("cudaGetDevice: ") + cudaGetErrorString(e));
+  *out = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (*out) return DOPT_OK;
+  if (SMEM) {
+    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+    if (e != cudaSuccess)
+      return fail(DOPT_E_CUDA, std::string(what) + ": shared memory attribute: " + cudaGetErrorString(e));
+  }
+  int st = grid_for(Kern, kMaxGrid, out, SMEM);
   if (st) return st;
-  if (grid_out) *grid_out = grid;
+  if (dev < 64) known[dev].store(*out, std::memory_order_relaxed);
+  return DOPT_OK;
+}
+
+// Launch of one kernel over a table.  A programmatic launch may start under
+// the kernel before it (programmatic stream serialization): its CTAs wait
+// for that grid before they read or write anything they may share with it.
+template <auto Kern, size_t SMEM = 0, typename P>
+int launch_table(const P& params, cudaStream_t s, const char* what, bool programmatic = false) {
+  int grid = 0;
+  int st = resident_ctas<Kern, SMEM>(&grid, what);
+  if (st) return st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = programmatic ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)std::max(1, std::min(grid, params.n_tiles)));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, params);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, Kern, params);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();  // reported here, not left for the next call to find
     return fail(DOPT_E_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
@@ -204,8 +224,9 @@ int launch_table(K kern, const P& params, int n_tiles, cudaStream_t s, const cha
 }
 
 // One launch each; the table's own count picks the compact parameter block.
-int launch_tensors_norm(const NormParamsT<kNormCap>& p, cudaStream_t s, int* grid);
-int tensors_norm_grid(int n_seg, int n_tiles, int* grid);
+int launch_tensors_norm(const NormParamsT<kNormCap>& p, cudaStream_t s);
+int tensors_norm_tile_bytes();
+int tensors_norm_grid(const NormParamsT<kNormCap>& p, int* grid);  // that launch's CTAs
 int launch_tensors_adamw(int32_t param_dtype, int32_t grad_dtype, const AdamParamsT<kAdamCap>& p, cudaStream_t s);
 int launch_tensors_adamw8(int32_t param_dtype, int32_t grad_dtype, const AdamParamsT<kAdamCap>& p, cudaStream_t s);
 int launch_state8_pack(int32_t values_dtype, const MomentParamsT<kMomentCap>& p, cudaStream_t s);

@@ -156,10 +156,10 @@ __global__ void __launch_bounds__(kThreads, 4) tensors_adamw(const __grid_consta
 
 template <typename PT, typename GT>
 int launch_adamw_t(const AdamParamsT<kAdamCap>& p, cudaStream_t s) {
+  const char* what = "tensors_adamw launch";
   if (p.n_seg <= kAdamSmallCap)
-    return launch_table(tensors_adamw<PT, GT, kAdamSmallCap>, compact_table<AdamParamsT<kAdamSmallCap>, AdamHead>(p),
-                        p.n_tiles, s, "tensors_adamw launch", nullptr, true);
-  return launch_table(tensors_adamw<PT, GT, kAdamCap>, p, p.n_tiles, s, "tensors_adamw launch", nullptr, true);
+    return launch_table<tensors_adamw<PT, GT, kAdamSmallCap>>(compact_table<AdamParamsT<kAdamSmallCap>, AdamHead>(p), s, what, true);
+  return launch_table<tensors_adamw<PT, GT, kAdamCap>>(p, s, what, true);
 }
 
 int launch_tensors_adamw(int32_t param_dtype, int32_t grad_dtype, const AdamParamsT<kAdamCap>& p, cudaStream_t s) {

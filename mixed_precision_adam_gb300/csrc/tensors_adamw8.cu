@@ -15,7 +15,6 @@
 #include <cuda_fp8.h>
 
 #include "tensors.cuh"
-#include "tma.cuh"
 
 namespace dopt {
 
@@ -483,19 +482,13 @@ __global__ void __launch_bounds__(kThreads, kCtas8) tensors_adamw8(const __grid_
   }
 }
 
-template <typename PT, typename GT, int CAP>
-int launch_adamw8_cap(const AdamParamsT<CAP>& p, cudaStream_t s) {
-  static std::atomic<uint64_t> smem_set{0};
-  auto kern = tensors_adamw8<PT, GT, CAP>;
-  if (int st = allow_dynamic_smem(kern, Ring8<GT>::kBytes, smem_set, "tensors_adamw8")) return st;
-  return launch_table(kern, p, p.n_tiles, s, "tensors_adamw8 launch", nullptr, true, Ring8<GT>::kBytes);
-}
-
 template <typename PT, typename GT>
 int launch_adamw8_t(const AdamParamsT<kAdamCap>& p, cudaStream_t s) {
+  const char* what = "tensors_adamw8 launch";
+  constexpr size_t kSmem = Ring8<GT>::kBytes;
   if (p.n_seg <= kAdamSmallCap)
-    return launch_adamw8_cap<PT, GT>(compact_table<AdamParamsT<kAdamSmallCap>, AdamHead>(p), s);
-  return launch_adamw8_cap<PT, GT>(p, s);
+    return launch_table<tensors_adamw8<PT, GT, kAdamSmallCap>, kSmem>(compact_table<AdamParamsT<kAdamSmallCap>, AdamHead>(p), s, what, true);
+  return launch_table<tensors_adamw8<PT, GT, kAdamCap>, kSmem>(p, s, what, true);
 }
 
 int launch_tensors_adamw8(int32_t param_dtype, int32_t grad_dtype, const AdamParamsT<kAdamCap>& p, cudaStream_t s) {
@@ -628,31 +621,32 @@ __global__ void __launch_bounds__(kThreads) state8_unpack(const __grid_constant_
   });
 }
 
-template <typename KSmall, typename KBig>
-int launch_moments(KSmall small, KBig big, const MomentParamsT<kMomentCap>& p, cudaStream_t s, const char* what) {
-  if (p.n_seg <= kMomentSmallCap) {
-    MomentParamsT<kMomentSmallCap> q{};
-    q.n_seg = p.n_seg;
-    q.n_tiles = p.n_tiles;
-    for (int i = 0; i < p.n_seg; ++i) q.seg[i] = p.seg[i];
-    return launch_table(small, q, p.n_tiles, s, what);
-  }
-  return launch_table(big, p, p.n_tiles, s, what);
+MomentParamsT<kMomentSmallCap> compact_moments(const MomentParamsT<kMomentCap>& p) {
+  MomentParamsT<kMomentSmallCap> q{};
+  q.n_seg = p.n_seg;
+  q.n_tiles = p.n_tiles;
+  for (int i = 0; i < p.n_seg; ++i) q.seg[i] = p.seg[i];
+  return q;
+}
+
+template <typename VT>
+int launch_pack_t(const MomentParamsT<kMomentCap>& p, cudaStream_t s) {
+  const char* what = "state8_pack launch";
+  return p.n_seg <= kMomentSmallCap ? launch_table<state8_pack<VT, kMomentSmallCap>>(compact_moments(p), s, what)
+                                    : launch_table<state8_pack<VT, kMomentCap>>(p, s, what);
+}
+template <typename VT>
+int launch_unpack_t(const MomentParamsT<kMomentCap>& p, cudaStream_t s) {
+  const char* what = "state8_unpack launch";
+  return p.n_seg <= kMomentSmallCap ? launch_table<state8_unpack<VT, kMomentSmallCap>>(compact_moments(p), s, what)
+                                    : launch_table<state8_unpack<VT, kMomentCap>>(p, s, what);
 }
 
 int launch_state8_pack(int32_t values_dtype, const MomentParamsT<kMomentCap>& p, cudaStream_t s) {
-  if (values_dtype == DOPT_F32)
-    return launch_moments(state8_pack<float, kMomentSmallCap>, state8_pack<float, kMomentCap>, p, s, "state8_pack launch");
-  return launch_moments(state8_pack<__nv_bfloat16, kMomentSmallCap>, state8_pack<__nv_bfloat16, kMomentCap>, p, s,
-                        "state8_pack launch");
+  return values_dtype == DOPT_F32 ? launch_pack_t<float>(p, s) : launch_pack_t<__nv_bfloat16>(p, s);
 }
-
 int launch_state8_unpack(int32_t values_dtype, const MomentParamsT<kMomentCap>& p, cudaStream_t s) {
-  if (values_dtype == DOPT_F32)
-    return launch_moments(state8_unpack<float, kMomentSmallCap>, state8_unpack<float, kMomentCap>, p, s,
-                          "state8_unpack launch");
-  return launch_moments(state8_unpack<__nv_bfloat16, kMomentSmallCap>, state8_unpack<__nv_bfloat16, kMomentCap>, p, s,
-                        "state8_unpack launch");
+  return values_dtype == DOPT_F32 ? launch_unpack_t<float>(p, s) : launch_unpack_t<__nv_bfloat16>(p, s);
 }
 
 }  // namespace dopt

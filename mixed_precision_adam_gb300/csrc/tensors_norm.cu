@@ -10,59 +10,73 @@
 // whose sum leaves [2^-90, 2^80] is squared again in fp64, out of line: that
 // covers overflow, underflow, infinities and NaN, so the fast path needs
 // no test per element.  fp64 per element, or a conversion per chunk, would
-// be bound by GB300's fp64 rate.
+// be bound by GB300's fp64 rate; with packed fp32 pairs and zeros found by a
+// running minimum an element takes about 3 issue slots of the 11 that its 2
+// bytes allow, and the pass is bound by memory: 1.35e9 bf16 grads in 391 us,
+// 6.89 TB/s (1.02 of the copy bandwidth).
 #include "tensors.cuh"
 
 namespace dopt {
 
-constexpr int kNormVecs = 4;  // 16-byte loads per thread and tile, all in flight together
+// 32-byte loads per thread and tile, all in flight together, and CTAs per SM:
+// four of each keep 128 KB per SM in flight.  Two loads: 5 % slower; more CTAs
+// with two loads, 25 % and more (registers); a ring of asynchronous copies in
+// shared memory, 43 % (its instructions per 16 bytes bound it).
+constexpr int kNormVecs = 4, kNormCtas = 4;
+constexpr int kNormTileBytes = kThreads * kNormVecs * 32;
 
-template <typename GT>
-__device__ __forceinline__ void widen_word(uint32_t w, float* x);  // the one or two elements of a 32-bit word
-template <>
-__device__ __forceinline__ void widen_word<float>(uint32_t w, float* x) { x[0] = __uint_as_float(w); }
-template <>
-__device__ __forceinline__ void widen_word<__nv_bfloat16>(uint32_t w, float* x) {
-  x[0] = __uint_as_float(w << 16);
-  x[1] = __uint_as_float(w & 0xFFFF0000u);
-}
-template <>
-__device__ __forceinline__ void widen_word<__half>(uint32_t w, float* x) {
-  x[0] = __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu)));
-  x[1] = __half2float(__ushort_as_half((unsigned short)(w >> 16)));
-}
-
-// A chunk: 16 elements, in 2 (16-bit) or 4 (fp32) vectors.
+// A chunk: 16 elements, in one (16-bit) or two (fp32) 32-byte vectors.
 template <typename GT>
 struct ChunkOf {
-  uint4 r[sizeof(GT)];
+  uint32_t r[4 * sizeof(GT)];
 };
+template <typename GT>
+constexpr int kChunkVecs = (int)sizeof(GT) / 2;
 
-template <typename GT, typename F>
-__device__ __forceinline__ void each_of(const ChunkOf<GT>& c, F&& f) {
-  constexpr int kPer = 4 / sizeof(GT);
-#pragma unroll
-  for (int k = 0; k < (int)sizeof(GT); ++k) {
-    const uint32_t w[4] = {c.r[k].x, c.r[k].y, c.r[k].z, c.r[k].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float x[2];
-      widen_word<GT>(w[j], x);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) f(x[i]);
-    }
-  }
+// Element pair i of a chunk.
+template <typename GT>
+__device__ __forceinline__ float2 pair_of(const ChunkOf<GT>& c, int i);
+template <>
+__device__ __forceinline__ float2 pair_of<float>(const ChunkOf<float>& c, int i) {
+  return make_float2(__uint_as_float(c.r[2 * i]), __uint_as_float(c.r[2 * i + 1]));
+}
+template <>
+__device__ __forceinline__ float2 pair_of<__nv_bfloat16>(const ChunkOf<__nv_bfloat16>& c, int i) {
+  return make_float2(__uint_as_float(c.r[i] << 16), __uint_as_float(c.r[i] & 0xFFFF0000u));
+}
+template <>
+__device__ __forceinline__ float2 pair_of<__half>(const ChunkOf<__half>& c, int i) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&c.r[i]));
+}
+
+__device__ __forceinline__ float min3_abs(float a, float b, float c) {
+  float d;
+  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // Squares of a chunk whose fp32 sum over- or underflowed, in fp64.
 template <typename GT>
 __device__ __noinline__ double chunk_wide(ChunkOf<GT> c, float inv) {
   double d = 0.0;
-  each_of<GT>(c, [&](float x) {
-    const double y = __fmul_rn(x, inv);
-    d += y * y;
-  });
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 x = pair_of<GT>(c, i);
+    const double a = __fmul_rn(x.x, inv), b = __fmul_rn(x.y, inv);
+    d += a * a + b * b;
+  }
   return d;
+}
+// The zeros of a chunk that has one.
+template <typename GT>
+__device__ __forceinline__ int chunk_zeros(const ChunkOf<GT>& c, float inv) {
+  int z = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 x = pair_of<GT>(c, i);
+    z += (__fmul_rn(x.x, inv) == 0.f) + (__fmul_rn(x.y, inv) == 0.f);
+  }
+  return z;
 }
 
 struct NormSum {
@@ -70,17 +84,20 @@ struct NormSum {
   double wide = 0.0;       // chunks outside the fast range
   int zeros = 0;
   template <typename GT>
-  __device__ __forceinline__ void add(const ChunkOf<GT>& ch, float inv) {
-    float q = 0.f;
+  __device__ __forceinline__ void add(const ChunkOf<GT>& ch, float2 inv) {
+    float2 q2 = make_float2(0.f, 0.f);
+    float least = __int_as_float(0x7F800000);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 x = __fmul2_rn(pair_of<GT>(ch, i), inv);
+      least = min3_abs(x.x, x.y, least);
+      q2 = __ffma2_rn(x, x, q2);
+    }
+    float q = __fadd_rn(q2.x, q2.y);
     int z = 0;
-    each_of<GT>(ch, [&](float x) {
-      x = __fmul_rn(x, inv);
-      z += x == 0.f;
-      q = fmaf(x, x, q);
-    });
-    zeros += z;
+    if (least == 0.f) zeros += z = chunk_zeros<GT>(ch, inv.x);
     if (!(q <= 0x1p80f) || (q < 0x1p-90f && z < 16)) {
-      wide += chunk_wide<GT>(ch, inv);
+      wide += chunk_wide<GT>(ch, inv.x);
       q = 0.f;
     }
     const float t = __fadd_rn(s, q), b = __fsub_rn(t, s);  // s stays below 2^80 times a thread's chunks
@@ -89,39 +106,49 @@ struct NormSum {
   }
 };
 
-// One tile: kNormVecs vectors per thread.  Tiles are cut on the 16-byte grid
+__device__ __forceinline__ void load32(const void* p, uint32_t* r) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p));
+}
+
+// One tile: kNormVecs vectors per thread.  Tiles are cut on the 32-byte grid
 // of the addresses (sg.shift elements before the tensor's first), so only a
 // tensor's first and last vector can be partial, whatever its alignment.
 template <typename GT>
-__device__ __forceinline__ void norm_tile(const NormSeg& sg, int t, float inv, NormSum& acc) {
-  constexpr int kPer = 16 / sizeof(GT), kChunks = kNormVecs / (int)sizeof(GT);
+__device__ __forceinline__ void norm_tile(const NormSeg& sg, int t, float2 inv, NormSum& acc) {
+  constexpr int kPer = 32 / sizeof(GT);  // elements per vector
   constexpr int kTile = kNormTileBytes / (int)sizeof(GT);
-  static_assert(kNormTileBytes == kThreads * kNormVecs * 16, "a tile is the CTA's vectors");
+  constexpr int kChunks = kNormVecs / kChunkVecs<GT>;
+  static_assert(kNormVecs % 2 == 0, "whole fp32 chunks");
   const int64_t first = (int64_t)(t - sg.tile0) * kTile - sg.shift;
   const GT* g = static_cast<const GT*>(sg.grad);
   ChunkOf<GT> ch[kChunks];
-  uint4* r = &ch[0].r[0];
+  uint32_t* r = &ch[0].r[0];
   if (first >= 0 && first + kTile <= sg.len) {
-    const uint4* p = reinterpret_cast<const uint4*>(g + first) + threadIdx.x;
+    const char* p = reinterpret_cast<const char*>(g + first) + threadIdx.x * 32;
 #pragma unroll
-    for (int u = 0; u < kNormVecs; ++u) r[u] = __ldcg(p + u * kThreads);
+    for (int u = 0; u < kNormVecs; ++u) load32(p + u * kThreads * 32, r + 8 * u);
   } else {
 #pragma unroll
     for (int u = 0; u < kNormVecs; ++u) {
       const int64_t e = first + (int64_t)(u * kThreads + threadIdx.x) * kPer;
-      r[u] = make_uint4(0u, 0u, 0u, 0u);
       if (e >= 0 && e + kPer <= sg.len) {
-        r[u] = __ldcg(reinterpret_cast<const uint4*>(g + e));
+        load32(g + e, r + 8 * u);
       } else {
         alignas(16) GT x[kPer];
-        *reinterpret_cast<uint4*>(x) = r[u];
+        uint32_t* w = reinterpret_cast<uint32_t*>(x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 0u;
+#pragma unroll
         for (int j = 0; j < kPer; ++j) {
           if (e + j >= 0 && e + j < sg.len)
             x[j] = g[e + j];
           else
             --acc.zeros;  // the filling counts as zeros below
         }
-        r[u] = *reinterpret_cast<const uint4*>(x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[8 * u + j] = w[j];
       }
     }
   }
@@ -130,19 +157,20 @@ __device__ __forceinline__ void norm_tile(const NormSeg& sg, int t, float inv, N
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) tensors_norm(const __grid_constant__ NormParamsT<CAP> p) {
+__global__ void __launch_bounds__(kThreads, kNormCtas) tensors_norm(const __grid_constant__ NormParamsT<CAP> p) {
   NormSum acc;
+  const float2 inv = make_float2(p.inv_scale, p.inv_scale);
   int si = 0;
   if ((int)blockIdx.x < p.n_tiles) si = find_seg(p, blockIdx.x);
   for (int t = blockIdx.x; t < p.n_tiles; t += gridDim.x) {
     si = next_seg(p, si, t);
     const NormSeg& sg = p.seg[si];
     if (sg.dtype == DOPT_F32)
-      norm_tile<float>(sg, t, p.inv_scale, acc);
+      norm_tile<float>(sg, t, inv, acc);
     else if (sg.dtype == DOPT_BF16)
-      norm_tile<__nv_bfloat16>(sg, t, p.inv_scale, acc);
+      norm_tile<__nv_bfloat16>(sg, t, inv, acc);
     else
-      norm_tile<__half>(sg, t, p.inv_scale, acc);
+      norm_tile<__half>(sg, t, inv, acc);
   }
   allow_dependent_launch();
   __shared__ double s_sum[kThreads / 32];
@@ -178,16 +206,21 @@ __global__ void __launch_bounds__(kThreads) tensors_norm(const __grid_constant__
   finalize_call(p.fin);
 }
 
-int tensors_norm_grid(int n_seg, int n_tiles, int* grid) {
-  return n_seg <= kNormSmallCap ? grid_for(tensors_norm<kNormSmallCap>, n_tiles, grid)
-                                : grid_for(tensors_norm<kNormCap>, n_tiles, grid);
+int tensors_norm_tile_bytes() { return kNormTileBytes; }
+
+int tensors_norm_grid(const NormParamsT<kNormCap>& p, int* grid) {
+  const char* what = "tensors_norm launch";
+  int st = p.n_seg <= kNormSmallCap ? resident_ctas<tensors_norm<kNormSmallCap>>(grid, what)
+                                    : resident_ctas<tensors_norm<kNormCap>>(grid, what);
+  *grid = std::max(1, std::min(*grid, p.n_tiles));
+  return st;
 }
 
-int launch_tensors_norm(const NormParamsT<kNormCap>& p, cudaStream_t s, int* grid) {
+int launch_tensors_norm(const NormParamsT<kNormCap>& p, cudaStream_t s) {
+  const char* what = "tensors_norm launch";
   if (p.n_seg <= kNormSmallCap)
-    return launch_table(tensors_norm<kNormSmallCap>, compact_table<NormParamsT<kNormSmallCap>, NormHead>(p), p.n_tiles,
-                        s, "tensors_norm launch", grid);
-  return launch_table(tensors_norm<kNormCap>, p, p.n_tiles, s, "tensors_norm launch", grid);
+    return launch_table<tensors_norm<kNormSmallCap>>(compact_table<NormParamsT<kNormSmallCap>, NormHead>(p), s, what);
+  return launch_table<tensors_norm<kNormCap>>(p, s, what);
 }
 
 }  // namespace dopt
