@@ -176,7 +176,7 @@ struct FinalizeArgs {
   float* d_norm;
   float* d_coef;
   int32_t* d_found;
-  int32_t* err_flag;
+  int32_t* err_flag;  // NULL: the passes before never wait for copies
   K2Step step;
   // global terms in device memory (a multi-rank step): when set, they
   // replace the partial sum plus remote_sumsq / remote_found
@@ -362,7 +362,7 @@ __device__ __forceinline__ void finalize_block(const FinalizeArgs& f) {
     z += (int)(fz >> 32);
   };
   // the error flag, read with the slots rather than after the sum
-  const int err_early = (threadIdx.x == 0 && !f.local_sumsq) ? __ldcg(f.err_flag) : 0;
+  const int err_early = (threadIdx.x == 0 && !f.local_sumsq && f.err_flag) ? __ldcg(f.err_flag) : 0;
   // every slot's load issued before any is summed (up to eight per thread
   // per round; a short tail predicated rather than looped)
   for (; i < f.n_slots; i += 8 * NT) {
@@ -403,7 +403,7 @@ __device__ __forceinline__ void finalize_block(const FinalizeArgs& f) {
   }
   if (threadIdx.x == 0) {
     const int kernel_error = err_early == kErrorMagic ? 1 : 0;
-    *f.err_flag = 0;
+    if (f.err_flag) *f.err_flag = 0;
     const double sumsq = f.d_global_sumsq ? __ldcg(f.d_global_sumsq) : s_sum[0] + f.remote_sumsq;
     const int remote_bad = f.d_global_sumsq ? (__ldcg(f.d_global_found) != 0) : (f.remote_found != 0);
     const int found = (s_bad[0] || remote_bad || kernel_error) ? 1 : 0;

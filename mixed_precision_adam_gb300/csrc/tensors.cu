@@ -107,12 +107,8 @@ int check_norm_args(int32_t n, float inv_scale, double max_norm, const void* ws,
 
 char* ws_at(void* ws, size_t offset) { return static_cast<char*>(ws) + offset; }
 
-// The norm launches of a list, the finalize in the last one.
+// The norm launches of a list, then the finalize.
 int run_norm(const dopt_tensor* ts, int32_t n, float inv_scale, FinalizeArgs fin, void* ws, cudaStream_t s) {
-  uint32_t* counter = reinterpret_cast<uint32_t*>(ws_at(ws, kFinCounterOffset));
-  // the ticket counter and the error word before it start every call at zero
-  cudaError_t e = cudaMemsetAsync(ws_at(ws, kErrorFlagOffset), 0, kFinCounterOffset + 4 - kErrorFlagOffset, s);
-  if (e != cudaSuccess) return fail(DOPT_E_CUDA, std::string("grad norm: ") + cudaGetErrorString(e));
   Partial* parts = reinterpret_cast<Partial*>(ws_at(ws, kScalarBytes));
   NormParamsT<kNormCap> p;
   p.inv_scale = inv_scale;
@@ -120,10 +116,9 @@ int run_norm(const dopt_tensor* ts, int32_t n, float inv_scale, FinalizeArgs fin
   fin.parts = parts;
   fin.n_slots = 0;
   int32_t k = 0;
-  for (;;) {
-    for (; k < n; ++k) {
+  do {
+    for (; k < n && p.n_seg < kNormCap; ++k) {
       if (ts[k].numel == 0) continue;
-      if (p.n_seg == kNormCap) break;
       const size_t elem = dtype_bytes(ts[k].grad_dtype);
       const int16_t shift = (int16_t)((reinterpret_cast<uintptr_t>(ts[k].grad) & (kNormVector - 1)) / elem);
       p.seg[p.n_seg++] = NormSeg{ts[k].grad, ts[k].numel, p.n_tiles, (int16_t)ts[k].grad_dtype, shift};
@@ -134,13 +129,10 @@ int run_norm(const dopt_tensor* ts, int32_t n, float inv_scale, FinalizeArgs fin
     if (st) return st;
     p.partials = parts + fin.n_slots;
     fin.n_slots += grid;
-    const bool last = k == n;
-    p.fin_counter = last ? counter : nullptr;
-    p.fin = fin;
     if ((st = launch_tensors_norm(p, s))) return st;
-    if (last) return DOPT_OK;
     p.n_seg = p.n_tiles = 0;
-  }
+  } while (k < n);
+  return launch_tensors_finalize(fin, s);
 }
 
 // AdamSeg::shift of a tensor with fp32 moments: its first element's index
@@ -332,7 +324,6 @@ int dopt_tensors_grad_norm(const dopt_tensor* tensors, int32_t n_tensors, float 
     f.d_norm = d_norm;
     f.d_coef = d_clip_coef;
     f.d_found = d_found_inf;
-    f.err_flag = reinterpret_cast<int32_t*>(ws_at(workspace, kErrorFlagOffset));
     return run_norm(tensors, n_tensors, inv_loss_scale, f, workspace, (cudaStream_t)stream);
   });
 }
@@ -368,7 +359,6 @@ int dopt_tensors_step(const dopt_tensor* tensors, int32_t n_tensors, const dopt_
     f.sc = sc;
     f.d_norm = d_norm;
     f.d_found = d_found_inf;
-    f.err_flag = reinterpret_cast<int32_t*>(ws_at(workspace, kErrorFlagOffset));
     DevStep* dev = reinterpret_cast<DevStep*>(ws_at(workspace, kDevStepOffset));
     if (d_step)
       f.step = K2Step{d_step, d_lr, hp->lr, hp->weight_decay, hp->beta1, hp->beta2, dev};

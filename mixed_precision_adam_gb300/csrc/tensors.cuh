@@ -3,7 +3,7 @@
 // parameters, as the run tables of the sharded step), typed loads and
 // stores, the AdamW arithmetic, and the 8-bit moments' encoding.
 //   tensors.cu        -- the C entry points: checks, tables, launches
-//   tensors_norm.cu   -- the grad norm (with the finalize in its last CTA)
+//   tensors_norm.cu   -- the grad norm, and the finalize
 //   tensors_adamw.cu  -- AdamW with fp32 moments
 //   tensors_adamw8.cu -- AdamW with 8-bit moments, and their pack / unpack
 #pragma once
@@ -30,9 +30,11 @@ constexpr int kNormVector = 32;  // bytes: the grid tiles are cut on
 struct NormHead {
   Partial* partials;      // one slot per CTA of this launch
   float inv_scale;
-  uint32_t* fin_counter;  // last launch of a call: the finalize's ticket counter, else NULL
-  FinalizeArgs fin;
   int32_t n_seg, n_tiles;
+};
+struct FinalizeParams {
+  FinalizeArgs fin;
+  int32_t n_tiles;  // 1: one CTA
 };
 template <int CAP>
 struct NormParamsT : NormHead {
@@ -225,6 +227,7 @@ int launch_table(const P& params, cudaStream_t s, const char* what, bool program
 
 // One launch each; the table's own count picks the compact parameter block.
 int launch_tensors_norm(const NormParamsT<kNormCap>& p, cudaStream_t s);
+int launch_tensors_finalize(const FinalizeArgs& fin, cudaStream_t s);
 int tensors_norm_tile_bytes();
 int tensors_norm_grid(const NormParamsT<kNormCap>& p, int* grid);  // that launch's CTAs
 int launch_tensors_adamw(int32_t param_dtype, int32_t grad_dtype, const AdamParamsT<kAdamCap>& p, cudaStream_t s);

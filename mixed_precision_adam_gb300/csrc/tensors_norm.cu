@@ -1,6 +1,9 @@
 // tensors_norm.cu -- the grad norm over a list of tensors: one pass over the
 // grads, sum of squares, non-finite flag and zero count per CTA, and the
-// finalize (norm, clip coefficient, skip decision) in the last CTA.
+// finalize (norm, clip coefficient, skip decision) in a launch of one CTA
+// that starts under it.  (A ticket counter and the finalize in the last CTA,
+// as the sharded step has it, needs its counter cleared before every call
+// and two fences after: 12.3 us for a 413,856-element list, against 6.5.)
 //
 // Mathematics: sum (g * inv_scale)^2.  A thread adds the squares of 16
 // elements in fp32 (a chunk; all terms positive, so at most 16 roundings
@@ -194,16 +197,15 @@ __global__ void __launch_bounds__(kThreads, kNormCtas) tensors_norm(const __grid
     }
     p.partials[blockIdx.x] = Partial{s_sum[0], isfinite(s_sum[0]) ? 0 : 1, s_zero[0]};
   }
-  if (!p.fin_counter) return;
-  __shared__ int s_last;
-  if (threadIdx.x == 0) {
-    __threadfence();  // this CTA's partial before its ticket
-    s_last = atomicAdd(p.fin_counter, 1u) == gridDim.x - 1;
-  }
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  finalize_call(p.fin);
+}
+
+// The finalize of a call: one CTA, launched to start under the last norm
+// launch and waiting for it (and so for the ones before it, which that one
+// waited for) before it reads their partials.
+__global__ void __launch_bounds__(kThreads) tensors_finalize(const __grid_constant__ FinalizeParams p) {
+  allow_dependent_launch();  // the AdamW launch behind it waits for this grid
+  wait_for_prior_grids();
+  finalize_block<kThreads>(p.fin);
 }
 
 int tensors_norm_tile_bytes() { return kNormTileBytes; }
@@ -221,6 +223,10 @@ int launch_tensors_norm(const NormParamsT<kNormCap>& p, cudaStream_t s) {
   if (p.n_seg <= kNormSmallCap)
     return launch_table<tensors_norm<kNormSmallCap>>(compact_table<NormParamsT<kNormSmallCap>, NormHead>(p), s, what);
   return launch_table<tensors_norm<kNormCap>>(p, s, what);
+}
+
+int launch_tensors_finalize(const FinalizeArgs& fin, cudaStream_t s) {
+  return launch_table<tensors_finalize>(FinalizeParams{fin, 1}, s, "tensors_finalize launch", true);
 }
 
 }  // namespace dopt
