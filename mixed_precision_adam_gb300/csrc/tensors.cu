@@ -138,19 +138,19 @@ int run_norm(const dopt_tensor* ts, int32_t n, float inv_scale, FinalizeArgs fin
 // AdamSeg::shift of a tensor with fp32 moments: its first element's index
 // within the groups of four that its arrays are read in, when they agree
 // (separate allocations, or views of buffers at one element offset).
-int32_t common_shift(const AdamSeg& g, int32_t pd, int32_t gd) {
+int32_t common_shift(const AdamSeg& g) {
   auto index = [](const void* p, size_t elem) { return (int32_t)(reinterpret_cast<uintptr_t>(p) / elem & 3); };
   const int32_t at = index(g.weight, 4);
-  const bool same = index(g.m, 4) == at && index(g.v, 4) == at && index(g.grad, dtype_bytes(gd)) == at &&
-                    index(g.param, dtype_bytes(pd)) == at;
+  const bool same = index(g.m, 4) == at && index(g.v, 4) == at && index(g.grad, dtype_bytes(g.grad_dtype)) == at &&
+                    index(g.param, dtype_bytes(g.param_dtype)) == at;
   return same ? at : -1;
 }
 
 // Whether a tensor with 8-bit moments has its first element on a vector
 // boundary of every array (16 bytes, 32 for the weights): the blocks start there.
-bool block_vectors(const AdamSeg& g, int32_t pd) {
+bool block_vectors(const AdamSeg& g) {
   return aligned_to(g.weight, 32) && aligned_to(g.m, 16) && aligned_to(g.v, 16) &&
-         aligned_to(g.grad, 16) && aligned_to(g.param, 8 * dtype_bytes(pd));
+         aligned_to(g.grad, 16) && aligned_to(g.param, 8 * dtype_bytes(g.param_dtype));
 }
 
 struct AdamJob {
@@ -164,8 +164,8 @@ struct AdamJob {
   bool early = false;  // the launch before is this call's norm
 };
 
-// The AdamW launches of a list: one table per combination of types in it
-// (more when it has more tensors than a table holds).
+// The AdamW launches of a list: one per moments' format in it (more when it
+// has more tensors than a table holds).
 int run_adamw(const dopt_tensor* ts, int32_t n, const AdamJob& j, cudaStream_t s) {
   const dopt_adamw_hparams* hp = j.hp;
   AdamParamsT<kAdamCap> p;
@@ -184,48 +184,47 @@ int run_adamw(const dopt_tensor* ts, int32_t n, const AdamJob& j, cudaStream_t s
   p.inv_scale = j.inv_scale;
   p.key = j.seed + (j.dev ? 0u : (uint32_t)hp->step * kHashStep);
   p.early = j.early ? 1 : 0;
-  for (int32_t moments : {DOPT_MOMENTS_F32, DOPT_MOMENTS_8BIT})
-    for (int32_t pd : {DOPT_F32, DOPT_BF16, DOPT_F16})
-      for (int32_t gd : {DOPT_F32, DOPT_BF16, DOPT_F16}) {
-        if (gd != DOPT_F32 && gd != pd) continue;
-        p.n_seg = p.n_tiles = 0;
-        auto flush = [&]() -> int {
-          if (!p.n_seg) return DOPT_OK;
-          int st = moments == DOPT_MOMENTS_F32 ? launch_tensors_adamw(pd, gd, p, s) : launch_tensors_adamw8(pd, gd, p, s);
-          p.n_seg = p.n_tiles = 0;
-          p.early = 1;
-          return st;
-        };
-        for (int32_t k = 0; k < n; ++k) {
-          const dopt_tensor& t = ts[k];
-          if (t.numel == 0 || t.moments != moments || t.param_dtype != pd || t.grad_dtype != gd) continue;
-          if (p.n_seg == kAdamCap)
-            if (int st = flush()) return st;
-          AdamSeg& g = p.seg[p.n_seg++];
-          g.param = t.param;
-          g.grad = t.grad;
-          g.weight = pd == DOPT_F32 ? static_cast<float*>(t.param) : t.master;
-          g.m = t.exp_avg;
-          g.v = t.exp_avg_sq;
-          g.m_scale = t.exp_avg_scale;
-          g.v_scale = t.exp_avg_sq_scale;
-          g.len = t.numel;
-          if (j.dev)
-            g.wd_mult = t.wd_mult;
-          else
-            g.decay = (float)(1.0 - p.lr_wd * t.wd_mult);
-          g.tile0 = p.n_tiles;
-          g.key = (uint32_t)k * kHashTensor;
-          if (moments == DOPT_MOMENTS_F32) {
-            g.shift = common_shift(g, pd, gd);
-            p.n_tiles += (int32_t)tiles_of(t.numel + std::max(g.shift, 0), kAdamTile32);
-          } else {
-            g.shift = block_vectors(g, pd) ? 0 : -1;
-            p.n_tiles += (int32_t)tiles_of(t.numel, kAdamTile);
-          }
-        }
+  for (int32_t moments : {DOPT_MOMENTS_F32, DOPT_MOMENTS_8BIT}) {
+    p.n_seg = p.n_tiles = 0;
+    auto flush = [&]() -> int {
+      if (!p.n_seg) return DOPT_OK;
+      int st = moments == DOPT_MOMENTS_F32 ? launch_tensors_adamw(p, s) : launch_tensors_adamw8(p, s);
+      p.n_seg = p.n_tiles = 0;
+      p.early = 1;
+      return st;
+    };
+    for (int32_t k = 0; k < n; ++k) {
+      const dopt_tensor& t = ts[k];
+      if (t.numel == 0 || t.moments != moments) continue;
+      if (p.n_seg == kAdamCap)
         if (int st = flush()) return st;
+      AdamSeg& g = p.seg[p.n_seg++];
+      g.param = t.param;
+      g.grad = t.grad;
+      g.weight = t.param_dtype == DOPT_F32 ? static_cast<float*>(t.param) : t.master;
+      g.m = t.exp_avg;
+      g.v = t.exp_avg_sq;
+      g.m_scale = t.exp_avg_scale;
+      g.v_scale = t.exp_avg_sq_scale;
+      g.len = t.numel;
+      if (j.dev)
+        g.wd_mult = t.wd_mult;
+      else
+        g.decay = (float)(1.0 - p.lr_wd * t.wd_mult);
+      g.tile0 = p.n_tiles;
+      g.key = (uint32_t)k * kHashTensor;
+      g.param_dtype = (int16_t)t.param_dtype;
+      g.grad_dtype = (int16_t)t.grad_dtype;
+      if (moments == DOPT_MOMENTS_F32) {
+        g.shift = common_shift(g);
+        p.n_tiles += (int32_t)tiles_of(t.numel + std::max(g.shift, 0), kAdamTile32);
+      } else {
+        g.shift = block_vectors(g) ? 0 : -1;
+        p.n_tiles += (int32_t)tiles_of(t.numel, kAdamTile);
       }
+    }
+    if (int st = flush()) return st;
+  }
   return DOPT_OK;
 }
 

@@ -62,7 +62,7 @@ struct AdamSeg {
   // from the boundary below the tensor's first element to it (0 to 3);
   // 8-bit moments, 0 when the first element is one; -1: none.
   int32_t shift;
-  int32_t reserved;
+  int16_t param_dtype, grad_dtype;  // dopt_dtype
 };
 constexpr int kAdamCap = 360, kAdamSmallCap = 40;
 constexpr int kAdamTile32 = 1024;  // elements per tile, fp32 moments
@@ -151,6 +151,18 @@ __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return
 template <>
 __device__ __forceinline__ __half narrow<__half>(float x) { return __float2half_rn(x); }
 
+// One element of an array whose type is known at run time.
+__device__ __forceinline__ float load_element(const void* p, int64_t i, int dtype) {
+  if (dtype == DOPT_F32) return static_cast<const float*>(p)[i];
+  if (dtype == DOPT_BF16) return widen(static_cast<const __nv_bfloat16*>(p)[i]);
+  return widen(static_cast<const __half*>(p)[i]);
+}
+// The 16-bit param of an fp32 weight (an fp32 param is the weight).
+__device__ __forceinline__ void store_param(void* p, int64_t i, int dtype, float w) {
+  if (dtype == DOPT_BF16) static_cast<__nv_bfloat16*>(p)[i] = narrow<__nv_bfloat16>(w);
+  if (dtype == DOPT_F16) static_cast<__half*>(p)[i] = narrow<__half>(w);
+}
+
 // One element of AdamW, each operation rounded once in fp32: the arithmetic
 // of the sharded step's AdamW pass.
 struct AdamScalars {
@@ -230,8 +242,8 @@ int launch_tensors_norm(const NormParamsT<kNormCap>& p, cudaStream_t s);
 int launch_tensors_finalize(const FinalizeArgs& fin, cudaStream_t s);
 int tensors_norm_tile_bytes();
 int tensors_norm_grid(const NormParamsT<kNormCap>& p, int* grid);  // that launch's CTAs
-int launch_tensors_adamw(int32_t param_dtype, int32_t grad_dtype, const AdamParamsT<kAdamCap>& p, cudaStream_t s);
-int launch_tensors_adamw8(int32_t param_dtype, int32_t grad_dtype, const AdamParamsT<kAdamCap>& p, cudaStream_t s);
+int launch_tensors_adamw(const AdamParamsT<kAdamCap>& p, cudaStream_t s);
+int launch_tensors_adamw8(const AdamParamsT<kAdamCap>& p, cudaStream_t s);
 int launch_state8_pack(int32_t values_dtype, const MomentParamsT<kMomentCap>& p, cudaStream_t s);
 int launch_state8_unpack(int32_t values_dtype, const MomentParamsT<kMomentCap>& p, cudaStream_t s);
 

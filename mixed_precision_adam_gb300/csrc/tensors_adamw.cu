@@ -10,49 +10,34 @@
 
 namespace dopt {
 
-// Four elements of a type, as loaded and stored at once.
-template <typename T>
-struct Four;
-template <>
-struct Four<float> {
-  using Raw = float4;
-  static __device__ __forceinline__ void widen4(const Raw& r, float* x) {
-    x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w;
-  }
-};
-template <>
-struct Four<__nv_bfloat16> {
-  using Raw = uint2;
-  static __device__ __forceinline__ void widen4(const Raw& r, float* x) {
+// Four elements of a 16-bit type, as loaded and stored at once.
+__device__ __forceinline__ float half_bits(unsigned bits) { return __half2float(__ushort_as_half((unsigned short)bits)); }
+__device__ __forceinline__ void widen4(const uint4& r, int dtype, float* x) {
+  if (dtype == DOPT_F32) {
+    x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y); x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
+  } else if (dtype == DOPT_BF16) {
     x[0] = __uint_as_float(r.x << 16); x[1] = __uint_as_float(r.x & 0xFFFF0000u);
     x[2] = __uint_as_float(r.y << 16); x[3] = __uint_as_float(r.y & 0xFFFF0000u);
+  } else {
+    x[0] = half_bits(r.x & 0xFFFFu); x[1] = half_bits(r.x >> 16);
+    x[2] = half_bits(r.y & 0xFFFFu); x[3] = half_bits(r.y >> 16);
   }
-  static __device__ __forceinline__ Raw narrow4(const float* x) {
+}
+__device__ __forceinline__ uint2 narrow4(int dtype, const float* x) {
+  if (dtype == DOPT_BF16) {
     const unsigned a = __bfloat16_as_ushort(__float2bfloat16_rn(x[0])), b = __bfloat16_as_ushort(__float2bfloat16_rn(x[1]));
     const unsigned c = __bfloat16_as_ushort(__float2bfloat16_rn(x[2])), d = __bfloat16_as_ushort(__float2bfloat16_rn(x[3]));
     return make_uint2(a | (b << 16), c | (d << 16));
   }
-};
-template <>
-struct Four<__half> {
-  using Raw = uint2;
-  static __device__ __forceinline__ float h(unsigned bits) { return __half2float(__ushort_as_half((unsigned short)bits)); }
-  static __device__ __forceinline__ void widen4(const Raw& r, float* x) {
-    x[0] = h(r.x & 0xFFFFu); x[1] = h(r.x >> 16);
-    x[2] = h(r.y & 0xFFFFu); x[3] = h(r.y >> 16);
-  }
-  static __device__ __forceinline__ Raw narrow4(const float* x) {
-    const unsigned a = __half_as_ushort(__float2half_rn(x[0])), b = __half_as_ushort(__float2half_rn(x[1]));
-    const unsigned c = __half_as_ushort(__float2half_rn(x[2])), d = __half_as_ushort(__float2half_rn(x[3]));
-    return make_uint2(a | (b << 16), c | (d << 16));
-  }
-};
+  const unsigned a = __half_as_ushort(__float2half_rn(x[0])), b = __half_as_ushort(__float2half_rn(x[1]));
+  const unsigned c = __half_as_ushort(__float2half_rn(x[2])), d = __half_as_ushort(__float2half_rn(x[3]));
+  return make_uint2(a | (b << 16), c | (d << 16));
+}
 
 // A thread's part of a tile.  `e` is its first element; `full`: its four
 // elements are in the tensor and every array has them on a vector boundary.
-template <typename GT>
 struct AdamPart {
-  typename Four<GT>::Raw g;
+  uint4 g;  // as loaded: 16-bit grads take two words
   float4 w, m, v;
   int64_t first;
   int64_t e;
@@ -61,8 +46,8 @@ struct AdamPart {
   bool full;
 };
 
-template <typename GT, typename P>
-__device__ __forceinline__ void place_part(const P& p, int t, int si, AdamPart<GT>& a) {
+template <typename P>
+__device__ __forceinline__ void place_part(const P& p, int t, int si, AdamPart& a) {
   const AdamSeg& sg = p.seg[si];
   a.si = si;
   // tiles are cut `shift` elements below the first one, where every array
@@ -71,28 +56,35 @@ __device__ __forceinline__ void place_part(const P& p, int t, int si, AdamPart<G
   a.e = a.first + threadIdx.x * 4;
   a.full = sg.shift >= 0 && a.e >= 0 && a.e + 4 <= sg.len;
 }
-template <typename GT, typename P>
-__device__ __forceinline__ void load_state(const P& p, AdamPart<GT>& a) {
+template <typename P>
+__device__ __forceinline__ void load_state(const P& p, AdamPart& a) {
   if (!a.full) return;
   const AdamSeg& sg = p.seg[a.si];
   a.w = __ldcs(reinterpret_cast<const float4*>(sg.weight + a.e));
   a.m = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(sg.m) + a.e));
   a.v = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(sg.v) + a.e));
 }
-template <typename GT, typename P>
-__device__ __forceinline__ void load_grad(const P& p, AdamPart<GT>& a) {
-  if (a.full)
-    a.g = __ldcs(reinterpret_cast<const typename Four<GT>::Raw*>(static_cast<const GT*>(p.seg[a.si].grad) + a.e));
+template <typename P>
+__device__ __forceinline__ void load_grad(const P& p, AdamPart& a) {
+  if (!a.full) return;
+  const AdamSeg& sg = p.seg[a.si];
+  if (sg.grad_dtype == DOPT_F32) {
+    a.g = __ldcs(reinterpret_cast<const uint4*>(static_cast<const float*>(sg.grad) + a.e));
+  } else {
+    const uint2 r = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(sg.grad) + a.e));
+    a.g.x = r.x;
+    a.g.y = r.y;
+  }
 }
 
-template <typename PT, typename GT, int CAP>
+template <int CAP>
 __global__ void __launch_bounds__(kThreads, 4) tensors_adamw(const __grid_constant__ AdamParamsT<CAP> p) {
   int t = blockIdx.x;
   const bool work = t < p.n_tiles;
-  AdamPart<GT> cur;
+  AdamPart cur;
   if (work) {
-    place_part<GT>(p, t, find_seg(p, t), cur);
-    if (p.early) load_state<GT>(p, cur);  // the launch before writes none of it
+    place_part(p, t, find_seg(p, t), cur);
+    if (p.early) load_state(p, cur);  // the launch before writes none of it
   }
   wait_for_prior_grids();
   if (!work || (p.found_inf && *p.found_inf)) return;
@@ -100,17 +92,17 @@ __global__ void __launch_bounds__(kThreads, 4) tensors_adamw(const __grid_consta
   s.c = p.coef ? *p.coef : 1.f;
   s.step_size = p.dev ? p.dev->step_size : p.step_size;
   s.bc2_sqrt = p.dev ? p.dev->bc2_sqrt : p.bc2_sqrt;
-  load_grad<GT>(p, cur);
-  if (!p.early) load_state<GT>(p, cur);
+  load_grad(p, cur);
+  if (!p.early) load_state(p, cur);
   cur.decay = decay_of_seg(p, p.seg[cur.si]);
   for (;;) {
-    AdamPart<GT> nxt;
+    AdamPart nxt;
     const int tn = t + (int)gridDim.x;
     const bool more = tn < p.n_tiles;
     if (more) {
-      place_part<GT>(p, tn, next_seg(p, cur.si, tn), nxt);
-      load_grad<GT>(p, nxt);
-      load_state<GT>(p, nxt);
+      place_part(p, tn, next_seg(p, cur.si, tn), nxt);
+      load_grad(p, nxt);
+      load_state(p, nxt);
       nxt.decay = nxt.si == cur.si ? cur.decay : decay_of_seg(p, p.seg[nxt.si]);
     }
     const AdamSeg& sg = p.seg[cur.si];
@@ -120,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 4) tensors_adamw(const __grid_consta
     float* const vp = static_cast<float*>(sg.v);
     if (cur.full) {
       float g[4];
-      Four<GT>::widen4(cur.g, g);
+      widen4(cur.g, sg.grad_dtype, g);
       float w[4] = {cur.w.x, cur.w.y, cur.w.z, cur.w.w};
       float m[4] = {cur.m.x, cur.m.y, cur.m.z, cur.m.w};
       float v[4] = {cur.v.x, cur.v.y, cur.v.z, cur.v.w};
@@ -129,8 +121,8 @@ __global__ void __launch_bounds__(kThreads, 4) tensors_adamw(const __grid_consta
       __stcs(reinterpret_cast<float4*>(wp + cur.e), make_float4(w[0], w[1], w[2], w[3]));
       __stcs(reinterpret_cast<float4*>(mp + cur.e), make_float4(m[0], m[1], m[2], m[3]));
       __stcs(reinterpret_cast<float4*>(vp + cur.e), make_float4(v[0], v[1], v[2], v[3]));
-      if constexpr (sizeof(PT) == 2)
-        __stcs(reinterpret_cast<uint2*>(static_cast<PT*>(sg.param) + cur.e), Four<PT>::narrow4(w));
+      if (sg.param_dtype != DOPT_F32)
+        __stcs(reinterpret_cast<uint2*>(static_cast<uint16_t*>(sg.param) + cur.e), narrow4(sg.param_dtype, w));
     } else {
       // a tensor's ragged ends (its own four elements), or a tensor whose
       // arrays have no common vector boundary (consecutive threads take
@@ -141,11 +133,11 @@ __global__ void __launch_bounds__(kThreads, 4) tensors_adamw(const __grid_consta
         const int64_t e = ends ? cur.e + j : cur.first + j * kThreads + threadIdx.x;
         if (e < 0 || e >= sg.len) continue;
         float w = wp[e], m = mp[e], v = vp[e];
-        adamw_element(widen<GT>(static_cast<const GT*>(sg.grad)[e]), p, s, w, m, v);
+        adamw_element(load_element(sg.grad, e, sg.grad_dtype), p, s, w, m, v);
         wp[e] = w;
         mp[e] = m;
         vp[e] = v;
-        if constexpr (sizeof(PT) == 2) static_cast<PT*>(sg.param)[e] = narrow<PT>(w);
+        store_param(sg.param, e, sg.param_dtype, w);
       }
     }
     if (!more) break;
@@ -154,21 +146,11 @@ __global__ void __launch_bounds__(kThreads, 4) tensors_adamw(const __grid_consta
   }
 }
 
-template <typename PT, typename GT>
-int launch_adamw_t(const AdamParamsT<kAdamCap>& p, cudaStream_t s) {
+int launch_tensors_adamw(const AdamParamsT<kAdamCap>& p, cudaStream_t s) {
   const char* what = "tensors_adamw launch";
   if (p.n_seg <= kAdamSmallCap)
-    return launch_table<tensors_adamw<PT, GT, kAdamSmallCap>>(compact_table<AdamParamsT<kAdamSmallCap>, AdamHead>(p), s, what, true);
-  return launch_table<tensors_adamw<PT, GT, kAdamCap>>(p, s, what, true);
-}
-
-int launch_tensors_adamw(int32_t param_dtype, int32_t grad_dtype, const AdamParamsT<kAdamCap>& p, cudaStream_t s) {
-  const bool f32 = grad_dtype == DOPT_F32;
-  switch (param_dtype) {
-    case DOPT_BF16: return f32 ? launch_adamw_t<__nv_bfloat16, float>(p, s) : launch_adamw_t<__nv_bfloat16, __nv_bfloat16>(p, s);
-    case DOPT_F16: return f32 ? launch_adamw_t<__half, float>(p, s) : launch_adamw_t<__half, __half>(p, s);
-    default: return launch_adamw_t<float, float>(p, s);
-  }
+    return launch_table<tensors_adamw<kAdamSmallCap>>(compact_table<AdamParamsT<kAdamSmallCap>, AdamHead>(p), s, what, true);
+  return launch_table<tensors_adamw<kAdamCap>>(p, s, what, true);
 }
 
 }  // namespace dopt

@@ -18,10 +18,9 @@
 
 namespace dopt {
 
-// Three CTAs per SM and three slots per warp: 16 to 20 KB per slot and CTA,
-// 144 to 180 KB of the SM's shared memory.  Four CTAs (64 registers) were 7 %
-// slower, two slots 5 %; four slots with fp32 grads leave room for two CTAs
-// only (21 % slower).
+// Three CTAs per SM and three slots per warp: 20 KB per slot and CTA, 180 KB of
+// the SM's shared memory.  Four CTAs (64 registers) were 7 % slower, two slots
+// 5 %; four slots leave room for two CTAs only (21 % slower).
 constexpr int kRing8 = 3, kCtas8 = 3;
 static_assert(kMomentBlock == 256 && kAdamTile % kMomentBlock == 0, "one warp per block, 8 elements per lane");
 
@@ -260,9 +259,8 @@ __device__ __forceinline__ const T* at_offset(const T* base, uint32_t elems) {
 // number of resident warps, both of which the update's arithmetic limits.
 // Each lane copies 16-byte pieces (grads, weights, then exp_avg's and
 // exp_avg_sq's codes); each warp waits for its own copies only.
-template <typename GT>
 struct Ring8 {
-  static constexpr int kGrad = kMomentBlock * (int)sizeof(GT), kWeight = kMomentBlock * 4, kCodes = kMomentBlock;
+  static constexpr int kGrad = kMomentBlock * 4, kWeight = kMomentBlock * 4, kCodes = kMomentBlock;  // parts' bytes
   static constexpr int kSlot = kGrad + kWeight + 2 * kCodes;
   static constexpr size_t kBytes = (size_t)kRing8 * (kThreads / 32) * kSlot;
 };
@@ -279,7 +277,7 @@ __device__ __forceinline__ uint32_t piece_at(uint32_t c) { return (c ^ ((c >> 3)
 __device__ __forceinline__ bool through_ring(const AdamSeg& sg, const Place8& a) {
   return sg.shift == 0 && (int)(threadIdx.x / 32 + 1) * kMomentBlock <= a.n;
 }
-template <typename GT, typename P>
+template <typename P>
 __device__ __forceinline__ void fetch_block(const P& p, const Place8& a, uint32_t slot, uint32_t& scales) {
   const AdamSeg& sg = p.seg[a.si];
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -287,20 +285,25 @@ __device__ __forceinline__ void fetch_block(const P& p, const Place8& a, uint32_
     scales = *at_offset(sg.m_scale + a.first / kMomentBlock, warp) |
              ((uint32_t)*at_offset(sg.v_scale + a.first / kMomentBlock, warp) << 8);
   if (!through_ring(sg, a)) return;
-  const char* g = reinterpret_cast<const char*>(static_cast<const GT*>(sg.grad) + a.first);
   const char* w = reinterpret_cast<const char*>(sg.weight + a.first);
+  if (sg.grad_dtype == DOPT_F32) {
+    const char* g = reinterpret_cast<const char*>(static_cast<const float*>(sg.grad) + a.first);
 #pragma unroll
-  for (int k = 0; k < Ring8<GT>::kGrad / 512; ++k) {
-    const uint32_t c = k * 32 + lane;
-    copy16(slot + (sizeof(GT) == 4 ? piece_at(c) : c * 16u), g + warp * Ring8<GT>::kGrad + c * 16u);
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t c = k * 32 + lane;
+      copy16(slot + piece_at(c), g + warp * Ring8::kGrad + c * 16u);
+    }
+  } else {
+    const char* g = reinterpret_cast<const char*>(static_cast<const uint16_t*>(sg.grad) + a.first);
+    copy16(slot + lane * 16u, g + warp * (kMomentBlock * 2) + lane * 16u);
   }
-  slot += Ring8<GT>::kGrad;
+  slot += Ring8::kGrad;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const uint32_t c = k * 32 + lane;
-    copy16(slot + piece_at(c), w + warp * Ring8<GT>::kWeight + c * 16u);
+    copy16(slot + piece_at(c), w + warp * Ring8::kWeight + c * 16u);
   }
-  slot += Ring8<GT>::kWeight;
+  slot += Ring8::kWeight;
   const uint8_t* codes = static_cast<const uint8_t*>(lane < 16 ? sg.m : sg.v) + a.first;
   copy16(slot + lane * 16u, codes + warp * kMomentBlock + (lane & 15u) * 16u);
 }
@@ -324,22 +327,26 @@ __device__ __forceinline__ void shared_floats(uint32_t at, uint32_t lane, float2
   }
 }
 // A lane's eight elements of its warp's slot.
-template <typename GT>
-__device__ __forceinline__ void from_ring(uint32_t slot, uint32_t lane, float2* g, float2* w, uint2& mc, uint2& vc) {
-  if constexpr (sizeof(GT) == 4)
+__device__ __forceinline__ void from_ring(uint32_t slot, uint32_t lane, int grad_dtype, float2* g, float2* w, uint2& mc,
+                                          uint2& vc) {
+  if (grad_dtype == DOPT_F32) {
     shared_floats(slot, lane, g);
-  else
-    Eight<GT>::widen8(shared16(slot + lane * 16u), g);
-  shared_floats(slot + Ring8<GT>::kGrad, lane, w);
-  mc = shared8(slot + Ring8<GT>::kGrad + Ring8<GT>::kWeight + lane * 8u);
-  vc = shared8(slot + Ring8<GT>::kGrad + Ring8<GT>::kWeight + Ring8<GT>::kCodes + lane * 8u);
+  } else {
+    const uint4 r = shared16(slot + lane * 16u);
+    if (grad_dtype == DOPT_BF16)
+      Eight<__nv_bfloat16>::widen8(r, g);
+    else
+      Eight<__half>::widen8(r, g);
+  }
+  shared_floats(slot + Ring8::kGrad, lane, w);
+  mc = shared8(slot + Ring8::kGrad + Ring8::kWeight + lane * 8u);
+  vc = shared8(slot + Ring8::kGrad + Ring8::kWeight + Ring8::kCodes + lane * 8u);
 }
 
 // Updates a warp's block.  key: the hash's argument for the tile's first
 // pair.  Element j of a lane: consecutive ones for a block through the
 // ring; 32 apart (consecutive lanes, consecutive elements) in a tensor's
 // ragged last block, or where the arrays have no common vector boundary.
-template <typename PT, typename GT>
 __device__ __forceinline__ void step_block(const AdamSeg& sg, const Place8& a, uint32_t slot, uint32_t scales,
                                            const Adam8& ad, uint32_t key) {
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -348,14 +355,14 @@ __device__ __forceinline__ void step_block(const AdamSeg& sg, const Place8& a, u
   uint2 mc, vc;
   const uint32_t at = threadIdx.x * 8, loose = warp * kMomentBlock + lane;
   if (ring) {
-    from_ring<GT>(slot, lane, g, w, mc, vc);
+    from_ring(slot, lane, sg.grad_dtype, g, w, mc, vc);
   } else {
     uint32_t mw[2] = {0u, 0u}, vw[2] = {0u, 0u};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint32_t e = loose + j * 32;
       const bool in = (int)e < a.n;
-      elem(g, j) = in ? widen<GT>(static_cast<const GT*>(sg.grad)[a.first + e]) : 0.f;
+      elem(g, j) = in ? load_element(sg.grad, a.first + e, sg.grad_dtype) : 0.f;
       elem(w, j) = in ? sg.weight[a.first + e] : 0.f;
       mw[j / 4] |= (in ? (uint32_t) static_cast<const uint8_t*>(sg.m)[a.first + e] : 0u) << (8 * (j & 3));
       vw[j / 4] |= (in ? (uint32_t) static_cast<const uint8_t*>(sg.v)[a.first + e] : 0u) << (8 * (j & 3));
@@ -368,14 +375,17 @@ __device__ __forceinline__ void step_block(const AdamSeg& sg, const Place8& a, u
   adamw_pairs(ad, both(__fmul_rn(ad.b1.x, m_unit(scales & 0xFFu))), g, w, m, v);
   if (ring) {
     store8(at_offset(sg.weight + a.first, at), w);
-    if constexpr (sizeof(PT) == 2) Eight<PT>::store(at_offset(static_cast<PT*>(sg.param) + a.first, at), w);
+    if (sg.param_dtype == DOPT_BF16)
+      Eight<__nv_bfloat16>::store(at_offset(static_cast<__nv_bfloat16*>(sg.param) + a.first, at), w);
+    else if (sg.param_dtype == DOPT_F16)
+      Eight<__half>::store(at_offset(static_cast<__half*>(sg.param) + a.first, at), w);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint32_t e = loose + j * 32;
       if ((int)e < a.n) {
         sg.weight[a.first + e] = elem(w, j);
-        if constexpr (sizeof(PT) == 2) static_cast<PT*>(sg.param)[a.first + e] = narrow<PT>(elem(w, j));
+        store_param(sg.param, a.first + e, sg.param_dtype, elem(w, j));
       } else {
         elem(m, j) = elem(v, j) = 0.f;  // past the end: no part in the scales (NaN blocks)
       }
@@ -415,12 +425,12 @@ __device__ __forceinline__ void step_block(const AdamSeg& sg, const Place8& a, u
   }
 }
 
-template <typename PT, typename GT, int CAP>
+template <int CAP>
 __global__ void __launch_bounds__(kThreads, kCtas8) tensors_adamw8(const __grid_constant__ AdamParamsT<CAP> p) {
   extern __shared__ uint4 ring[];
   uint32_t slot0;
   asm("{.reg .u64 t; cvta.to.shared.u64 t, %1; cvt.u32.u64 %0, t;}" : "=r"(slot0) : "l"(ring));
-  slot0 += threadIdx.x / 32 * (kRing8 * Ring8<GT>::kSlot);
+  slot0 += threadIdx.x / 32 * (kRing8 * Ring8::kSlot);
   int t = blockIdx.x;
   Place8 cur = {}, ahead;
   uint32_t scales[kRing8];  // of the tiles in flight, this one's first
@@ -434,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, kCtas8) tensors_adamw8(const __grid_
   for (int k = 0; k < kRing8 - 1; ++k) {
     if (ta < p.n_tiles) {
       if (k) ahead = place_tile(p, ta, next_seg(p, ahead.si, ta));
-      fetch_block<GT>(p, ahead, slot0 + k * Ring8<GT>::kSlot, scales[k]);
+      fetch_block(p, ahead, slot0 + k * Ring8::kSlot, scales[k]);
       ta += gridDim.x;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -456,18 +466,18 @@ __global__ void __launch_bounds__(kThreads, kCtas8) tensors_adamw8(const __grid_
   ad.eps = both(fmaxf(p.eps, 0x1p-126f));  // the reciprocal takes subnormals for 0
   ad.decay = both(decay_of_seg(p, p.seg[cur.si]));
   const uint32_t key = p.key + (p.d_step ? (uint32_t)*p.d_step * kHashStep : 0u);
-  uint32_t slot = slot0, slot_ahead = slot0 + (kRing8 - 1) * Ring8<GT>::kSlot;
-  const uint32_t slot_end = slot0 + kRing8 * Ring8<GT>::kSlot;
+  uint32_t slot = slot0, slot_ahead = slot0 + (kRing8 - 1) * Ring8::kSlot;
+  const uint32_t slot_end = slot0 + kRing8 * Ring8::kSlot;
   for (;;) {
     if (ta < p.n_tiles) {
       ahead = place_tile(p, ta, next_seg(p, ahead.si, ta));
-      fetch_block<GT>(p, ahead, slot_ahead, scales[kRing8 - 1]);
+      fetch_block(p, ahead, slot_ahead, scales[kRing8 - 1]);
       ta += gridDim.x;
     }
     asm volatile("cp.async.commit_group;\n cp.async.wait_group %0;" ::"n"(kRing8 - 1) : "memory");
     __syncwarp();  // the warp's copies, not this lane's alone
     if ((int)(threadIdx.x / 32 * kMomentBlock) < cur.n)
-      step_block<PT, GT>(p.seg[cur.si], cur, slot, scales[0], ad,
+      step_block(p.seg[cur.si], cur, slot, scales[0], ad,
                          key + p.seg[cur.si].key + (uint32_t)(cur.first >> 1) * kHashPair);
     t += gridDim.x;
     if (t >= p.n_tiles) break;
@@ -477,27 +487,16 @@ __global__ void __launch_bounds__(kThreads, kCtas8) tensors_adamw8(const __grid_
 #pragma unroll
     for (int k = 0; k + 1 < kRing8; ++k) scales[k] = scales[k + 1];
     slot_ahead = slot;
-    slot = slot + Ring8<GT>::kSlot == slot_end ? slot0 : slot + Ring8<GT>::kSlot;
+    slot = slot + Ring8::kSlot == slot_end ? slot0 : slot + Ring8::kSlot;
     __syncwarp();  // every lane has read the slot before it is filled again
   }
 }
 
-template <typename PT, typename GT>
-int launch_adamw8_t(const AdamParamsT<kAdamCap>& p, cudaStream_t s) {
+int launch_tensors_adamw8(const AdamParamsT<kAdamCap>& p, cudaStream_t s) {
   const char* what = "tensors_adamw8 launch";
-  constexpr size_t kSmem = Ring8<GT>::kBytes;
   if (p.n_seg <= kAdamSmallCap)
-    return launch_table<tensors_adamw8<PT, GT, kAdamSmallCap>, kSmem>(compact_table<AdamParamsT<kAdamSmallCap>, AdamHead>(p), s, what, true);
-  return launch_table<tensors_adamw8<PT, GT, kAdamCap>, kSmem>(p, s, what, true);
-}
-
-int launch_tensors_adamw8(int32_t param_dtype, int32_t grad_dtype, const AdamParamsT<kAdamCap>& p, cudaStream_t s) {
-  const bool f32 = grad_dtype == DOPT_F32;
-  switch (param_dtype) {
-    case DOPT_BF16: return f32 ? launch_adamw8_t<__nv_bfloat16, float>(p, s) : launch_adamw8_t<__nv_bfloat16, __nv_bfloat16>(p, s);
-    case DOPT_F16: return f32 ? launch_adamw8_t<__half, float>(p, s) : launch_adamw8_t<__half, __half>(p, s);
-    default: return launch_adamw8_t<float, float>(p, s);
-  }
+    return launch_table<tensors_adamw8<kAdamSmallCap>, Ring8::kBytes>(compact_table<AdamParamsT<kAdamSmallCap>, AdamHead>(p), s, what, true);
+  return launch_table<tensors_adamw8<kAdamCap>, Ring8::kBytes>(p, s, what, true);
 }
 
 // ------------------------------------------------------- pack and unpack --
