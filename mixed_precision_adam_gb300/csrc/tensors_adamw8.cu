@@ -327,17 +327,12 @@ __device__ __forceinline__ void shared_floats(uint32_t at, uint32_t lane, float2
   }
 }
 // A lane's eight elements of its warp's slot.
-__device__ __forceinline__ void from_ring(uint32_t slot, uint32_t lane, int grad_dtype, float2* g, float2* w, uint2& mc,
-                                          uint2& vc) {
-  if (grad_dtype == DOPT_F32) {
+template <typename GT>
+__device__ __forceinline__ void from_ring(uint32_t slot, uint32_t lane, float2* g, float2* w, uint2& mc, uint2& vc) {
+  if constexpr (sizeof(GT) == 4)
     shared_floats(slot, lane, g);
-  } else {
-    const uint4 r = shared16(slot + lane * 16u);
-    if (grad_dtype == DOPT_BF16)
-      Eight<__nv_bfloat16>::widen8(r, g);
-    else
-      Eight<__half>::widen8(r, g);
-  }
+  else
+    Eight<GT>::widen8(shared16(slot + lane * 16u), g);
   shared_floats(slot + Ring8::kGrad, lane, w);
   mc = shared8(slot + Ring8::kGrad + Ring8::kWeight + lane * 8u);
   vc = shared8(slot + Ring8::kGrad + Ring8::kWeight + Ring8::kCodes + lane * 8u);
@@ -347,6 +342,7 @@ __device__ __forceinline__ void from_ring(uint32_t slot, uint32_t lane, int grad
 // pair.  Element j of a lane: consecutive ones for a block through the
 // ring; 32 apart (consecutive lanes, consecutive elements) in a tensor's
 // ragged last block, or where the arrays have no common vector boundary.
+template <typename PT, typename GT>
 __device__ __forceinline__ void step_block(const AdamSeg& sg, const Place8& a, uint32_t slot, uint32_t scales,
                                            const Adam8& ad, uint32_t key) {
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -355,7 +351,7 @@ __device__ __forceinline__ void step_block(const AdamSeg& sg, const Place8& a, u
   uint2 mc, vc;
   const uint32_t at = threadIdx.x * 8, loose = warp * kMomentBlock + lane;
   if (ring) {
-    from_ring(slot, lane, sg.grad_dtype, g, w, mc, vc);
+    from_ring<GT>(slot, lane, g, w, mc, vc);
   } else {
     uint32_t mw[2] = {0u, 0u}, vw[2] = {0u, 0u};
 #pragma unroll
@@ -375,10 +371,7 @@ __device__ __forceinline__ void step_block(const AdamSeg& sg, const Place8& a, u
   adamw_pairs(ad, both(__fmul_rn(ad.b1.x, m_unit(scales & 0xFFu))), g, w, m, v);
   if (ring) {
     store8(at_offset(sg.weight + a.first, at), w);
-    if (sg.param_dtype == DOPT_BF16)
-      Eight<__nv_bfloat16>::store(at_offset(static_cast<__nv_bfloat16*>(sg.param) + a.first, at), w);
-    else if (sg.param_dtype == DOPT_F16)
-      Eight<__half>::store(at_offset(static_cast<__half*>(sg.param) + a.first, at), w);
+    if constexpr (sizeof(PT) == 2) Eight<PT>::store(at_offset(static_cast<PT*>(sg.param) + a.first, at), w);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -422,6 +415,24 @@ __device__ __forceinline__ void step_block(const AdamSeg& sg, const Place8& a, u
         static_cast<uint8_t*>(sg.v)[a.first + e] = (uint8_t)((j < 4 ? vc.x : vc.y) >> (8 * (j & 3)));
       }
     }
+  }
+}
+
+// The block's update for its tensor's types (the same for the whole CTA).
+__device__ __forceinline__ void step_block_of(const AdamSeg& sg, const Place8& a, uint32_t slot, uint32_t scales,
+                                              const Adam8& ad, uint32_t key) {
+  if (sg.param_dtype == DOPT_BF16) {
+    if (sg.grad_dtype == DOPT_BF16)
+      step_block<__nv_bfloat16, __nv_bfloat16>(sg, a, slot, scales, ad, key);
+    else
+      step_block<__nv_bfloat16, float>(sg, a, slot, scales, ad, key);
+  } else if (sg.param_dtype == DOPT_F16) {
+    if (sg.grad_dtype == DOPT_F16)
+      step_block<__half, __half>(sg, a, slot, scales, ad, key);
+    else
+      step_block<__half, float>(sg, a, slot, scales, ad, key);
+  } else {
+    step_block<float, float>(sg, a, slot, scales, ad, key);
   }
 }
 
@@ -477,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, kCtas8) tensors_adamw8(const __grid_
     asm volatile("cp.async.commit_group;\n cp.async.wait_group %0;" ::"n"(kRing8 - 1) : "memory");
     __syncwarp();  // the warp's copies, not this lane's alone
     if ((int)(threadIdx.x / 32 * kMomentBlock) < cur.n)
-      step_block(p.seg[cur.si], cur, slot, scales[0], ad,
+      step_block_of(p.seg[cur.si], cur, slot, scales[0], ad,
                          key + p.seg[cur.si].key + (uint32_t)(cur.first >> 1) * kHashPair);
     t += gridDim.x;
     if (t >= p.n_tiles) break;
