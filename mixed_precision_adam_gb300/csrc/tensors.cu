@@ -268,12 +268,11 @@ int run_moments(const dopt_moment_tensor* ts, int32_t n, bool pack, cudaStream_t
       if (t.numel == 0 || t.values_dtype != dt || (!t.exp_avg && !t.exp_avg_sq)) continue;
       if (p.n_seg == kMomentCap)
         if (int st = flush()) return st;
-      const size_t elem = dtype_bytes(t.values_dtype);
-      const bool vec = (!t.exp_avg || (aligned_to(t.exp_avg, 8 * elem) && aligned_to(t.exp_avg_codes, 8))) &&
-                       (!t.exp_avg_sq || (aligned_to(t.exp_avg_sq, 8 * elem) && aligned_to(t.exp_avg_sq_codes, 8)));
+      const bool vec = (!t.exp_avg || (aligned_to(t.exp_avg, 32) && aligned_to(t.exp_avg_codes, 16))) &&
+                       (!t.exp_avg_sq || (aligned_to(t.exp_avg_sq, 32) && aligned_to(t.exp_avg_sq_codes, 16)));
       p.seg[p.n_seg++] = MomentSeg{t.exp_avg,          t.exp_avg_sq,    t.exp_avg_codes,    t.exp_avg_sq_codes,
                                    t.exp_avg_scale,    t.exp_avg_sq_scale, t.numel,         p.n_tiles, vec ? 1 : 0};
-      p.n_tiles += (int32_t)tiles_of(t.numel, kAdamTile);
+      p.n_tiles += (int32_t)tiles_of(t.numel, pack ? kAdamTile : kUnpackTile);
     }
     if (int st = flush()) return st;
   }

@@ -99,6 +99,7 @@ struct MomentSeg {
   int32_t tile0;
   int32_t vec;  // 1: every array has the first element on a vector boundary
 };
+constexpr int kUnpackTile = 4096;  // elements per tile (pack: kAdamTile)
 constexpr int kMomentCap = 500, kMomentSmallCap = 60;
 template <int CAP>
 struct MomentParamsT {
