@@ -646,7 +646,8 @@ int dopt_state_from_model(const dopt_shard_map* map, int32_t buffer, int32_t ran
  * call's work on the stream has run).  Every array of a tensor is contiguous
  * and has `numel` elements; it needs only its own elements' alignment (4
  * bytes for fp32, 2 for bf16/fp16, 1 for codes) -- a tensor whose arrays
- * all start on 32-byte boundaries takes the vector path.  Arrays of one
+ * start at one element offset from 16-byte boundaries (fp32 moments), or on
+ * 32-byte boundaries (8-bit moments), is read in vectors, others by element.  Arrays of one
  * call must not overlap, but for the list's read-only grads.
  *
  * Moments are held in fp32, or in 8 bits per element (DOPT_MOMENTS_8BIT,
@@ -720,8 +721,8 @@ size_t dopt_tensors_workspace_bytes(int32_t n_tensors);
  *                  < 1, else 1;
  *   *d_found_inf = 1 if any g is non-finite.
  * Any of the three may be NULL.  Only grad, grad_dtype and numel of the
- * tensors are used.  Squares are added in fp32 over 8 or 16 elements of a
- * thread, then in fp64 in a fixed order: the same list gives the same bits
+ * tensors are used.  Squares are added in fp32 over 16 elements, those
+ * sums with their rounding errors in fp32, then in fp64, in a fixed order: the same list gives the same bits
  * on the same kind of GPU.  Elements whose squares would leave the fp32 range
  * are squared in fp64.  dopt_read_step_stats reads the statistics (with
  * the count of zero grads) from the workspace.
@@ -732,12 +733,14 @@ int dopt_tensors_grad_norm(const dopt_tensor* tensors, int32_t n_tensors, float 
                            float* d_clip_coef, int32_t* d_found_inf, dopt_stream stream);
 
 /*
- * AdamW over a list of tensors: per element the arithmetic of
- * dopt_adam_step (each operation rounded once in fp32), with
- *   g = (fp32(grad) * inv_loss_scale) * (*d_clip_coef)
- * and, for 8-bit moments, the stored values widened before the update and
- * the new ones rounded to codes after it (the weight is stepped with the
- * new moments before that rounding).  `seed` is the stochastic rounding's.
+ * AdamW over a list of tensors, with
+ *   g = (fp32(grad) * inv_loss_scale) * (*d_clip_coef).
+ * fp32 moments: per element the arithmetic of dopt_adam_step, bit for bit.
+ * 8-bit moments: the same formulas in fp32, on the stored values widened;
+ * the new moments step the weight and are then rounded to codes.  There b1 m
+ * + (1-b1) g and b2 v + (1-b2) g^2 are fused multiply-adds, and the root and
+ * the division of the weight's update are approximate (a few fp32 ulps of
+ * the update).  `seed` is the stochastic rounding's.
  * d_clip_coef NULL: 1.  If d_found_inf is given and *d_found_inf is nonzero,
  * nothing is written.
  */

@@ -204,8 +204,9 @@ def _check(status):
 def _ptr(x):
     if x is None:
         return None
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
+    get = getattr(x, "data_ptr", None)
+    if get is not None:
+        return get()
     if hasattr(x, "__array_interface__"):  # numpy array (host memory)
         return x.__array_interface__["data"][0]
     return int(x)
@@ -214,9 +215,8 @@ def _ptr(x):
 def _stream(s):
     if s is None:
         return None
-    if hasattr(s, "cuda_stream"):
-        return s.cuda_stream
-    return int(s)
+    handle = getattr(s, "cuda_stream", None)
+    return int(s) if handle is None else handle
 
 
 def _ptr_array(xs):
@@ -561,24 +561,43 @@ def dopt_loss_scaler_update(s, found_inf):
     return s.scale
 
 
-def _array(entry, name, numel, dtypes, where):
-    """(pointer, numel, dtype name) of a list entry's array: a pointer, or a
-    torch tensor, which must be contiguous, of one of `dtypes` (torch dtype
-    names) and of `numel` elements (None: any)."""
-    x = entry.get(name)
-    if x is None or not hasattr(x, "data_ptr"):
-        return _ptr(x), numel, None
-    dt = str(x.dtype).replace("torch.", "")
-    if not x.is_contiguous():
-        raise DoptError(E_INVALID, f"{where}: {name} is not contiguous")
-    if dt not in dtypes:
-        raise DoptError(E_INVALID, f"{where}: {name} is {dt}, not {' or '.join(dtypes)}")
-    if numel is not None and x.numel() != numel:
-        raise DoptError(E_INVALID, f"{where}: {name} has {x.numel()} elements, not {numel}")
-    return x.data_ptr(), x.numel(), dt
-
-
 _DTYPE = {"float32": F32, "bfloat16": BF16, "float16": F16}
+_VALUES, _CODES, _EITHER = ("float32", "bfloat16"), ("uint8",), ("float32", "uint8")
+_dtype_names = {}  # torch dtype -> its name without "torch."
+
+
+def _array(entry, name, numel, dtypes, k, devices):
+    """(pointer, numel, dtype name) of an array of list entry k: a pointer,
+    or a torch tensor, which must be contiguous, of one of `dtypes` (torch
+    dtype names) and of `numel` elements (None: any); its device is added to
+    `devices`."""
+    x = entry.get(name)
+    get = getattr(x, "data_ptr", None)
+    if get is None:
+        if hasattr(x, "__array_interface__"):
+            raise DoptError(E_INVALID, f"tensor {k}: {name} is a host array")
+        return _ptr(x), numel, None
+    dt = _dtype_names.get(x.dtype)
+    if dt is None:
+        dt = _dtype_names[x.dtype] = str(x.dtype).replace("torch.", "")
+    n = x.numel()
+    if not x.is_contiguous():
+        raise DoptError(E_INVALID, f"tensor {k}: {name} is not contiguous")
+    if dt not in dtypes:
+        raise DoptError(E_INVALID, f"tensor {k}: {name} is {dt}, not {' or '.join(dtypes)}")
+    if numel is not None and n != numel:
+        raise DoptError(E_INVALID, f"tensor {k}: {name} has {n} elements, not {numel}")
+    if n:
+        devices.add(x.get_device())
+    return get(), n, dt
+
+
+def _listed(lst):
+    """The C arguments of a list whose tensors are on one GPU (pointers are
+    taken as they are)."""
+    if -1 in lst.devices or len(lst.devices) > 1:
+        raise DoptError(E_INVALID, "a list's tensors must be on one GPU")
+    return lst.c, lst.n
 
 
 class TensorList:
@@ -595,43 +614,48 @@ class TensorList:
         self.n = len(entries)
         self.c = (dopt_tensor * max(1, self.n))()
         self._keep = [dict(e) for e in entries]
+        self.devices = d = set()
         for k, e in enumerate(entries):
-            where = f"tensor {k}"
             t = self.c[k]
-            param, n, pdt = _array(e, "param", e.get("numel"), _DTYPE, where)
-            t.grad, n, gdt = _array(e, "grad", n, _DTYPE, where)
+            param, n, pdt = _array(e, "param", e.get("numel"), _DTYPE, k, d)
+            t.grad, n, gdt = _array(e, "grad", n, _DTYPE, k, d)
             if n is None:
-                raise DoptError(E_INVALID, f"{where}: numel is not given")
+                raise DoptError(E_INVALID, f"tensor {k}: numel is not given")
             t.numel, t.param = int(n), param
             t.grad_dtype = _DTYPE[gdt] if gdt else int(e.get("grad_dtype", F32))
             t.param_dtype = _DTYPE[pdt] if pdt else int(e.get("param_dtype", t.grad_dtype))
-            t.master = _array(e, "master", n, ("float32",), where)[0]
-            t.exp_avg, _, mdt = _array(e, "exp_avg", n, ("float32", "uint8"), where)
-            t.exp_avg_sq, _, vdt = _array(e, "exp_avg_sq", n, ("float32", "uint8"), where)
+            t.master = _array(e, "master", n, ("float32",), k, d)[0]
+            t.exp_avg, _, mdt = _array(e, "exp_avg", n, _EITHER, k, d)
+            t.exp_avg_sq, _, vdt = _array(e, "exp_avg_sq", n, _EITHER, k, d)
             if mdt != vdt:
-                raise DoptError(E_INVALID, f"{where}: exp_avg and exp_avg_sq differ in format")
+                raise DoptError(E_INVALID, f"tensor {k}: exp_avg and exp_avg_sq differ in format")
             eight = e.get("exp_avg_scale") is not None
             if mdt and (mdt == "uint8") != eight:
-                raise DoptError(E_INVALID, f"{where}: uint8 moments, and only they, come with scales")
-            t.moments = int(e.get("moments", MOMENTS_8BIT if eight else MOMENTS_F32))
+                raise DoptError(E_INVALID, f"tensor {k}: uint8 moments, and only they, come with scales")
+            t.moments = MOMENTS_8BIT if eight else MOMENTS_F32
+            if e.get("moments") is not None:
+                if mdt and int(e["moments"]) != t.moments:
+                    raise DoptError(E_INVALID, f"tensor {k}: moments are {mdt}")
+                t.moments = int(e["moments"])
             blocks = dopt_moment_blocks(max(0, t.numel))
-            t.exp_avg_scale = _array(e, "exp_avg_scale", blocks, ("uint8",), where)[0]
-            t.exp_avg_sq_scale = _array(e, "exp_avg_sq_scale", blocks, ("uint8",), where)[0]
+            t.exp_avg_scale = _array(e, "exp_avg_scale", blocks, _CODES, k, d)[0]
+            t.exp_avg_sq_scale = _array(e, "exp_avg_sq_scale", blocks, _CODES, k, d)[0]
             t.wd_mult = float(e.get("wd_mult", 1.0))
 
     def set_grads(self, grads):
         """Points the tensors at other grads (same sizes and dtypes)."""
         if len(grads) != self.n:
             raise DoptError(E_INVALID, f"{len(grads)} grads for {self.n} tensors")
-        ptrs = []
+        ptrs, d = [], set()
         for k, g in enumerate(grads):
-            ptr, _, dt = _array(dict(grad=g), "grad", self.c[k].numel, _DTYPE, f"tensor {k}")
+            ptr, _, dt = _array(dict(grad=g), "grad", self.c[k].numel, _DTYPE, k, d)
             if dt and _DTYPE[dt] != self.c[k].grad_dtype:
                 raise DoptError(E_INVALID, f"tensor {k}: grad is {dt}, unlike before")
             ptrs.append(ptr)
         for k, (g, ptr) in enumerate(zip(grads, ptrs)):
             self.c[k].grad = ptr
             self._keep[k]["grad"] = g
+        self.devices |= d
 
 
 class MomentList:
@@ -645,22 +669,21 @@ class MomentList:
         self.n = len(entries)
         self.c = (dopt_moment_tensor * max(1, self.n))()
         self._keep = [dict(e) for e in entries]
-        values = ("float32", "bfloat16")
+        self.devices = d = set()
         for k, e in enumerate(entries):
-            where = f"tensor {k}"
             t = self.c[k]
-            t.exp_avg, n, mdt = _array(e, "exp_avg", e.get("numel"), values, where)
-            t.exp_avg_sq, n, vdt = _array(e, "exp_avg_sq", n, values, where)
+            t.exp_avg, n, mdt = _array(e, "exp_avg", e.get("numel"), _VALUES, k, d)
+            t.exp_avg_sq, n, vdt = _array(e, "exp_avg_sq", n, _VALUES, k, d)
             if n is None:
-                raise DoptError(E_INVALID, f"{where}: numel is not given")
+                raise DoptError(E_INVALID, f"tensor {k}: numel is not given")
             if mdt and vdt and mdt != vdt:
-                raise DoptError(E_INVALID, f"{where}: exp_avg and exp_avg_sq differ in dtype")
+                raise DoptError(E_INVALID, f"tensor {k}: exp_avg and exp_avg_sq differ in dtype")
             t.numel = int(n)
             t.values_dtype = _DTYPE[mdt or vdt] if mdt or vdt else int(e.get("values_dtype", F32))
             blocks = dopt_moment_blocks(max(0, t.numel))
             for name in ("exp_avg", "exp_avg_sq"):
-                setattr(t, name + "_codes", _array(e, name + "_codes", t.numel, ("uint8",), where)[0])
-                setattr(t, name + "_scale", _array(e, name + "_scale", blocks, ("uint8",), where)[0])
+                setattr(t, name + "_codes", _array(e, name + "_codes", t.numel, _CODES, k, d)[0])
+                setattr(t, name + "_scale", _array(e, name + "_scale", blocks, _CODES, k, d)[0])
 
 
 def dopt_moment_blocks(numel):
@@ -679,7 +702,7 @@ def dopt_tensors_grad_norm(tensors, inv_loss_scale, max_norm, workspace, workspa
                            d_clip_coef, d_found_inf, stream=None):
     """Grad norm, clip coefficient and non-finite flag (device scalars) of a
     TensorList."""
-    _check(_c["dopt_tensors_grad_norm"](tensors.c, tensors.n, inv_loss_scale, max_norm, _ptr(workspace),
+    _check(_c["dopt_tensors_grad_norm"](*_listed(tensors), inv_loss_scale, max_norm, _ptr(workspace),
                                         workspace_bytes, _ptr(d_norm), _ptr(d_clip_coef), _ptr(d_found_inf),
                                         _stream(stream)))
 
@@ -688,7 +711,7 @@ def dopt_tensors_adam_step(tensors, hp, step, inv_loss_scale=1.0, seed=0, d_clip
                            d_found_inf=None, stream=None):
     """AdamW over a TensorList; seed: of the 8-bit second moments' rounding."""
     h = _hparams(hp, step)
-    _check(_c["dopt_tensors_adam_step"](tensors.c, tensors.n, ctypes.byref(h), inv_loss_scale,
+    _check(_c["dopt_tensors_adam_step"](*_listed(tensors), ctypes.byref(h), inv_loss_scale,
                                         seed & 0xFFFFFFFF, _ptr(d_clip_coef), _ptr(d_found_inf),
                                         _stream(stream)))
 
@@ -697,19 +720,19 @@ def dopt_tensors_step(tensors, hp, step, workspace, workspace_bytes, *, inv_loss
                       seed=0, d_step=None, d_lr=None, d_found_inf=None, d_norm=None, stream=None):
     """Grad norm, clip, skip and AdamW over a TensorList, without waiting."""
     h = _hparams(hp, step)
-    _check(_c["dopt_tensors_step"](tensors.c, tensors.n, ctypes.byref(h), inv_loss_scale, max_norm,
+    _check(_c["dopt_tensors_step"](*_listed(tensors), ctypes.byref(h), inv_loss_scale, max_norm,
                                    seed & 0xFFFFFFFF, _ptr(d_step), _ptr(d_lr), _ptr(workspace),
                                    workspace_bytes, _ptr(d_found_inf), _ptr(d_norm), _stream(stream)))
 
 
 def dopt_state8_pack(moments, stream=None):
     """The values of a MomentList into its 8-bit codes and scales."""
-    _check(_c["dopt_state8_pack"](moments.c, moments.n, _stream(stream)))
+    _check(_c["dopt_state8_pack"](*_listed(moments), _stream(stream)))
 
 
 def dopt_state8_unpack(moments, stream=None):
     """The codes and scales of a MomentList into its values."""
-    _check(_c["dopt_state8_unpack"](moments.c, moments.n, _stream(stream)))
+    _check(_c["dopt_state8_unpack"](*_listed(moments), _stream(stream)))
 
 
 def exported_symbols():

@@ -219,9 +219,11 @@ int64_t replica_extent(const dopt_shard_map* m, int32_t buffer, int32_t rank, bo
   return full ? m->buffers[buffer].numel : shard_extent(m, buffer, rank);
 }
 
+}  // namespace
+
 #if DOPT_BOUNDS_CHECK
 // Device address of g_bounds_record on the current device.
-int bounds_record(unsigned long long** out) {
+int dopt::bounds_record(unsigned long long** out) {
   static std::mutex mu;
   static unsigned long long* addr[64] = {};
   int dev = 0;
@@ -238,6 +240,8 @@ int bounds_record(unsigned long long** out) {
   return DOPT_OK;
 }
 #endif
+
+namespace {
 
 // Launches K1 over every chunk of a run list; with stats, chunk i writes its
 // partials to workspace region region_first + i.

@@ -204,10 +204,12 @@ struct Extents {
 // Where a range is checked, as recorded.
 enum BoundsSite : int {
   kSiteK1Rep = 1, kSiteK1Main = 2, kSiteK1Bucket = 3, kSiteTmaCopy = 4,
-  kSiteK3Main = 5, kSiteK3State = 6, kSiteK3Master = 7, kSiteK3Param = 8
+  kSiteK3Main = 5, kSiteK3State = 6, kSiteK3Master = 7, kSiteK3Param = 8,
+  kSiteListNorm = 9, kSiteListAdam = 10, kSiteListAdam8 = 11, kSiteListMoments = 12
 };
 
 #if DOPT_BOUNDS_CHECK
+int bounds_record(unsigned long long** out);  // device address of the record on the current device
 __device__ __forceinline__ bool range_ok(const Extents& x, int site, int64_t lo, int64_t n, int64_t extent) {
   if (lo >= 0 && n >= 0 && lo + n <= extent) return true;
   if (atomicAdd(x.record, 1ull) == 0ull) {

@@ -107,10 +107,22 @@ int check_norm_args(int32_t n, float inv_scale, double max_norm, const void* ws,
 
 char* ws_at(void* ws, size_t offset) { return static_cast<char*>(ws) + offset; }
 
+// A table's record of tiles outside their tensor (debug builds).
+template <typename P>
+int set_record(P& p) {
+#if DOPT_BOUNDS_CHECK
+  return bounds_record(&p.record);
+#else
+  (void)p;
+  return DOPT_OK;
+#endif
+}
+
 // The norm launches of a list, then the finalize.
 int run_norm(const dopt_tensor* ts, int32_t n, float inv_scale, FinalizeArgs fin, void* ws, cudaStream_t s) {
   Partial* parts = reinterpret_cast<Partial*>(ws_at(ws, kScalarBytes));
   NormParamsT<kNormCap> p;
+  if (int st = set_record(p)) return st;
   p.inv_scale = inv_scale;
   p.n_seg = p.n_tiles = 0;
   fin.parts = parts;
@@ -169,6 +181,7 @@ struct AdamJob {
 int run_adamw(const dopt_tensor* ts, int32_t n, const AdamJob& j, cudaStream_t s) {
   const dopt_adamw_hparams* hp = j.hp;
   AdamParamsT<kAdamCap> p;
+  if (int st = set_record(p)) return st;
   p.coef = j.coef;
   p.found_inf = j.found;
   p.dev = j.dev;
@@ -255,6 +268,7 @@ int check_moments(const dopt_moment_tensor* ts, int32_t n, const char* fn) {
 
 int run_moments(const dopt_moment_tensor* ts, int32_t n, bool pack, cudaStream_t s) {
   MomentParamsT<kMomentCap> p;
+  if (int st = set_record(p)) return st;
   for (int32_t dt : {DOPT_F32, DOPT_BF16}) {
     p.n_seg = p.n_tiles = 0;
     auto flush = [&]() -> int {

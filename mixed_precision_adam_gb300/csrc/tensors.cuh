@@ -27,10 +27,27 @@ struct NormSeg {
 constexpr int kNormCap = 1280, kNormSmallCap = 64;
 constexpr int kNormVector = 32;  // bytes: the grid tiles are cut on
 
+// Debug builds (DOPT_BOUNDS_CHECK=1): every table carries the address of the
+// record of tiles found outside their tensor (the first element at or past
+// its end, or more elements than it has left); such a tile is skipped.
+#if DOPT_BOUNDS_CHECK
+#define DOPT_LIST_RECORD unsigned long long* record;
+#define DOPT_TILE_OK(p, site, lo, n, len) (::dopt::tile_ok((p).record, (site), (lo), (n), (len)))
+__device__ __forceinline__ bool tile_ok(unsigned long long* record, int site, int64_t lo, int64_t n, int64_t len) {
+  Extents x{};
+  x.record = record;
+  return range_ok(x, site, lo, n > 0 ? n : len + 1, len);  // a tile without elements has no place in a table
+}
+#else
+#define DOPT_LIST_RECORD
+#define DOPT_TILE_OK(p, site, lo, n, len) true
+#endif
+
 struct NormHead {
   Partial* partials;      // one slot per CTA of this launch
   float inv_scale;
   int32_t n_seg, n_tiles;
+  DOPT_LIST_RECORD
 };
 struct FinalizeParams {
   FinalizeArgs fin;
@@ -79,6 +96,7 @@ struct AdamHead {
   uint32_t key;    // seed (+ the step's term, unless d_step)
   int32_t early;   // 1: this launch follows a kernel of the same call that writes none of its state
   int32_t n_seg, n_tiles;
+  DOPT_LIST_RECORD
 };
 template <int CAP>
 struct AdamParamsT : AdamHead {
@@ -101,9 +119,12 @@ struct MomentSeg {
 };
 constexpr int kUnpackTile = 4096;  // elements per tile (pack: kAdamTile)
 constexpr int kMomentCap = 500, kMomentSmallCap = 60;
-template <int CAP>
-struct MomentParamsT {
+struct MomentHead {
   int32_t n_seg, n_tiles;
+  DOPT_LIST_RECORD
+};
+template <int CAP>
+struct MomentParamsT : MomentHead {
   MomentSeg seg[CAP];
 };
 static_assert(sizeof(MomentParamsT<kMomentCap>) <= 32764, "kernel parameter limit");

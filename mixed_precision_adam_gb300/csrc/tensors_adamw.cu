@@ -55,6 +55,10 @@ __device__ __forceinline__ void place_part(const P& p, int t, int si, AdamPart& 
   a.first = (int64_t)(t - sg.tile0) * kAdamTile32 - max(sg.shift, 0);
   a.e = a.first + threadIdx.x * 4;
   a.full = sg.shift >= 0 && a.e >= 0 && a.e + 4 <= sg.len;
+  if (!DOPT_TILE_OK(p, kSiteListAdam, a.first + max(sg.shift, 0), 1, sg.len + max(sg.shift, 0))) {
+    a.e = a.first = sg.len;  // no elements
+    a.full = false;
+  }
 }
 template <typename P>
 __device__ __forceinline__ void load_state(const P& p, AdamPart& a) {

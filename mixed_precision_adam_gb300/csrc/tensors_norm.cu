@@ -168,6 +168,9 @@ __global__ void __launch_bounds__(kThreads, kNormCtas) tensors_norm(const __grid
   for (int t = blockIdx.x; t < p.n_tiles; t += gridDim.x) {
     si = next_seg(p, si, t);
     const NormSeg& sg = p.seg[si];
+    if (!DOPT_TILE_OK(p, kSiteListNorm, (int64_t)(t - sg.tile0) * (kNormTileBytes / (sg.dtype == DOPT_F32 ? 4 : 2)), 1,
+                      sg.len + sg.shift))
+      continue;
     if (sg.dtype == DOPT_F32)
       norm_tile<float>(sg, t, inv, acc);
     else if (sg.dtype == DOPT_BF16)

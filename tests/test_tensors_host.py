@@ -145,6 +145,25 @@ def test_the_binding_refuses_what_the_pointers_would_hide():
         refused(dopt.E_INVALID, lambda: dopt.MomentList([bad]))
 
 
+def test_the_binding_refuses_host_memory():
+    """Lists may be made of CPU tensors, but no kernel gets their addresses."""
+    ok = dict(param=torch.zeros(24), grad=torch.zeros(24), exp_avg=torch.zeros(24), exp_avg_sq=torch.zeros(24))
+    lst = dopt.TensorList([ok])
+    ws = dopt.dopt_tensors_workspace_bytes(1)
+    for call in (lambda: dopt.dopt_tensors_adam_step(lst, HP, 1), lambda: dopt.dopt_tensors_step(lst, HP, 1, 4096, ws),
+                 lambda: dopt.dopt_tensors_grad_norm(lst, 1.0, 1.0, 4096, ws, None, None, None)):
+        refused(dopt.E_INVALID, call)
+    m = dict(exp_avg=torch.zeros(24), exp_avg_codes=torch.zeros(24, dtype=torch.uint8),
+             exp_avg_scale=torch.zeros(1, dtype=torch.uint8))
+    for fn in (dopt.dopt_state8_pack, dopt.dopt_state8_unpack):
+        refused(dopt.E_INVALID, lambda: fn(dopt.MomentList([m])))
+    refused(dopt.E_INVALID, lambda: dopt.TensorList([dict(ok, grad=np.zeros(24, np.float32))]))
+    lst = dopt.TensorList([entry()])
+    lst.set_grads([torch.zeros(1000, dtype=torch.bfloat16)])
+    refused(dopt.E_INVALID, lambda: dopt.dopt_tensors_adam_step(lst, HP, 1))
+    refused(dopt.E_INVALID, lambda: dopt.TensorList([dict(ok, moments=dopt.MOMENTS_8BIT)]))
+
+
 # -------------------------------------------------- the 64-bit restatement --
 
 def test_e4m3_values_are_torchs():
