@@ -133,10 +133,10 @@ static_assert(sizeof(MomentParamsT<kMomentCap>) <= 32764, "kernel parameter limi
 constexpr uint32_t kHashPair = 0x9E3779B9u, kHashTensor = 0x510E527Fu, kHashStep = 0x6A09E667u;
 constexpr uint32_t kHashMul1 = 0xBB67AE85u, kHashMul2 = 0xA54FF53Bu;
 
-// The tensor holding tile t, by bisection (a CTA's first tile).
+// The tensor holding tile t, from tensor lo on, by bisection.
 template <typename P>
-__device__ __forceinline__ int find_seg(const P& p, int t) {
-  int lo = 0, hi = p.n_seg - 1;
+__device__ __forceinline__ int find_seg(const P& p, int t, int lo = 0) {
+  int hi = p.n_seg - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (p.seg[mid].tile0 <= t)
@@ -146,11 +146,14 @@ __device__ __forceinline__ int find_seg(const P& p, int t) {
   }
   return lo;
 }
-// The same for a later tile, from the one before.
+// The same for a later tile, from the one before: mostly the same tensor or the
+// next one; among many small tensors it may be hundreds further on.
 template <typename P>
 __device__ __forceinline__ int next_seg(const P& p, int si, int t) {
-  while (si + 1 < p.n_seg && p.seg[si + 1].tile0 <= t) ++si;
-  return si;
+  if (si + 1 >= p.n_seg || p.seg[si + 1].tile0 > t) return si;
+  ++si;
+  if (si + 1 >= p.n_seg || p.seg[si + 1].tile0 > t) return si;
+  return find_seg(p, t, si + 1);
 }
 
 // ------------------------------------------------------- elements by type --

@@ -138,6 +138,10 @@ __device__ __forceinline__ void norm_tile(const NormSeg& sg, int t, float2 inv, 
       const int64_t e = first + (int64_t)(u * kThreads + threadIdx.x) * kPer;
       if (e >= 0 && e + kPer <= sg.len) {
         load32(g + e, r + 8 * u);
+      } else if (e >= sg.len) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[8 * u + j] = 0u;
+        acc.zeros -= kPer;
       } else {
         alignas(16) GT x[kPer];
         uint32_t* w = reinterpret_cast<uint32_t*>(x);
