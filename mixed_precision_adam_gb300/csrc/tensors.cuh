@@ -133,10 +133,9 @@ static_assert(sizeof(MomentParamsT<kMomentCap>) <= 32764, "kernel parameter limi
 constexpr uint32_t kHashPair = 0x9E3779B9u, kHashTensor = 0x510E527Fu, kHashStep = 0x6A09E667u;
 constexpr uint32_t kHashMul1 = 0xBB67AE85u, kHashMul2 = 0xA54FF53Bu;
 
-// The tensor holding tile t, from tensor lo on, by bisection.
+// The tensor holding tile t among lo .. hi, by bisection.
 template <typename P>
-__device__ __forceinline__ int find_seg(const P& p, int t, int lo = 0) {
-  int hi = p.n_seg - 1;
+__device__ __forceinline__ int find_seg(const P& p, int t, int lo, int hi) {
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (p.seg[mid].tile0 <= t)
@@ -146,14 +145,31 @@ __device__ __forceinline__ int find_seg(const P& p, int t, int lo = 0) {
   }
   return lo;
 }
-// The same for a later tile, from the one before: mostly the same tensor or the
-// next one; among many small tensors it may be hundreds further on.
 template <typename P>
-__device__ __forceinline__ int next_seg(const P& p, int si, int t) {
+__device__ __forceinline__ int find_seg(const P& p, int t) {
+  return find_seg(p, t, 0, p.n_seg - 1);
+}
+// The same for a CTA's later tile, from the one before: in a large tensor the
+// same one; among small tensors as many further on as the last time, nearly.
+// `hop` keeps that number.  (Each entry read is a dependent load of the
+// parameters: with plain bisections 1000 tensors of 50,000 elements took
+// 193 us with 8-bit moments against 140, 253 with fp32 against 225.)
+template <typename P>
+__device__ __forceinline__ int next_seg(const P& p, int si, int t, int& hop) {
   if (si + 1 >= p.n_seg || p.seg[si + 1].tile0 > t) return si;
-  ++si;
-  if (si + 1 >= p.n_seg || p.seg[si + 1].tile0 > t) return si;
-  return find_seg(p, t, si + 1);
+  const int guess = min(si + max(hop, 1), p.n_seg - 1);
+  int found;
+  if (p.seg[guess].tile0 <= t) {
+    found = guess;
+    if (guess + 1 < p.n_seg && p.seg[guess + 1].tile0 <= t) {
+      found = guess + 1;
+      if (guess + 2 < p.n_seg && p.seg[guess + 2].tile0 <= t) found = find_seg(p, t, guess + 2, p.n_seg - 1);
+    }
+  } else {
+    found = p.seg[guess - 1].tile0 <= t ? guess - 1 : find_seg(p, t, si + 1, guess - 1);
+  }
+  hop = found - si;
+  return found;
 }
 
 // ------------------------------------------------------- elements by type --

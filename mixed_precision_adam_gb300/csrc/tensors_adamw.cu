@@ -85,6 +85,7 @@ template <int CAP>
 __global__ void __launch_bounds__(kThreads, 4) tensors_adamw(const __grid_constant__ AdamParamsT<CAP> p) {
   int t = blockIdx.x;
   const bool work = t < p.n_tiles;
+  int hop = 1;
   AdamPart cur;
   if (work) {
     place_part(p, t, find_seg(p, t), cur);
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 4) tensors_adamw(const __grid_consta
     const int tn = t + (int)gridDim.x;
     const bool more = tn < p.n_tiles;
     if (more) {
-      place_part(p, tn, next_seg(p, cur.si, tn), nxt);
+      place_part(p, tn, next_seg(p, cur.si, tn, hop), nxt);
       load_grad(p, nxt);
       load_state(p, nxt);
       nxt.decay = nxt.si == cur.si ? cur.decay : decay_of_seg(p, p.seg[nxt.si]);

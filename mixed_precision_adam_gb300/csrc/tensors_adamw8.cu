@@ -10,8 +10,8 @@
 // elements per instruction, codes are made two at a time, and the inputs
 // come through a ring in shared memory.  A warp has a block of 256 elements
 // at a time, so a block's largest moments are one warp reduction each.
-// Measured on 1.35e9 bf16 elements: 3325 us, 6.48 TB/s (0.96 of the copy
-// bandwidth); fp32 params and grads 6.59 TB/s.
+// Measured on 1.35e9 bf16 elements: 3278 us, 6.57 TB/s (0.97 of the copy
+// bandwidth); 3.1e8 fp32 params and grads: 757 us, 6.51 TB/s.
 #include <cuda_fp8.h>
 
 #include "tensors.cuh"
@@ -448,6 +448,8 @@ __global__ void __launch_bounds__(kThreads, kCtas8) tensors_adamw8(const __grid_
   int t = blockIdx.x;
   Place8 cur = {}, ahead;
   uint32_t scales[kRing8];  // of the tiles in flight, this one's first
+  int tensor[kRing8];
+  int hop = 1;
   if (!p.early) wait_for_prior_grids();
   // the first kRing8 - 1 tiles; the launch before this one, when it is of
   // the same call, writes none of what they read
@@ -457,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, kCtas8) tensors_adamw8(const __grid_
 #pragma unroll
   for (int k = 0; k < kRing8 - 1; ++k) {
     if (ta < p.n_tiles) {
-      if (k) ahead = place_tile(p, ta, next_seg(p, ahead.si, ta));
+      if (k) ahead = place_tile(p, ta, next_seg(p, ahead.si, ta, hop));
+      tensor[k] = ahead.si;
       fetch_block(p, ahead, slot0 + k * Ring8::kSlot, scales[k]);
       ta += gridDim.x;
     }
@@ -484,7 +487,8 @@ __global__ void __launch_bounds__(kThreads, kCtas8) tensors_adamw8(const __grid_
   const uint32_t slot_end = slot0 + kRing8 * Ring8::kSlot;
   for (;;) {
     if (ta < p.n_tiles) {
-      ahead = place_tile(p, ta, next_seg(p, ahead.si, ta));
+      ahead = place_tile(p, ta, next_seg(p, ahead.si, ta, hop));
+      tensor[kRing8 - 1] = ahead.si;
       fetch_block(p, ahead, slot_ahead, scales[kRing8 - 1]);
       ta += gridDim.x;
     }
@@ -495,11 +499,14 @@ __global__ void __launch_bounds__(kThreads, kCtas8) tensors_adamw8(const __grid_
                          key + p.seg[cur.si].key + (uint32_t)(cur.first >> 1) * kHashPair);
     t += gridDim.x;
     if (t >= p.n_tiles) break;
-    const Place8 next = place_tile(p, t, next_seg(p, cur.si, t));
+    const Place8 next = place_tile(p, t, tensor[1]);
     if (next.si != cur.si) ad.decay = both(decay_of_seg(p, p.seg[next.si]));
     cur = next;
 #pragma unroll
-    for (int k = 0; k + 1 < kRing8; ++k) scales[k] = scales[k + 1];
+    for (int k = 0; k + 1 < kRing8; ++k) {
+      scales[k] = scales[k + 1];
+      tensor[k] = tensor[k + 1];
+    }
     slot_ahead = slot;
     slot = slot + Ring8::kSlot == slot_end ? slot0 : slot + Ring8::kSlot;
     __syncwarp();  // every lane has read the slot before it is filled again
@@ -550,9 +557,9 @@ __device__ __forceinline__ void store_codes(uint8_t* x, bool vec, int lane, int 
 // elements of the block, the tensor's vector flag).
 template <int CAP, typename F>
 __device__ __forceinline__ void each_block(const MomentParamsT<CAP>& p, F&& f) {
-  int si = -1;
+  int si = -1, hop = 1;
   for (int t = blockIdx.x; t < p.n_tiles; t += gridDim.x) {
-    si = si < 0 ? find_seg(p, t) : next_seg(p, si, t);
+    si = si < 0 ? find_seg(p, t) : next_seg(p, si, t, hop);
     const MomentSeg& sg = p.seg[si];
     if (!DOPT_TILE_OK(p, kSiteListMoments, (int64_t)(t - sg.tile0) * kAdamTile, 1, sg.len)) continue;
     const int64_t off = (int64_t)(t - sg.tile0) * kAdamTile + (threadIdx.x / 32) * kMomentBlock;
@@ -661,6 +668,7 @@ __global__ void __launch_bounds__(kThreads, 4) state8_unpack(const __grid_consta
   static_assert(kUnpackTile == kThreads * 16 && kMomentBlock % 16 == 0, "sixteen elements per thread");
   int t = blockIdx.x;
   if (t >= p.n_tiles) return;
+  int hop = 1;
   UnpackPlace cur = place_codes(p, t, find_seg(p, t));
   Codes16 c;
   load_codes16(p, cur, c);
@@ -670,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 4) state8_unpack(const __grid_consta
     UnpackPlace next = cur;
     Codes16 d;
     if (more) {
-      next = place_codes(p, t, next_seg(p, cur.si, t));
+      next = place_codes(p, t, next_seg(p, cur.si, t, hop));
       load_codes16(p, next, d);
     }
     const MomentSeg& sg = p.seg[cur.si];

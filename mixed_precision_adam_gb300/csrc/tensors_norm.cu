@@ -167,10 +167,10 @@ template <int CAP>
 __global__ void __launch_bounds__(kThreads, kNormCtas) tensors_norm(const __grid_constant__ NormParamsT<CAP> p) {
   NormSum acc;
   const float2 inv = make_float2(p.inv_scale, p.inv_scale);
-  int si = 0;
+  int si = 0, hop = 1;
   if ((int)blockIdx.x < p.n_tiles) si = find_seg(p, blockIdx.x);
   for (int t = blockIdx.x; t < p.n_tiles; t += gridDim.x) {
-    si = next_seg(p, si, t);
+    si = next_seg(p, si, t, hop);
     const NormSeg& sg = p.seg[si];
     if (!DOPT_TILE_OK(p, kSiteListNorm, (int64_t)(t - sg.tile0) * (kNormTileBytes / (sg.dtype == DOPT_F32 ? 4 : 2)), 1,
                       sg.len + sg.shift))
