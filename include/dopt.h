@@ -678,7 +678,8 @@ int dopt_state_from_model(const dopt_shard_map* map, int32_t buffer, int32_t ran
  *   p = x * 0xBB67AE85 (64 bits); x = low(p) ^ high(p);
  *   p = x * 0xA54FF53B (64 bits); x = low(p) ^ high(p);
  *   r = the low half of x for even i, the high half for odd i.
- * The values of 8-bit moments are exact in bf16.
+ * The values of 8-bit moments are exact in bf16.  Moments that start at
+ * zero start as codes and scales of 0.
  */
 typedef enum {
   DOPT_MOMENTS_F32 = 0, /* exp_avg, exp_avg_sq: float; no scales            */
