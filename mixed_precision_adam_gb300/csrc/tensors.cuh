@@ -76,7 +76,7 @@ struct AdamSeg {
   int32_t tile0;
   uint32_t key;  // 8-bit moments: the tensor's term of the rounding hash
   // Where the arrays have a common vector boundary: fp32 moments, elements
-  // from the boundary below the tensor's first element to it (0 to 3);
+  // from the boundary below the tensor's first element to it (0 to 31);
   // 8-bit moments, 0 when the first element is one; -1: none.
   int32_t shift;
   int16_t param_dtype, grad_dtype;  // dopt_dtype
