@@ -356,15 +356,29 @@ __device__ __forceinline__ void step_block(const AdamSeg& sg, const Place8& a, u
   if (ring) {
     from_ring<GT>(slot, lane, g, w, mc, vc);
   } else {
+    // every load before any use of one: the path has no copies ahead
+    GT gr[8];
+    float wr[8];
+    uint8_t mr[8], vr[8];
+    const GT* const gp = static_cast<const GT*>(sg.grad) + a.first + loose;
+    const float* const wp = sg.weight + a.first + loose;
+    const uint8_t* const mp = static_cast<const uint8_t*>(sg.m) + a.first + loose;
+    const uint8_t* const vp = static_cast<const uint8_t*>(sg.v) + a.first + loose;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool in = (int)(loose + j * 32) < a.n;
+      gr[j] = in ? gp[j * 32] : GT(0.f);
+      wr[j] = in ? wp[j * 32] : 0.f;
+      mr[j] = in ? mp[j * 32] : 0;
+      vr[j] = in ? vp[j * 32] : 0;
+    }
     uint32_t mw[2] = {0u, 0u}, vw[2] = {0u, 0u};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t e = loose + j * 32;
-      const bool in = (int)e < a.n;
-      elem(g, j) = in ? load_element(sg.grad, a.first + e, sg.grad_dtype) : 0.f;
-      elem(w, j) = in ? sg.weight[a.first + e] : 0.f;
-      mw[j / 4] |= (in ? (uint32_t) static_cast<const uint8_t*>(sg.m)[a.first + e] : 0u) << (8 * (j & 3));
-      vw[j / 4] |= (in ? (uint32_t) static_cast<const uint8_t*>(sg.v)[a.first + e] : 0u) << (8 * (j & 3));
+      elem(g, j) = widen<GT>(gr[j]);
+      elem(w, j) = wr[j];
+      mw[j / 4] |= (uint32_t)mr[j] << (8 * (j & 3));
+      vw[j / 4] |= (uint32_t)vr[j] << (8 * (j & 3));
     }
     mc = make_uint2(mw[0], mw[1]);
     vc = make_uint2(vw[0], vw[1]);
@@ -381,7 +395,7 @@ __device__ __forceinline__ void step_block(const AdamSeg& sg, const Place8& a, u
       const uint32_t e = loose + j * 32;
       if ((int)e < a.n) {
         sg.weight[a.first + e] = elem(w, j);
-        store_param(sg.param, a.first + e, sg.param_dtype, elem(w, j));
+        if constexpr (sizeof(PT) == 2) static_cast<PT*>(sg.param)[a.first + e] = narrow<PT>(elem(w, j));
       } else {
         elem(m, j) = elem(v, j) = 0.f;  // past the end: no part in the scales (NaN blocks)
       }
@@ -704,13 +718,25 @@ __global__ void __launch_bounds__(kThreads, 4) state8_unpack(const __grid_consta
     } else {
       // a tensor's ragged end, or arrays with no common vector boundary:
       // consecutive lanes take consecutive elements
-#pragma unroll 1
-      for (uint32_t j = 0; j < 16; ++j) {
-        const uint32_t i = sg.vec ? e + j : threadIdx.x + j * kThreads;
-        if ((int)i >= cur.n) continue;
-        const int64_t at = cur.first + i, block = cur.first / kMomentBlock + i / kMomentBlock;
-        if (sg.m) static_cast<VT*>(sg.m)[at] = narrow<VT>(widen_m1(sg.mc[at], sg.ms[block]));
-        if (sg.v) static_cast<VT*>(sg.v)[at] = narrow<VT>(widen_v1(sg.vc[at], sg.vs[block]));
+      for (uint32_t j0 = 0; j0 < 16; j0 += 8) {
+        uint8_t cm[8], cv[8], sm[8], sv[8];
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) {
+          const uint32_t i = sg.vec ? e + j0 + j : threadIdx.x + (j0 + j) * kThreads;
+          const int64_t at = cur.first + i, block = cur.first / kMomentBlock + i / kMomentBlock;
+          const bool in = (int)i < cur.n;
+          cm[j] = in && sg.m ? sg.mc[at] : 0;
+          sm[j] = in && sg.m ? sg.ms[block] : 0;
+          cv[j] = in && sg.v ? sg.vc[at] : 0;
+          sv[j] = in && sg.v ? sg.vs[block] : 0;
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) {
+          const uint32_t i = sg.vec ? e + j0 + j : threadIdx.x + (j0 + j) * kThreads;
+          const int64_t at = cur.first + i;
+          if ((int)i < cur.n && sg.m) static_cast<VT*>(sg.m)[at] = narrow<VT>(widen_m1(cm[j], sm[j]));
+          if ((int)i < cur.n && sg.v) static_cast<VT*>(sg.v)[at] = narrow<VT>(widen_v1(cv[j], sv[j]));
+        }
       }
     }
     if (!more) break;
