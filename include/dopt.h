@@ -737,11 +737,10 @@ int dopt_tensors_grad_norm(const dopt_tensor* tensors, int32_t n_tensors, float 
  * AdamW over a list of tensors, with
  *   g = (fp32(grad) * inv_loss_scale) * (*d_clip_coef).
  * fp32 moments: per element the arithmetic of dopt_adam_step, bit for bit.
- * 8-bit moments: the same formulas in fp32, on the stored values widened;
- * the new moments step the weight and are then rounded to codes.  There b1 m
- * + (1-b1) g and b2 v + (1-b2) g^2 are fused multiply-adds, and the root and
- * the division of the weight's update are approximate (a few fp32 ulps of
- * the update).  `seed` is the stochastic rounding's.
+ * 8-bit moments: the same moments' arithmetic on the stored values widened;
+ * the new moments step the weight and are then rounded to codes.  The root
+ * and the division of the weight's update are approximate there (a few fp32
+ * ulps of the update).  `seed` is the stochastic rounding's.
  * d_clip_coef NULL: 1.  If d_found_inf is given and *d_found_inf is nonzero,
  * nothing is written.
  */

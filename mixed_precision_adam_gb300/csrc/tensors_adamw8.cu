@@ -200,13 +200,16 @@ __device__ __forceinline__ uint2 narrow_v(const float2* v, uint32_t s, const uin
   return s == 255u ? make_uint2(0u, 0u) : c;
 }
 
-// AdamW on eight elements, two per instruction, in fp32: the decays of m and v
-// and the weight's update are fused multiply-adds (one rounding less than
-// the separate operations), and the update takes the hardware's approximate
-// root and reciprocal, each within 2^-22 of the exact (the root takes a
-// subnormal v, below 1.2e-38, for 0: its root, 1e-19, is far below any eps
-// that matters).  Correctly rounded ones cost half of the kernel's
-// instructions, which then bound it: 5.0 ms against 3.8 on 1.35e9 elements.
+// AdamW on eight elements, in fp32, two per instruction but for the moments'
+// sums: the moments round each operation once, bit for bit as the fp32 ones
+// do, and a packed sum of packed products would be compiled into a fused
+// multiply-add whatever its rounding mode says (found by comparing results
+// on sm_103a; 2 % of the instructions).  The weight's update takes the
+// hardware's approximate root and reciprocal, each within 2^-22 of the exact
+// (the root takes a subnormal v, below 1.2e-38, for 0: its root, 1e-19, is
+// far below any eps that matters).  Correctly rounded ones cost half of the
+// kernel's instructions, which then bound it: 5.0 ms against 3.8 on 1.35e9
+// elements.
 struct Adam8 {
   float2 inv_scale, c, decay, b1, b2, omb1, omb2, minus_size, inv_bc2, eps;
 };
@@ -221,14 +224,17 @@ __device__ __forceinline__ float reciprocal(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float2 sum2(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
 // m arrives without its block's unit, which b1 carries (a power of two:
 // the product is the same).
 __device__ __forceinline__ void adamw_pairs(const Adam8& a, float2 b1_unit, float2* g, float2* w, float2* m, float2* v) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const float2 gk = __fmul2_rn(__fmul2_rn(g[k], a.inv_scale), a.c);
-    m[k] = __ffma2_rn(b1_unit, m[k], __fmul2_rn(a.omb1, gk));
-    v[k] = __ffma2_rn(a.b2, v[k], __fmul2_rn(__fmul2_rn(a.omb2, gk), gk));
+    m[k] = sum2(__fmul2_rn(b1_unit, m[k]), __fmul2_rn(a.omb1, gk));
+    v[k] = sum2(__fmul2_rn(a.b2, v[k]), __fmul2_rn(__fmul2_rn(a.omb2, gk), gk));
     const float2 denom = __ffma2_rn(make_float2(root(v[k].x), root(v[k].y)), a.inv_bc2, a.eps);
     const float2 u = __fmul2_rn(m[k], make_float2(reciprocal(denom.x), reciprocal(denom.y)));
     w[k] = __ffma2_rn(a.minus_size, u, __fmul2_rn(w[k], a.decay));
