@@ -222,8 +222,9 @@ int64_t replica_extent(const dopt_shard_map* m, int32_t buffer, int32_t rank, bo
 }  // namespace
 
 #if DOPT_BOUNDS_CHECK
+namespace dopt {
 // Device address of g_bounds_record on the current device.
-int dopt::bounds_record(unsigned long long** out) {
+int bounds_record(unsigned long long** out) {
   static std::mutex mu;
   static unsigned long long* addr[64] = {};
   int dev = 0;
@@ -239,6 +240,7 @@ int dopt::bounds_record(unsigned long long** out) {
   *out = addr[dev];
   return DOPT_OK;
 }
+}  // namespace dopt
 #endif
 
 namespace {

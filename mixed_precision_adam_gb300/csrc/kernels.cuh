@@ -176,7 +176,7 @@ struct FinalizeArgs {
   float* d_norm;
   float* d_coef;
   int32_t* d_found;
-  int32_t* err_flag;  // NULL: the passes before never wait for copies
+  int32_t* err_flag;
   K2Step step;
   // global terms in device memory (a multi-rank step): when set, they
   // replace the partial sum plus remote_sumsq / remote_found
@@ -204,12 +204,10 @@ struct Extents {
 // Where a range is checked, as recorded.
 enum BoundsSite : int {
   kSiteK1Rep = 1, kSiteK1Main = 2, kSiteK1Bucket = 3, kSiteTmaCopy = 4,
-  kSiteK3Main = 5, kSiteK3State = 6, kSiteK3Master = 7, kSiteK3Param = 8,
-  kSiteListNorm = 9, kSiteListAdam = 10, kSiteListAdam8 = 11, kSiteListMoments = 12
+  kSiteK3Main = 5, kSiteK3State = 6, kSiteK3Master = 7, kSiteK3Param = 8
 };
 
 #if DOPT_BOUNDS_CHECK
-int bounds_record(unsigned long long** out);  // device address of the record on the current device
 __device__ __forceinline__ bool range_ok(const Extents& x, int site, int64_t lo, int64_t n, int64_t extent) {
   if (lo >= 0 && n >= 0 && lo + n <= extent) return true;
   if (atomicAdd(x.record, 1ull) == 0ull) {
@@ -364,7 +362,7 @@ __device__ __forceinline__ void finalize_block(const FinalizeArgs& f) {
     z += (int)(fz >> 32);
   };
   // the error flag, read with the slots rather than after the sum
-  const int err_early = (threadIdx.x == 0 && !f.local_sumsq && f.err_flag) ? __ldcg(f.err_flag) : 0;
+  const int err_early = (threadIdx.x == 0 && !f.local_sumsq) ? __ldcg(f.err_flag) : 0;
   // every slot's load issued before any is summed (up to eight per thread
   // per round; a short tail predicated rather than looped)
   for (; i < f.n_slots; i += 8 * NT) {
@@ -405,7 +403,7 @@ __device__ __forceinline__ void finalize_block(const FinalizeArgs& f) {
   }
   if (threadIdx.x == 0) {
     const int kernel_error = err_early == kErrorMagic ? 1 : 0;
-    if (f.err_flag) *f.err_flag = 0;
+    *f.err_flag = 0;
     const double sumsq = f.d_global_sumsq ? __ldcg(f.d_global_sumsq) : s_sum[0] + f.remote_sumsq;
     const int remote_bad = f.d_global_sumsq ? (__ldcg(f.d_global_found) != 0) : (f.remote_found != 0);
     const int found = (s_bad[0] || remote_bad || kernel_error) ? 1 : 0;

@@ -125,6 +125,7 @@ int run_norm(const dopt_tensor* ts, int32_t n, float inv_scale, FinalizeArgs fin
   if (int st = set_record(p)) return st;
   p.inv_scale = inv_scale;
   p.n_seg = p.n_tiles = 0;
+  p.err_flag = fin.err_flag = reinterpret_cast<int32_t*>(ws_at(ws, kErrorFlagOffset));
   fin.parts = parts;
   fin.n_slots = 0;
   int32_t k = 0;

@@ -30,7 +30,9 @@ constexpr int kNormVector = 32;  // bytes: the grid tiles are cut on
 // Debug builds (DOPT_BOUNDS_CHECK=1): every table carries the address of the
 // record of tiles found outside their tensor (the first element at or past
 // its end, or more elements than it has left); such a tile is skipped.
+enum ListBoundsSite : int { kSiteListNorm = 9, kSiteListAdam = 10, kSiteListAdam8 = 11, kSiteListMoments = 12 };
 #if DOPT_BOUNDS_CHECK
+int bounds_record(unsigned long long** out);  // device address of the record on the current device
 #define DOPT_LIST_RECORD unsigned long long* record;
 #define DOPT_TILE_OK(p, site, lo, n, len) (::dopt::tile_ok((p).record, (site), (lo), (n), (len)))
 __device__ __forceinline__ bool tile_ok(unsigned long long* record, int site, int64_t lo, int64_t n, int64_t len) {
@@ -45,6 +47,7 @@ __device__ __forceinline__ bool tile_ok(unsigned long long* record, int site, in
 
 struct NormHead {
   Partial* partials;      // one slot per CTA of this launch
+  int32_t* err_flag;      // the finalize's error word, which these kernels never set: cleared
   float inv_scale;
   int32_t n_seg, n_tiles;
   DOPT_LIST_RECORD

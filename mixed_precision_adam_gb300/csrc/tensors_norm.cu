@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, kNormCtas) tensors_norm(const __grid
       s_sum[0] += s_sum[i];
       s_zero[0] += s_zero[i];
     }
+    if (blockIdx.x == 0) *p.err_flag = 0;
     p.partials[blockIdx.x] = Partial{s_sum[0], isfinite(s_sum[0]) ? 0 : 1, s_zero[0]};
   }
 }
