@@ -9,6 +9,7 @@ package fails loudly when the library has not been built.
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # DOPT_LIBRARY may name another in-tree build of the same library (the
@@ -169,9 +170,9 @@ _c = {
     "dopt_tensors_grad_norm": _proto("dopt_tensors_grad_norm", ctypes.c_int, _P, _I32, _F, _D, _P, _SZ,
                                      _P, _P, _P, _P),
     "dopt_tensors_adam_step": _proto("dopt_tensors_adam_step", ctypes.c_int, _P, _I32,
-                                     ctypes.POINTER(dopt_adamw_hparams), _F, ctypes.c_uint32, _P, _P, _P),
+                                     _P, _F, ctypes.c_uint32, _P, _P, _P),
     "dopt_tensors_step": _proto("dopt_tensors_step", ctypes.c_int, _P, _I32,
-                                ctypes.POINTER(dopt_adamw_hparams), _F, _D, ctypes.c_uint32, _P, _P, _P,
+                                _P, _F, _D, ctypes.c_uint32, _P, _P, _P,
                                 _SZ, _P, _P, _P),
     "dopt_state8_pack": _proto("dopt_state8_pack", ctypes.c_int, _P, _I32, _P),
     "dopt_state8_unpack": _proto("dopt_state8_unpack", ctypes.c_int, _P, _I32, _P),
@@ -595,9 +596,13 @@ def _array(entry, name, numel, dtypes, k, devices):
 def _listed(lst):
     """The C arguments of a list whose tensors are on one GPU (pointers are
     taken as they are)."""
-    if -1 in lst.devices or len(lst.devices) > 1:
+    d = lst.devices
+    if len(d) > 1 or -1 in d:
         raise DoptError(E_INVALID, "a list's tensors must be on one GPU")
     return lst.c, lst.n
+
+
+_hp_bytes = struct.Struct("=5dq").pack  # dopt_adamw_hparams
 
 
 class TensorList:
@@ -710,8 +715,8 @@ def dopt_tensors_grad_norm(tensors, inv_loss_scale, max_norm, workspace, workspa
 def dopt_tensors_adam_step(tensors, hp, step, inv_loss_scale=1.0, seed=0, d_clip_coef=None,
                            d_found_inf=None, stream=None):
     """AdamW over a TensorList; seed: of the 8-bit second moments' rounding."""
-    h = _hparams(hp, step)
-    _check(_c["dopt_tensors_adam_step"](*_listed(tensors), ctypes.byref(h), inv_loss_scale,
+    h = _hp_bytes(hp["lr"], hp["beta1"], hp["beta2"], hp["eps"], hp["weight_decay"], int(step))
+    _check(_c["dopt_tensors_adam_step"](*_listed(tensors), h, inv_loss_scale,
                                         seed & 0xFFFFFFFF, _ptr(d_clip_coef), _ptr(d_found_inf),
                                         _stream(stream)))
 
@@ -719,8 +724,8 @@ def dopt_tensors_adam_step(tensors, hp, step, inv_loss_scale=1.0, seed=0, d_clip
 def dopt_tensors_step(tensors, hp, step, workspace, workspace_bytes, *, inv_loss_scale=1.0, max_norm=1.0,
                       seed=0, d_step=None, d_lr=None, d_found_inf=None, d_norm=None, stream=None):
     """Grad norm, clip, skip and AdamW over a TensorList, without waiting."""
-    h = _hparams(hp, step)
-    _check(_c["dopt_tensors_step"](*_listed(tensors), ctypes.byref(h), inv_loss_scale, max_norm,
+    h = _hp_bytes(hp["lr"], hp["beta1"], hp["beta2"], hp["eps"], hp["weight_decay"], int(step))
+    _check(_c["dopt_tensors_step"](*_listed(tensors), h, inv_loss_scale, max_norm,
                                    seed & 0xFFFFFFFF, _ptr(d_step), _ptr(d_lr), _ptr(workspace),
                                    workspace_bytes, _ptr(d_found_inf), _ptr(d_norm), _stream(stream)))
 
