@@ -258,7 +258,7 @@ int resident_ctas(int* out, const char* what) {
 // Launch of one kernel over a table.  A programmatic launch may start under
 // the kernel before it (programmatic stream serialization): its CTAs wait
 // for that grid before they read or write anything they may share with it.
-template <auto Kern, size_t SMEM = 0, typename P>
+template <auto Kern, size_t SMEM = 0, int THREADS = kThreads, typename P>
 int launch_table(const P& params, cudaStream_t s, const char* what, bool programmatic = false) {
   int grid = 0;
   int st = resident_ctas<Kern, SMEM>(&grid, what);
@@ -268,7 +268,7 @@ int launch_table(const P& params, cudaStream_t s, const char* what, bool program
   attr[0].val.programmaticStreamSerializationAllowed = programmatic ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::max(1, std::min(grid, params.n_tiles)));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
   cfg.attrs = attr;

@@ -209,11 +209,14 @@ __global__ void __launch_bounds__(kThreads, kNormCtas) tensors_norm(const __grid
 
 // The finalize of a call: one CTA, launched to start under the last norm
 // launch and waiting for it (and so for the ones before it, which that one
-// waited for) before it reads their partials.
-__global__ void __launch_bounds__(kThreads) tensors_finalize(const __grid_constant__ FinalizeParams p) {
+// waited for) before it reads their partials.  128 threads: up to 608 slots
+// are one round of loads, and fewer warps share the SM's slow fp64 unit (256:
+// 2 to 4 % on small lists, 512: 12 %).
+constexpr int kFinalizeThreads = 128;
+__global__ void __launch_bounds__(kFinalizeThreads) tensors_finalize(const __grid_constant__ FinalizeParams p) {
   allow_dependent_launch();  // the AdamW launch behind it waits for this grid
   wait_for_prior_grids();
-  finalize_block<kThreads>(p.fin);
+  finalize_block<kFinalizeThreads>(p.fin);
 }
 
 int tensors_norm_tile_bytes() { return kNormTileBytes; }
@@ -234,7 +237,7 @@ int launch_tensors_norm(const NormParamsT<kNormCap>& p, cudaStream_t s) {
 }
 
 int launch_tensors_finalize(const FinalizeArgs& fin, cudaStream_t s) {
-  return launch_table<tensors_finalize>(FinalizeParams{fin, 1}, s, "tensors_finalize launch", true);
+  return launch_table<tensors_finalize, 0, kFinalizeThreads>(FinalizeParams{fin, 1}, s, "tensors_finalize launch", true);
 }
 
 }  // namespace dopt

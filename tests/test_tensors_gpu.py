@@ -472,6 +472,59 @@ def test_whole_step_equals_its_parts():
         assert all(np.array_equal(a[k], b[k], equal_nan=True) for k in a)
 
 
+def test_state_rewritten_by_a_kernel_right_before_each_step():
+    """The AdamW launch may start under the norm's; what a kernel before the step wrote must still be what it
+    reads: weights, moments and grads rewritten on the stream before every step, no wait in between."""
+    live, ref = step_list(22), step_list(22)
+    ws = torch.zeros(dopt.dopt_tensors_workspace_bytes(4), dtype=torch.uint8, device="cuda")
+    other = step_list(23)  # other weights, moments and grads, of the same shapes
+    names = ["param", "master", "grad", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"]
+    saved = [{k: a[k].view.clone() for k in names if k in a} for a in ref.arrays]
+    for step in range(1, 21):
+        # live: through other values and back, on the device, right before the step
+        for src in (other.arrays, saved):
+            for a, b in zip(live.arrays, src):
+                for k in names:
+                    if k in a:
+                        a[k].view.copy_(b[k].view if hasattr(b[k], "guards_intact") else b[k])
+        dopt.dopt_tensors_step(live.list, HP, step, ws, ws.numel(), seed=step)
+        torch.cuda.synchronize()
+        for a, b in zip(ref.arrays, saved):
+            for k in b:
+                a[k].view.copy_(b[k])
+        torch.cuda.synchronize()
+        norm, coef, found = scalars()
+        dopt.dopt_tensors_grad_norm(ref.list, 1.0, 1.0, ws, ws.numel(), norm, coef, found)
+        torch.cuda.synchronize()
+        adam(ref, step, seed=step, coef=coef, found=found)
+        torch.cuda.synchronize()
+        for k, (x, y) in enumerate(zip(ref.values(), live.values())):
+            for name in x:
+                assert np.array_equal(x[name], y[name]), (step, k, name)
+
+
+def test_two_lists_on_two_streams():
+    """Two lists stepped at once, each with its workspace, equal the same lists stepped alone."""
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    cases = [step_list(30), step_list(31)]
+    alone = [step_list(30), step_list(31)]
+    ws = [torch.zeros(dopt.dopt_tensors_workspace_bytes(4), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for step in range(1, 31):
+        for c, w, s in zip(cases, ws, streams):
+            dopt.dopt_tensors_step(c.list, HP, step, w, w.numel(), seed=9, stream=s)
+    torch.cuda.synchronize()
+    for c, w in zip(alone, ws):
+        for step in range(1, 31):
+            dopt.dopt_tensors_step(c.list, HP, step, w, w.numel(), seed=9)
+        torch.cuda.synchronize()
+    for c, a in zip(cases, alone):
+        c.check_guards()
+        for k, (x, y) in enumerate(zip(a.values(), c.values())):
+            for name in x:
+                assert np.array_equal(x[name], y[name]), (k, name)
+
+
 def test_device_step_count_in_a_graph():
     """Captured once, replayed: the same bits as host-numbered steps; a skipped replay does not count."""
     host, dev = step_list(21), step_list(21)
