@@ -10,8 +10,8 @@
 // elements per instruction, codes are made two at a time, and the inputs
 // come through a ring in shared memory.  A warp has a block of 256 elements
 // at a time, so a block's largest moments are one warp reduction each.
-// Measured on 1.35e9 bf16 elements: 3278 us, 6.57 TB/s (0.97 of the copy
-// bandwidth); 3.1e8 fp32 params and grads: 757 us, 6.51 TB/s.
+// Measured on 1.35e9 bf16 elements: 3.32 ms, 6.5 TB/s (0.96 of the copy
+// bandwidth); 3.1e8 fp32 params and grads: 762 us, 6.47 TB/s.
 #include <cuda_fp8.h>
 
 #include "tensors.cuh"
@@ -36,9 +36,8 @@ __device__ __forceinline__ uint32_t hash_pair(uint32_t x) {
   return (uint32_t)q ^ (uint32_t)(q >> 32);
 }
 
-// A block's exp_avg scale from the bits of its largest magnitude; the
-// multiplier that brings the block to e4m3's range (0 for a block that is
-// not finite).
+// A block's scales from the bits of its largest magnitude: 255 where that is
+// not finite or above the largest code.
 __device__ __forceinline__ uint32_t m_scale_of(uint32_t top) {
   const uint32_t e = exponent_of(top, 0x1FFFFFu);
   return e >= 255u ? 255u : max((int)e - 8, 8);
@@ -551,10 +550,9 @@ int launch_tensors_adamw8(const AdamParamsT<kAdamCap>& p, cudaStream_t s) {
 // Packing takes one warp per block, eight elements per lane: consecutive ones
 // in vectors where every array has its first element on a vector boundary and
 // the block is whole, else 32 apart.  A thread loads its next tile's values
-// before it packs this one's
-// (16-bit values only: at 1.3e8 elements bf16 ones take 150 us so and 162
-// without; fp32 ones 190 us without, at the copy bandwidth, and 199 with).
-// Five CTAs per SM; six spill (fp32 206 us).
+// before it packs this one's when they are bf16: 1.3e8 elements take 150 us
+// so and 162 without; fp32 ones 190 us without, at the copy bandwidth, and
+// 199 with.  Five CTAs per SM; six spill (fp32 206 us).
 template <typename VT>
 constexpr bool kPackAhead = sizeof(VT) == 2;
 constexpr int kPackCtas = 5;
