@@ -30,34 +30,40 @@ class Array:
 
 
 class Case:
-    """tensors: dicts of numel, param, grad ("f32", "bf16", "f16"), moments (32 or 8), offset, wd_mult, zero
-    (share of zero grads and moments)."""
+    """tensors: dicts of numel, param, grad ("f32", "bf16", "f16"), moments (32 or 8), offset (of every array, in
+    elements) and offsets (of the arrays named, instead), wd_mult, zero (share of zero grads and moments)."""
 
     def __init__(self, tensors, seed, grad_size=1e-2, scale=1.0):
         import mixed_precision_adam_gb300 as dopt
         gen = torch.Generator().manual_seed(seed)
         self.spec, self.arrays, entries = tensors, [], []
         for t in tensors:
-            n, off = t["numel"], t.get("offset", 0)
+            n, offs = t["numel"], t.get("offsets", {})
+
+            def off(name, default=t.get("offset", 0), offs=offs):
+                return offs.get(name, default)
+
             size = torch.exp(torch.randn(n, generator=gen)) * grad_size
             size *= torch.rand(n, generator=gen) >= t.get("zero", 0.0)
-            a = dict(grad=Array(torch.randn(n, generator=gen) * size * scale, TORCH[t["grad"]], off))
+            a = dict(grad=Array(torch.randn(n, generator=gen) * size * scale, TORCH[t["grad"]], off("grad")))
             w = torch.randn(n, generator=gen) * 0.05
-            a["param"] = Array(w.to(TORCH[t["param"]]), TORCH[t["param"]], off)
+            a["param"] = Array(w.to(TORCH[t["param"]]), TORCH[t["param"]], off("param"))
             if t["param"] != "f32":
-                a["master"] = Array(w, torch.float32, off)
+                a["master"] = Array(w, torch.float32, off("master"))
             m, v = torch.randn(n, generator=gen) * size * 0.3, torch.rand(n, generator=gen) * size * size
             if t["moments"] == 32:
-                a["exp_avg"], a["exp_avg_sq"] = Array(m, torch.float32, off), Array(v, torch.float32, off)
+                a["exp_avg"] = Array(m, torch.float32, off("exp_avg"))
+                a["exp_avg_sq"] = Array(v, torch.float32, off("exp_avg_sq"))
             else:
                 ms, vs = O.m_scale(m.double().numpy()), O.v_scale(v.double().numpy())
-                a["exp_avg_scale"], a["exp_avg_sq_scale"] = (Array(torch.from_numpy(s), torch.uint8, off) for s in (ms, vs))
+                a["exp_avg_scale"] = Array(torch.from_numpy(ms), torch.uint8, off("exp_avg_scale"))
+                a["exp_avg_sq_scale"] = Array(torch.from_numpy(vs), torch.uint8, off("exp_avg_sq_scale"))
                 mc = torch.randint(0, 255, (n,), generator=gen)
                 mc = torch.where(mc == 127, 3, mc)  # e4m3's NaN codes are never stored
                 vc = torch.randint(0, 256, (n,), generator=gen)
                 zero = size == 0
-                a["exp_avg"] = Array(torch.where(zero, 0, mc), torch.uint8, off)
-                a["exp_avg_sq"] = Array(torch.where(zero, 0, vc), torch.uint8, off)
+                a["exp_avg"] = Array(torch.where(zero, 0, mc), torch.uint8, off("exp_avg"))
+                a["exp_avg_sq"] = Array(torch.where(zero, 0, vc), torch.uint8, off("exp_avg_sq"))
             self.arrays.append(a)
             entries.append(dict({k: x.view for k, x in a.items()}, wd_mult=t.get("wd_mult", 1.0)))
         self.list = dopt.TensorList(entries)

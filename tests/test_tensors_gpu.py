@@ -150,6 +150,20 @@ def test_step_sizes_and_offsets(types, moments, offset):
         case.check_step(step, 1 / 1024, float(coef), 99)
 
 
+@pytest.mark.parametrize("types", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("moments", [32, 8])
+@pytest.mark.parametrize("by", [1, 4, 8, 16])
+def test_step_with_one_array_off_the_others_grid(types, moments, by):
+    """Each array in turn starts `by` elements further on than the rest."""
+    names = ["param", "grad", "exp_avg", "exp_avg_sq"] + (["master"] if types[0] != "f32" else []) + \
+        (["exp_avg_scale", "exp_avg_sq_scale"] if moments == 8 else [])
+    case = Case([dict(numel=n, param=types[0], grad=types[1], moments=moments, offsets={name: by})
+                 for name in names for n in (5, 2500, 30000)], seed=by)
+    for step in (1, 2):
+        adam(case, step, seed=5)
+        case.check_step(step, seed=5)
+
+
 def test_step_of_a_mixed_list():
     """Every type and moment format in one list, in no order."""
     tensors = []
