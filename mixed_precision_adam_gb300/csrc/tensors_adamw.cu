@@ -5,10 +5,15 @@
 // grads and params, 30 with fp32 grads, 28 for fp32 params): bound by
 // memory.  A CTA strides over the list's tiles; a thread has four elements
 // of a tile, and loads its next tile's before it computes and stores this
-// one's, so the memory pipe stays busy under the arithmetic.
+// one's, so the memory pipe stays busy under the arithmetic.  Measured on
+// 1.35e9 bf16 params with fp32 grads: 5.83 ms, 6.93 TB/s (1.02 of the copy
+// bandwidth; 6.05 ms without a limit to a CTA's walk); fp16 ones with fp16
+// grads: 5.6 ms, 6.7 TB/s.
 #include "tensors.cuh"
 
 namespace dopt {
+
+constexpr int kRounds32 = 24;  // of a CTA's walk over the tiles (see launch_walk)
 
 // Four elements of a 16-bit type, as loaded and stored at once.
 __device__ __forceinline__ float half_bits(unsigned bits) { return __half2float(__ushort_as_half((unsigned short)bits)); }
@@ -83,8 +88,9 @@ __device__ __forceinline__ void load_grad(const P& p, AdamPart& a) {
 
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, 4) tensors_adamw(const __grid_constant__ AdamParamsT<CAP> p) {
-  int t = blockIdx.x;
-  const bool work = t < p.n_tiles;
+  const TileWalk walk = tile_walk(p);
+  int t = walk.first;
+  const bool work = t < walk.end;
   int hop = 1;
   AdamPart cur;
   if (work) {
@@ -102,8 +108,8 @@ __global__ void __launch_bounds__(kThreads, 4) tensors_adamw(const __grid_consta
   cur.decay = decay_of_seg(p, p.seg[cur.si]);
   for (;;) {
     AdamPart nxt;
-    const int tn = t + (int)gridDim.x;
-    const bool more = tn < p.n_tiles;
+    const int tn = t + p.stride;
+    const bool more = tn < walk.end;
     if (more) {
       place_part(p, tn, next_seg(p, cur.si, tn, hop), nxt);
       load_grad(p, nxt);
@@ -151,11 +157,13 @@ __global__ void __launch_bounds__(kThreads, 4) tensors_adamw(const __grid_consta
   }
 }
 
-int launch_tensors_adamw(const AdamParamsT<kAdamCap>& p, cudaStream_t s) {
+int launch_tensors_adamw(AdamParamsT<kAdamCap>& p, cudaStream_t s) {
   const char* what = "tensors_adamw launch";
-  if (p.n_seg <= kAdamSmallCap)
-    return launch_table<tensors_adamw<kAdamSmallCap>>(compact_table<AdamParamsT<kAdamSmallCap>, AdamHead>(p), s, what, true);
-  return launch_table<tensors_adamw<kAdamCap>>(p, s, what, true);
+  if (p.n_seg <= kAdamSmallCap) {
+    AdamParamsT<kAdamSmallCap> small = compact_table<AdamParamsT<kAdamSmallCap>, AdamHead>(p);
+    return launch_walk<tensors_adamw<kAdamSmallCap>, 0, kRounds32>(small, s, what, true);
+  }
+  return launch_walk<tensors_adamw<kAdamCap>, 0, kRounds32>(p, s, what, true);
 }
 
 }  // namespace dopt

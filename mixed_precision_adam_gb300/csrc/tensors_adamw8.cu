@@ -10,8 +10,8 @@
 // elements per instruction, codes are made two at a time, and the inputs
 // come through a ring in shared memory.  A warp has a block of 256 elements
 // at a time, so a block's largest moments are one warp reduction each.
-// Measured on 1.35e9 bf16 elements: 3.32 ms, 6.5 TB/s (0.96 of the copy
-// bandwidth); 3.1e8 fp32 params and grads: 762 us, 6.47 TB/s.
+// Measured on 1.35e9 bf16 elements: 3.13 ms, 6.88 TB/s (1.02 of the copy
+// bandwidth); as many fp32 params and grads: 3.05 ms, 7.1 TB/s.
 #include <cuda_fp8.h>
 
 #include "tensors.cuh"
@@ -21,7 +21,9 @@ namespace dopt {
 // Three CTAs per SM and three slots per warp: 20 KB per slot and CTA, 180 KB of
 // the SM's shared memory.  Four CTAs (64 registers) were 7 % slower, two slots
 // 5 %; four slots leave room for two CTAs only (21 % slower).
-constexpr int kRing8 = 3, kCtas8 = 3;
+// Rounds of a CTA's walk over the tiles (see launch_walk): the best of 1 to 64
+// and of no limit, which took 3490 us on 1.35e9 bf16 elements against 3133.
+constexpr int kRing8 = 3, kCtas8 = 3, kRounds8 = 24;
 static_assert(kMomentBlock == 256 && kAdamTile % kMomentBlock == 0, "one warp per block, 8 elements per lane");
 
 __device__ __forceinline__ uint32_t exponent_of(uint32_t bits, uint32_t up) { return (bits + up) >> 23; }
@@ -351,103 +353,110 @@ __device__ __forceinline__ void from_ring(uint32_t slot, uint32_t lane, float2* 
   vc = shared8(slot + Ring8::kGrad + Ring8::kWeight + Ring8::kCodes + lane * 8u);
 }
 
-// Updates a warp's block.  key: the hash's argument for the tile's first
-// pair.  Element j of a lane: consecutive ones for a block through the
-// ring; 32 apart (consecutive lanes, consecutive elements) in a tensor's
-// ragged last block, or where the arrays have no common vector boundary.
+// Updates a warp's block that came through the ring.  key: the hash's
+// argument for the tile's first pair.
 template <typename PT, typename GT>
 __device__ __forceinline__ void step_block(const AdamSeg& sg, const Place8& a, uint32_t slot, uint32_t scales,
                                            const Adam8& ad, uint32_t key) {
-  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const bool ring = through_ring(sg, a);
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, at = threadIdx.x * 8;
   float2 g[4], w[4], m[4], v[4];
   uint2 mc, vc;
-  const uint32_t at = threadIdx.x * 8, loose = warp * kMomentBlock + lane;
-  if (ring) {
-    from_ring<GT>(slot, lane, g, w, mc, vc);
-  } else {
-    // every load before any use of one: the path has no copies ahead
-    GT gr[8];
-    float wr[8];
-    uint8_t mr[8], vr[8];
-    const GT* const gp = static_cast<const GT*>(sg.grad) + a.first + loose;
-    const float* const wp = sg.weight + a.first + loose;
-    const uint8_t* const mp = static_cast<const uint8_t*>(sg.m) + a.first + loose;
-    const uint8_t* const vp = static_cast<const uint8_t*>(sg.v) + a.first + loose;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const bool in = (int)(loose + j * 32) < a.n;
-      gr[j] = in ? gp[j * 32] : GT(0.f);
-      wr[j] = in ? wp[j * 32] : 0.f;
-      mr[j] = in ? mp[j * 32] : 0;
-      vr[j] = in ? vp[j * 32] : 0;
-    }
-    uint32_t mw[2] = {0u, 0u}, vw[2] = {0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      elem(g, j) = widen<GT>(gr[j]);
-      elem(w, j) = wr[j];
-      mw[j / 4] |= (uint32_t)mr[j] << (8 * (j & 3));
-      vw[j / 4] |= (uint32_t)vr[j] << (8 * (j & 3));
-    }
-    mc = make_uint2(mw[0], mw[1]);
-    vc = make_uint2(vw[0], vw[1]);
-  }
+  from_ring<GT>(slot, lane, g, w, mc, vc);
   widen_m(mc, m);
   widen_v(vc, scales >> 8, v);
   adamw_pairs(ad, both(__fmul_rn(ad.b1.x, m_unit(scales & 0xFFu))), g, w, m, v);
-  if (ring) {
-    store8(at_offset(sg.weight + a.first, at), w);
-    if constexpr (sizeof(PT) == 2) Eight<PT>::store(at_offset(static_cast<PT*>(sg.param) + a.first, at), w);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t e = loose + j * 32;
-      if ((int)e < a.n) {
-        sg.weight[a.first + e] = elem(w, j);
-        if constexpr (sizeof(PT) == 2) static_cast<PT*>(sg.param)[a.first + e] = narrow<PT>(elem(w, j));
-      } else {
-        elem(m, j) = elem(v, j) = 0.f;  // past the end: no part in the scales (NaN blocks)
-      }
-    }
-  }
+  store8(at_offset(sg.weight + a.first, at), w);
+  if constexpr (sizeof(PT) == 2) Eight<PT>::store(at_offset(static_cast<PT*>(sg.param) + a.first, at), w);
   const uint32_t ms = m_scale_of(block_top(m)), vs = v_scale_of(block_top(v));
   uint32_t r16[4];
-  if (ring) {
-    const uint32_t y = key + (at >> 1) * kHashPair;
+  const uint32_t y = key + (at >> 1) * kHashPair;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) r16[k] = hash_pair(y + k * kHashPair);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t y = key + (warp * (kMomentBlock / 2) + (lane >> 1) + k * 32) * kHashPair;
-      r16[k] = __byte_perm(hash_pair(y), hash_pair(y + 16 * kHashPair), (lane & 1) ? 0x7632 : 0x5410);
-    }
-  }
-  mc = narrow_m(m, ms);
-  vc = narrow_v(v, vs, r16);
+  for (int k = 0; k < 4; ++k) r16[k] = hash_pair(y + k * kHashPair);
   if (lane == 0) {
     *at_offset(sg.m_scale + a.first / kMomentBlock, warp) = (uint8_t)ms;
     *at_offset(sg.v_scale + a.first / kMomentBlock, warp) = (uint8_t)vs;
   }
-  if (ring) {
-    __stcs(reinterpret_cast<uint2*>(at_offset(static_cast<uint8_t*>(sg.m) + a.first, at)), mc);
-    __stcs(reinterpret_cast<uint2*>(at_offset(static_cast<uint8_t*>(sg.v) + a.first, at)), vc);
-  } else {
+  __stcs(reinterpret_cast<uint2*>(at_offset(static_cast<uint8_t*>(sg.m) + a.first, at)), narrow_m(m, ms));
+  __stcs(reinterpret_cast<uint2*>(at_offset(static_cast<uint8_t*>(sg.v) + a.first, at)), narrow_v(v, vs, r16));
+}
+
+// Updates a block of n elements from element `first` of a tensor (its ragged
+// last one, or any where the arrays have no common vector boundary).  Element
+// j of a lane is 32 apart from the next: consecutive lanes, consecutive
+// elements.  One body for every type: five copies of it beside the path above
+// cost that path 3 %, and a call out of line half its speed (its arguments go
+// through memory).
+__device__ __forceinline__ void step_loose(const AdamSeg& sg, int64_t first, int n, uint32_t scales, const Adam8& ad, uint32_t key) {
+  const uint32_t lane = threadIdx.x % 32;
+  float* const wp = sg.weight + first + lane;
+  uint8_t* const mp = static_cast<uint8_t*>(sg.m) + first + lane;
+  uint8_t* const vp = static_cast<uint8_t*>(sg.v) + first + lane;
+  float2 g[4], w[4], m[4], v[4];
+  uint32_t mw[2] = {0u, 0u}, vw[2] = {0u, 0u};
+  // every load before any use of one: the path has no copies ahead
+  if (sg.grad_dtype == DOPT_F32) {
+    const float* const gp = static_cast<const float*>(sg.grad) + first + lane;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t e = loose + j * 32;
-      if ((int)e < a.n) {
-        static_cast<uint8_t*>(sg.m)[a.first + e] = (uint8_t)((j < 4 ? mc.x : mc.y) >> (8 * (j & 3)));
-        static_cast<uint8_t*>(sg.v)[a.first + e] = (uint8_t)((j < 4 ? vc.x : vc.y) >> (8 * (j & 3)));
-      }
+    for (int j = 0; j < 8; ++j) elem(g, j) = (int)lane + j * 32 < n ? gp[j * 32] : 0.f;
+  } else {
+    const uint16_t* const gp = static_cast<const uint16_t*>(sg.grad) + first + lane;
+    uint16_t r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = (int)lane + j * 32 < n ? gp[j * 32] : 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      elem(g, j) = sg.grad_dtype == DOPT_BF16 ? __uint_as_float((uint32_t)r[j] << 16) : __half2float(__ushort_as_half(r[j]));
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const bool in = (int)lane + j * 32 < n;
+    elem(w, j) = in ? wp[j * 32] : 0.f;
+    mw[j / 4] |= (in ? (uint32_t)mp[j * 32] : 0u) << (8 * (j & 3));
+    vw[j / 4] |= (in ? (uint32_t)vp[j * 32] : 0u) << (8 * (j & 3));
+  }
+  widen_m(make_uint2(mw[0], mw[1]), m);
+  widen_v(make_uint2(vw[0], vw[1]), scales >> 8, v);
+  adamw_pairs(ad, both(__fmul_rn(ad.b1.x, m_unit(scales & 0xFFu))), g, w, m, v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if ((int)lane + j * 32 < n) {
+      wp[j * 32] = elem(w, j);
+      store_param(sg.param, first + lane + j * 32, sg.param_dtype, elem(w, j));
+    } else {
+      elem(m, j) = elem(v, j) = 0.f;  // past the end: no part in the scales (NaN blocks)
+    }
+  }
+  const uint32_t ms = m_scale_of(block_top(m)), vs = v_scale_of(block_top(v));
+  uint32_t r16[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t y = key + ((uint32_t)(first >> 1) + (lane >> 1) + k * 32) * kHashPair;
+    r16[k] = __byte_perm(hash_pair(y), hash_pair(y + 16 * kHashPair), (lane & 1) ? 0x7632 : 0x5410);
+  }
+  const uint2 mc = narrow_m(m, ms), vc = narrow_v(v, vs, r16);
+  if (lane == 0) {
+    sg.m_scale[first / kMomentBlock] = (uint8_t)ms;
+    sg.v_scale[first / kMomentBlock] = (uint8_t)vs;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if ((int)lane + j * 32 < n) {
+      mp[j * 32] = (uint8_t)((j < 4 ? mc.x : mc.y) >> (8 * (j & 3)));
+      vp[j * 32] = (uint8_t)((j < 4 ? vc.x : vc.y) >> (8 * (j & 3)));
     }
   }
 }
 
 // The block's update for its tensor's types (the same for the whole CTA).
+// key: the hash's argument for the tensor's first pair.
 __device__ __forceinline__ void step_block_of(const AdamSeg& sg, const Place8& a, uint32_t slot, uint32_t scales,
                                               const Adam8& ad, uint32_t key) {
+  if (!through_ring(sg, a)) {
+    const int64_t block = (int64_t)(threadIdx.x / 32) * kMomentBlock;
+    step_loose(sg, a.first + block, min(a.n - (int)block, kMomentBlock), scales, ad, key);
+    return;
+  }
+  key += (uint32_t)(a.first >> 1) * kHashPair;
   if (sg.param_dtype == DOPT_BF16) {
     if (sg.grad_dtype == DOPT_BF16)
       step_block<__nv_bfloat16, __nv_bfloat16>(sg, a, slot, scales, ad, key);
@@ -469,7 +478,8 @@ __global__ void __launch_bounds__(kThreads, kCtas8) tensors_adamw8(const __grid_
   uint32_t slot0;
   asm("{.reg .u64 t; cvta.to.shared.u64 t, %1; cvt.u32.u64 %0, t;}" : "=r"(slot0) : "l"(ring));
   slot0 += threadIdx.x / 32 * (kRing8 * Ring8::kSlot);
-  int t = blockIdx.x;
+  const TileWalk walk = tile_walk(p);
+  int t = walk.first;
   Place8 cur = {}, ahead;
   uint32_t scales[kRing8];  // of the tiles in flight, this one's first
   int tensor[kRing8];
@@ -477,21 +487,21 @@ __global__ void __launch_bounds__(kThreads, kCtas8) tensors_adamw8(const __grid_
   if (!p.early) wait_for_prior_grids();
   // the first kRing8 - 1 tiles; the launch before this one, when it is of
   // the same call, writes none of what they read
-  if (t < p.n_tiles) cur = place_tile(p, t, find_seg(p, t));
+  if (t < walk.end) cur = place_tile(p, t, find_seg(p, t));
   ahead = cur;
   int ta = t;
 #pragma unroll
   for (int k = 0; k < kRing8 - 1; ++k) {
-    if (ta < p.n_tiles) {
+    if (ta < walk.end) {
       if (k) ahead = place_tile(p, ta, next_seg(p, ahead.si, ta, hop));
       tensor[k] = ahead.si;
       fetch_block(p, ahead, slot0 + k * Ring8::kSlot, scales[k]);
-      ta += gridDim.x;
+      ta += p.stride;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   if (p.early) wait_for_prior_grids();
-  if (t >= p.n_tiles || (p.found_inf && *p.found_inf)) {
+  if (t >= walk.end || (p.found_inf && *p.found_inf)) {
     asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
@@ -510,19 +520,18 @@ __global__ void __launch_bounds__(kThreads, kCtas8) tensors_adamw8(const __grid_
   uint32_t slot = slot0, slot_ahead = slot0 + (kRing8 - 1) * Ring8::kSlot;
   const uint32_t slot_end = slot0 + kRing8 * Ring8::kSlot;
   for (;;) {
-    if (ta < p.n_tiles) {
+    if (ta < walk.end) {
       ahead = place_tile(p, ta, next_seg(p, ahead.si, ta, hop));
       tensor[kRing8 - 1] = ahead.si;
       fetch_block(p, ahead, slot_ahead, scales[kRing8 - 1]);
-      ta += gridDim.x;
+      ta += p.stride;
     }
     asm volatile("cp.async.commit_group;\n cp.async.wait_group %0;" ::"n"(kRing8 - 1) : "memory");
     __syncwarp();  // the warp's copies, not this lane's alone
     if ((int)(threadIdx.x / 32 * kMomentBlock) < cur.n)
-      step_block_of(p.seg[cur.si], cur, slot, scales[0], ad,
-                         key + p.seg[cur.si].key + (uint32_t)(cur.first >> 1) * kHashPair);
-    t += gridDim.x;
-    if (t >= p.n_tiles) break;
+      step_block_of(p.seg[cur.si], cur, slot, scales[0], ad, key + p.seg[cur.si].key);
+    t += p.stride;
+    if (t >= walk.end) break;
     const Place8 next = place_tile(p, t, tensor[1]);
     if (next.si != cur.si) ad.decay = both(decay_of_seg(p, p.seg[next.si]));
     cur = next;
@@ -537,11 +546,13 @@ __global__ void __launch_bounds__(kThreads, kCtas8) tensors_adamw8(const __grid_
   }
 }
 
-int launch_tensors_adamw8(const AdamParamsT<kAdamCap>& p, cudaStream_t s) {
+int launch_tensors_adamw8(AdamParamsT<kAdamCap>& p, cudaStream_t s) {
   const char* what = "tensors_adamw8 launch";
-  if (p.n_seg <= kAdamSmallCap)
-    return launch_table<tensors_adamw8<kAdamSmallCap>, Ring8::kBytes>(compact_table<AdamParamsT<kAdamSmallCap>, AdamHead>(p), s, what, true);
-  return launch_table<tensors_adamw8<kAdamCap>, Ring8::kBytes>(p, s, what, true);
+  if (p.n_seg <= kAdamSmallCap) {
+    AdamParamsT<kAdamSmallCap> small = compact_table<AdamParamsT<kAdamSmallCap>, AdamHead>(p);
+    return launch_walk<tensors_adamw8<kAdamSmallCap>, Ring8::kBytes, kRounds8>(small, s, what, true);
+  }
+  return launch_walk<tensors_adamw8<kAdamCap>, Ring8::kBytes, kRounds8>(p, s, what, true);
 }
 
 // ------------------------------------------------------- pack and unpack --
@@ -551,10 +562,11 @@ int launch_tensors_adamw8(const AdamParamsT<kAdamCap>& p, cudaStream_t s) {
 // the block is whole, else 32 apart.  A thread loads its next tile's values
 // before it packs this one's when they are bf16: 1.3e8 elements take 150 us
 // so and 162 without; fp32 ones 190 us without, at the copy bandwidth, and
-// 199 with.  Five CTAs per SM; six spill (fp32 206 us).
+// 199 with.  Five CTAs per SM; six spill (fp32 206 us).  16 rounds of a walk:
+// 1.35e9 fp32 elements 1841 us, 7.31 TB/s, against 1915 without a limit.
 template <typename VT>
 constexpr bool kPackAhead = sizeof(VT) == 2;
-constexpr int kPackCtas = 5;
+constexpr int kPackCtas = 5, kPackRounds = 16;
 template <typename VT>
 struct Values8 {
   typename Eight<VT>::Raw m, v;
@@ -618,8 +630,9 @@ __device__ __forceinline__ void loose_codes(uint8_t* x, int n, uint2 c) {
 
 template <typename VT, int CAP>
 __global__ void __launch_bounds__(kThreads, kPackCtas) state8_pack(const __grid_constant__ MomentParamsT<CAP> p) {
-  int t = blockIdx.x;
-  if (t >= p.n_tiles) return;
+  const TileWalk walk = tile_walk(p);
+  int t = walk.first;
+  if (t >= walk.end) return;
   int hop = 1;
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   Place8 cur = place_values(p, t, find_seg(p, t));
@@ -627,8 +640,8 @@ __global__ void __launch_bounds__(kThreads, kPackCtas) state8_pack(const __grid_
   if constexpr (kPackAhead<VT>) load_values(p, cur, x);
   for (;;) {
     if constexpr (!kPackAhead<VT>) load_values(p, cur, x);
-    t += gridDim.x;
-    const bool more = t < p.n_tiles;
+    t += p.stride;
+    const bool more = t < walk.end;
     Place8 next = cur;
     Values8<VT> y;
     if (more) {
@@ -703,10 +716,11 @@ __device__ __forceinline__ float widen_v1(uint32_t code, uint32_t s) {
 
 // Sixteen elements per thread, which lie in one block.  A thread loads its
 // next tile's codes before it widens and stores this one's.  Bound by memory
-// at this mix of one byte read per two or four written: 5.8 to
-// 6.1 TB/s at 1.3e8 and 1.3e9 elements (eight elements, no prefetch: 5.5 and
-// 6.0); two to four CTAs per SM are alike, six 3 % slower; fp32 stores of 1 KB
-// runs per warp (eight elements and eight half a tile on) 1 %.
+// at this mix of one byte read per two or four written: at 1.35e9 elements
+// 1160 us to bf16 and 1928 to fp32, 6.96 and 6.98 TB/s, with walks of two
+// rounds; 1268 and 2198 without a limit (see launch_walk).  Two to four CTAs
+// per SM are alike, six 3 % slower; fp32 stores of 1 KB runs per warp 1 %.
+constexpr int kUnpackRounds = 2;
 struct Codes16 {
   uint4 m, v;
   uint32_t ms, vs;
@@ -746,15 +760,16 @@ __device__ __forceinline__ void load_codes16(const P& p, const UnpackPlace& a, C
 template <typename VT, int CAP>
 __global__ void __launch_bounds__(kThreads, 4) state8_unpack(const __grid_constant__ MomentParamsT<CAP> p) {
   static_assert(kUnpackTile == kThreads * 16 && kMomentBlock % 16 == 0, "sixteen elements per thread");
-  int t = blockIdx.x;
-  if (t >= p.n_tiles) return;
+  const TileWalk walk = tile_walk(p);
+  int t = walk.first;
+  if (t >= walk.end) return;
   int hop = 1;
   UnpackPlace cur = place_codes(p, t, find_seg(p, t));
   Codes16 c;
   load_codes16(p, cur, c);
   for (;;) {
-    t += gridDim.x;
-    const bool more = t < p.n_tiles;
+    t += p.stride;
+    const bool more = t < walk.end;
     UnpackPlace next = cur;
     Codes16 d;
     if (more) {
@@ -781,15 +796,15 @@ __global__ void __launch_bounds__(kThreads, 4) state8_unpack(const __grid_consta
         widen_v(make_uint2(c.v.z, c.v.w), c.vs, hi);
         store16<VT>(at_offset(static_cast<VT*>(sg.v) + cur.first, e), lo, hi);
       }
-    } else {
-      // a tensor's ragged end, or arrays with no common vector boundary, where
-      // consecutive lanes take consecutive elements: four loads at a time
+    } else if (!sg.vec) {
+      // arrays with no common vector boundary: consecutive lanes take
+      // consecutive elements, four loads at a time
 #pragma unroll 1
       for (uint32_t j0 = 0; j0 < 16; j0 += 4) {
         uint8_t cm[4], cv[4], sm[4], sv[4];
 #pragma unroll
         for (uint32_t j = 0; j < 4; ++j) {
-          const uint32_t i = sg.vec ? e + j0 + j : threadIdx.x + (j0 + j) * kThreads;
+          const uint32_t i = threadIdx.x + (j0 + j) * kThreads;
           const bool in = (int)i < cur.n;
           const int64_t at = cur.first + i, block = cur.first / kMomentBlock + i / kMomentBlock;
           cm[j] = in && sg.m ? sg.mc[at] : 0;
@@ -799,12 +814,19 @@ __global__ void __launch_bounds__(kThreads, 4) state8_unpack(const __grid_consta
         }
 #pragma unroll
         for (uint32_t j = 0; j < 4; ++j) {
-          const uint32_t i = sg.vec ? e + j0 + j : threadIdx.x + (j0 + j) * kThreads;
+          const uint32_t i = threadIdx.x + (j0 + j) * kThreads;
           if ((int)i >= cur.n) continue;
           if (sg.m) static_cast<VT*>(sg.m)[cur.first + i] = narrow<VT>(widen_m1(cm[j], sm[j]));
           if (sg.v) static_cast<VT*>(sg.v)[cur.first + i] = narrow<VT>(widen_v1(cv[j], sv[j]));
         }
       }
+    }
+    // a tensor's ragged end, fewer than sixteen elements: one per thread
+    const int tail = (cur.n & ~15) + (int)threadIdx.x;
+    if (sg.vec && tail < cur.n) {
+      const int64_t at = cur.first + tail;
+      if (sg.m) static_cast<VT*>(sg.m)[at] = narrow<VT>(widen_m1(sg.mc[at], sg.ms[at / kMomentBlock]));
+      if (sg.v) static_cast<VT*>(sg.v)[at] = narrow<VT>(widen_v1(sg.vc[at], sg.vs[at / kMomentBlock]));
     }
     if (!more) break;
     cur = next;
@@ -812,23 +834,29 @@ __global__ void __launch_bounds__(kThreads, 4) state8_unpack(const __grid_consta
   }
 }
 
-template <typename VT>
-int launch_pack_t(const MomentParamsT<kMomentCap>& p, cudaStream_t s) {
-  const char* what = "state8_pack launch";
-  return p.n_seg <= kMomentSmallCap ? launch_table<state8_pack<VT, kMomentSmallCap>>(compact_table<MomentParamsT<kMomentSmallCap>, MomentHead>(p), s, what)
-                                    : launch_table<state8_pack<VT, kMomentCap>>(p, s, what);
+// Launches a pack or unpack kernel's walk, with the compact table where it fits.
+template <auto Small, auto Big, int ROUNDS>
+int launch_moments(MomentParamsT<kMomentCap>& p, cudaStream_t s, const char* what) {
+  if (p.n_seg <= kMomentSmallCap) {
+    MomentParamsT<kMomentSmallCap> small = compact_table<MomentParamsT<kMomentSmallCap>, MomentHead>(p);
+    return launch_walk<Small, 0, ROUNDS>(small, s, what, false);
+  }
+  return launch_walk<Big, 0, ROUNDS>(p, s, what, false);
 }
 template <typename VT>
-int launch_unpack_t(const MomentParamsT<kMomentCap>& p, cudaStream_t s) {
-  const char* what = "state8_unpack launch";
-  return p.n_seg <= kMomentSmallCap ? launch_table<state8_unpack<VT, kMomentSmallCap>>(compact_table<MomentParamsT<kMomentSmallCap>, MomentHead>(p), s, what)
-                                    : launch_table<state8_unpack<VT, kMomentCap>>(p, s, what);
+int launch_pack_t(MomentParamsT<kMomentCap>& p, cudaStream_t s) {
+  return launch_moments<state8_pack<VT, kMomentSmallCap>, state8_pack<VT, kMomentCap>, kPackRounds>(p, s, "state8_pack launch");
+}
+template <typename VT>
+int launch_unpack_t(MomentParamsT<kMomentCap>& p, cudaStream_t s) {
+  return launch_moments<state8_unpack<VT, kMomentSmallCap>, state8_unpack<VT, kMomentCap>, kUnpackRounds>(
+      p, s, "state8_unpack launch");
 }
 
-int launch_state8_pack(int32_t values_dtype, const MomentParamsT<kMomentCap>& p, cudaStream_t s) {
+int launch_state8_pack(int32_t values_dtype, MomentParamsT<kMomentCap>& p, cudaStream_t s) {
   return values_dtype == DOPT_F32 ? launch_pack_t<float>(p, s) : launch_pack_t<__nv_bfloat16>(p, s);
 }
-int launch_state8_unpack(int32_t values_dtype, const MomentParamsT<kMomentCap>& p, cudaStream_t s) {
+int launch_state8_unpack(int32_t values_dtype, MomentParamsT<kMomentCap>& p, cudaStream_t s) {
   return values_dtype == DOPT_F32 ? launch_unpack_t<float>(p, s) : launch_unpack_t<__nv_bfloat16>(p, s);
 }
 
