@@ -740,7 +740,8 @@ int dopt_tensors_grad_norm(const dopt_tensor* tensors, int32_t n_tensors, float 
  * 8-bit moments: the same moments' arithmetic on the stored values widened;
  * the new moments step the weight and are then rounded to codes.  The root
  * and the division of the weight's update are approximate there (a few fp32
- * ulps of the update).  `seed` is the stochastic rounding's.
+ * ulps of the update, subnormal second moments included); an eps that is 0
+ * in fp32 counts as 2^-150.  `seed` is the stochastic rounding's.
  * d_clip_coef NULL: 1.  If d_found_inf is given and *d_found_inf is nonzero,
  * nothing is written.
  */

@@ -166,6 +166,10 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// The least of eight that are not NaN.
+__device__ __forceinline__ float least_of(const float2* x) {
+  return min3(min3(min3(x[0].x, x[0].y, x[1].x), x[1].y, x[2].x), min3(x[2].y, x[3].x, x[3].y), x[3].y);
+}
 
 __device__ __forceinline__ uint2 narrow_m(const float2* m, uint32_t s) {
   const float up = __uint_as_float((254u - s) << 23);
@@ -175,11 +179,12 @@ __device__ __forceinline__ uint2 narrow_m(const float2* m, uint32_t s) {
   for (int k = 0; k < 4; ++k) h[k] = __nv_cvt_float2_to_fp8x2(__fmul2_rn(m[k], up2), __NV_SATFINITE, __NV_E4M3);
   return s == 255u ? make_uint2(0u, 0u) : make_uint2(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
 }
-// r16: the elements' rounding bits, two per word (0x8000: nearest).  Two codes
+// r16: the elements' rounding bits, two per word (0x8000: nearest); least: of
+// the elements.  Two codes
 // at a time in the halves of a word: the fp32 patterns' upper halves, held
 // at the smallest code or above, less the base, shifted down to bytes.  The
 // scale keeps codes at most 255.
-__device__ __forceinline__ uint2 narrow_v(const float2* v, uint32_t s, const uint32_t* r16) {
+__device__ __forceinline__ uint2 narrow_v(const float2* v, uint32_t s, const uint32_t* r16, float least) {
   const uint32_t base16 = s * 0x00800080u, least16 = base16 + 0x00100010u;
   uint32_t h[4];
 #pragma unroll
@@ -189,8 +194,6 @@ __device__ __forceinline__ uint2 narrow_v(const float2* v, uint32_t s, const uin
     h[k] = (__vmaxu2(__byte_perm(a, b, 0x7632), least16) - base16) >> 4;  // codes in bytes 0 and 2
   }
   uint2 c = make_uint2(__byte_perm(h[0], h[1], 0x6420), __byte_perm(h[2], h[3], 0x6420));
-  const float least = min3(min3(min3(v[0].x, v[0].y, v[1].x), v[1].y, v[2].x), min3(v[2].y, v[3].x, v[3].y),
-                           v[3].y);
   if (least == 0.f) {  // zeros have code 0
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -205,11 +208,13 @@ __device__ __forceinline__ uint2 narrow_v(const float2* v, uint32_t s, const uin
 // do, and a packed sum of packed products would be compiled into a fused
 // multiply-add whatever its rounding mode says (found by comparing results
 // on sm_103a; 2 % of the instructions).  The weight's update takes the
-// hardware's approximate root and reciprocal, each within 2^-22 of the exact
-// (the root takes a subnormal v, below 1.2e-38, for 0: its root, 1e-19, is
-// far below any eps that matters).  Correctly rounded ones cost half of the
-// kernel's instructions, which then bound it: 5.0 ms against 3.8 on 1.35e9
-// elements.
+// hardware's approximate root and reciprocal, each within 2^-22 of the exact.
+// Correctly rounded ones cost half of the kernel's instructions, which then
+// bound it: 5.0 ms against 3.8 on 1.35e9 elements.  The root takes subnormals
+// for 0, and eps may be smaller than theirs (1.1e-19 at 2^-126), so a lane
+// that has such a v (or a zero) takes those roots again, 2^24 times as large:
+// a root that keeps them is 1 % slower on every element, and 11 % on tensors
+// off the vector grid.
 struct Adam8 {
   float2 inv_scale, c, decay, b1, b2, omb1, omb2, minus_size, inv_bc2, eps;
 };
@@ -228,17 +233,30 @@ __device__ __forceinline__ float2 sum2(float2 a, float2 b) {
   return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
 }
 // m arrives without its block's unit, which b1 carries (a power of two:
-// the product is the same).
-__device__ __forceinline__ void adamw_pairs(const Adam8& a, float2 b1_unit, float2* g, float2* w, float2* m, float2* v) {
+// the product is the same).  Returns the least v.
+__device__ __forceinline__ float adamw_pairs(const Adam8& a, float2 b1_unit, float2* g, float2* w, float2* m, float2* v) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const float2 gk = __fmul2_rn(__fmul2_rn(g[k], a.inv_scale), a.c);
     m[k] = sum2(__fmul2_rn(b1_unit, m[k]), __fmul2_rn(a.omb1, gk));
     v[k] = sum2(__fmul2_rn(a.b2, v[k]), __fmul2_rn(__fmul2_rn(a.omb2, gk), gk));
-    const float2 denom = __ffma2_rn(make_float2(root(v[k].x), root(v[k].y)), a.inv_bc2, a.eps);
+  }
+  float2 r[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) r[k] = make_float2(root(v[k].x), root(v[k].y));
+  const float least = least_of(v);
+  if (least < 0x1p-126f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (elem(v, j) < 0x1p-126f) elem(r, j) = __fmul_rn(root(__fmul_rn(elem(v, j), 0x1p24f)), 0x1p-12f);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 denom = __ffma2_rn(r[k], a.inv_bc2, a.eps);
     const float2 u = __fmul2_rn(m[k], make_float2(reciprocal(denom.x), reciprocal(denom.y)));
     w[k] = __ffma2_rn(a.minus_size, u, __fmul2_rn(w[k], a.decay));
   }
+  return least;
 }
 
 // Where a tile lies.  All of it is the same for the whole CTA, so that
@@ -364,7 +382,7 @@ __device__ __forceinline__ void step_block(const AdamSeg& sg, const Place8& a, u
   from_ring<GT>(slot, lane, g, w, mc, vc);
   widen_m(mc, m);
   widen_v(vc, scales >> 8, v);
-  adamw_pairs(ad, both(__fmul_rn(ad.b1.x, m_unit(scales & 0xFFu))), g, w, m, v);
+  const float least = adamw_pairs(ad, both(__fmul_rn(ad.b1.x, m_unit(scales & 0xFFu))), g, w, m, v);
   store8(at_offset(sg.weight + a.first, at), w);
   if constexpr (sizeof(PT) == 2) Eight<PT>::store(at_offset(static_cast<PT*>(sg.param) + a.first, at), w);
   const uint32_t ms = m_scale_of(block_top(m)), vs = v_scale_of(block_top(v));
@@ -377,7 +395,7 @@ __device__ __forceinline__ void step_block(const AdamSeg& sg, const Place8& a, u
     *at_offset(sg.v_scale + a.first / kMomentBlock, warp) = (uint8_t)vs;
   }
   __stcs(reinterpret_cast<uint2*>(at_offset(static_cast<uint8_t*>(sg.m) + a.first, at)), narrow_m(m, ms));
-  __stcs(reinterpret_cast<uint2*>(at_offset(static_cast<uint8_t*>(sg.v) + a.first, at)), narrow_v(v, vs, r16));
+  __stcs(reinterpret_cast<uint2*>(at_offset(static_cast<uint8_t*>(sg.v) + a.first, at)), narrow_v(v, vs, r16, least));
 }
 
 // Updates a block of n elements from element `first` of a tensor (its ragged
@@ -416,7 +434,7 @@ __device__ __forceinline__ void step_loose(const AdamSeg& sg, int64_t first, int
   }
   widen_m(make_uint2(mw[0], mw[1]), m);
   widen_v(make_uint2(vw[0], vw[1]), scales >> 8, v);
-  adamw_pairs(ad, both(__fmul_rn(ad.b1.x, m_unit(scales & 0xFFu))), g, w, m, v);
+  const float least = adamw_pairs(ad, both(__fmul_rn(ad.b1.x, m_unit(scales & 0xFFu))), g, w, m, v);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     if ((int)lane + j * 32 < n) {
@@ -433,7 +451,7 @@ __device__ __forceinline__ void step_loose(const AdamSeg& sg, int64_t first, int
     const uint32_t y = key + ((uint32_t)(first >> 1) + (lane >> 1) + k * 32) * kHashPair;
     r16[k] = __byte_perm(hash_pair(y), hash_pair(y + 16 * kHashPair), (lane & 1) ? 0x7632 : 0x5410);
   }
-  const uint2 mc = narrow_m(m, ms), vc = narrow_v(v, vs, r16);
+  const uint2 mc = narrow_m(m, ms), vc = narrow_v(v, vs, r16, least);
   if (lane == 0) {
     sg.m_scale[first / kMomentBlock] = (uint8_t)ms;
     sg.v_scale[first / kMomentBlock] = (uint8_t)vs;
@@ -512,9 +530,13 @@ __global__ void __launch_bounds__(kThreads, kCtas8) tensors_adamw8(const __grid_
   ad.b2 = both(p.b2);
   ad.omb1 = both(p.omb1);
   ad.omb2 = both(p.omb2);
-  ad.minus_size = both(p.dev ? -p.dev->step_size : -p.step_size);
-  ad.inv_bc2 = both(__fdiv_rn(1.f, p.dev ? p.dev->bc2_sqrt : p.bc2_sqrt));
-  ad.eps = both(fmaxf(p.eps, 0x1p-126f));  // the reciprocal takes subnormals for 0
+  // The reciprocal takes subnormals for 0, so a denominator near them is formed
+  // 2^24 times as large, as is the step size; 2^-126 there keeps an eps that
+  // is 0 in fp32 from dividing 0 by 0.
+  const float lift = p.eps < 0x1p-100f ? 0x1p24f : 1.f;
+  ad.minus_size = both(-lift * (p.dev ? p.dev->step_size : p.step_size));
+  ad.inv_bc2 = both(lift * __fdiv_rn(1.f, p.dev ? p.dev->bc2_sqrt : p.bc2_sqrt));
+  ad.eps = both(fmaxf(lift * p.eps, 0x1p-126f));
   ad.decay = both(decay_of_seg(p, p.seg[cur.si]));
   const uint32_t key = p.key + (p.d_step ? (uint32_t)*p.d_step * kHashStep : 0u);
   uint32_t slot = slot0, slot_ahead = slot0 + (kRing8 - 1) * Ring8::kSlot;
@@ -607,7 +629,7 @@ __device__ __forceinline__ uint2 pack_v_values(float2* v, uint32_t& s) {
   }
   s = v_scale_of(min(__reduce_max_sync(0xFFFFFFFFu, top), 0x7FFFFFFFu));
   const uint32_t nearest[4] = {0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u};
-  return narrow_v(v, s, nearest);
+  return narrow_v(v, s, nearest, least_of(v));
 }
 
 // A lane's elements of a block that is not read in vectors, and its codes'
