@@ -619,11 +619,12 @@ class TensorList:
         self.n = len(entries)
         self.c = (dopt_tensor * max(1, self.n))()
         self._keep = [dict(e) for e in entries]
-        self.devices = d = set()
+        self._state_devices = d = set()  # of all arrays but the grads
+        grad_devices = set()
         for k, e in enumerate(entries):
             t = self.c[k]
             param, n, pdt = _array(e, "param", e.get("numel"), _DTYPE, k, d)
-            t.grad, n, gdt = _array(e, "grad", n, _DTYPE, k, d)
+            t.grad, n, gdt = _array(e, "grad", n, _DTYPE, k, grad_devices)
             if n is None:
                 raise DoptError(E_INVALID, f"tensor {k}: numel is not given")
             t.numel, t.param = int(n), param
@@ -646,6 +647,7 @@ class TensorList:
             t.exp_avg_scale = _array(e, "exp_avg_scale", blocks, _CODES, k, d)[0]
             t.exp_avg_sq_scale = _array(e, "exp_avg_sq_scale", blocks, _CODES, k, d)[0]
             t.wd_mult = float(e.get("wd_mult", 1.0))
+        self.devices = d | grad_devices
 
     def set_grads(self, grads):
         """Points the tensors at other grads (same sizes and dtypes)."""
@@ -660,7 +662,7 @@ class TensorList:
         for k, (g, ptr) in enumerate(zip(grads, ptrs)):
             self.c[k].grad = ptr
             self._keep[k]["grad"] = g
-        self.devices |= d
+        self.devices = self._state_devices | d
 
 
 class MomentList:
