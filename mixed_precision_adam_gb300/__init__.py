@@ -593,12 +593,21 @@ def _array(entry, name, numel, dtypes, k, devices):
     return get(), n, dt
 
 
+def _current_device():
+    """The GPU that launches go to."""
+    import torch
+    return torch.cuda.current_device()
+
+
 def _listed(lst):
-    """The C arguments of a list whose tensors are on one GPU (pointers are
-    taken as they are)."""
+    """The C arguments of a list whose tensors are on the current GPU
+    (pointers are taken as they are)."""
     d = lst.devices
-    if len(d) > 1 or -1 in d:
-        raise DoptError(E_INVALID, "a list's tensors must be on one GPU")
+    if d:
+        if len(d) > 1 or -1 in d:
+            raise DoptError(E_INVALID, "a list's tensors must be on one GPU")
+        if _current_device() not in d:
+            raise DoptError(E_INVALID, f"the list's tensors are on GPU {min(d)}, not the current one")
     return lst.c, lst.n
 
 
