@@ -578,9 +578,7 @@ def _array(entry, name, numel, dtypes, k, devices):
         if hasattr(x, "__array_interface__"):
             raise DoptError(E_INVALID, f"tensor {k}: {name} is a host array")
         return _ptr(x), numel, None
-    dt = _dtype_names.get(x.dtype)
-    if dt is None:
-        dt = _dtype_names[x.dtype] = str(x.dtype).replace("torch.", "")
+    dt = _dtype_name(x.dtype)
     n = x.numel()
     if not x.is_contiguous():
         raise DoptError(E_INVALID, f"tensor {k}: {name} is not contiguous")
@@ -593,22 +591,77 @@ def _array(entry, name, numel, dtypes, k, devices):
     return get(), n, dt
 
 
+_one_gpu = None  # whether the process sees one GPU, asked once
+
+
 def _current_device():
     """The GPU that launches go to."""
+    global _one_gpu
+    if _one_gpu:
+        return 0
     import torch
+    if _one_gpu is None:
+        _one_gpu = torch.cuda.device_count() == 1
     return torch.cuda.current_device()
 
 
-def _listed(lst):
-    """The C arguments of a list whose tensors are on the current GPU
-    (pointers are taken as they are)."""
+def _gpu_of(lst):
+    """The current GPU, which a list's tensors must be on; None for a list of
+    pointers, which are taken as they are."""
     d = lst.devices
-    if d:
-        if len(d) > 1 or -1 in d:
-            raise DoptError(E_INVALID, "a list's tensors must be on one GPU")
-        if _current_device() not in d:
-            raise DoptError(E_INVALID, f"the list's tensors are on GPU {min(d)}, not the current one")
-    return lst.c, lst.n
+    if not d:
+        return None
+    if len(d) > 1 or -1 in d:
+        raise DoptError(E_INVALID, "a list's tensors must be on one GPU")
+    gpu = _current_device()
+    if gpu not in d:
+        raise DoptError(E_INVALID, f"the list's tensors are on GPU {min(d)}, not the current one")
+    return gpu
+
+
+def _scalar(x, name, dtype, gpu):
+    """Pointer of a call's scalar in device memory: a pointer, or a torch
+    tensor on the current GPU, of `dtype` or of as many bytes."""
+    if x is None:
+        return None
+    try:
+        if x.get_device() == gpu and _dtype_names.get(x.dtype) == dtype and (p := x.data_ptr()):
+            return p
+    except AttributeError:
+        pass
+    return _device_memory(x, name, dtype, 8 if dtype.endswith("64") else 4)
+
+
+def _workspace(x, size, gpu):
+    """The same for the workspace, of any type."""
+    try:
+        if x.get_device() == gpu and x.nbytes >= size:
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    return _device_memory(x, "workspace", None, size)
+
+
+def _device_memory(x, name, dtype, size):
+    if getattr(x, "data_ptr", None) is None:
+        if hasattr(x, "__array_interface__"):
+            raise DoptError(E_INVALID, f"{name} is a host array")
+        return _ptr(x)
+    at = x.get_device()
+    if at < 0 or at != _current_device():
+        raise DoptError(E_INVALID, f"{name} is on {'the host' if at < 0 else f'GPU {at}'}, not the current GPU")
+    if dtype is not None and _dtype_name(x.dtype) not in (dtype, "uint8"):
+        raise DoptError(E_INVALID, f"{name} is {_dtype_name(x.dtype)}, not {dtype}")
+    if x.nbytes < size:
+        raise DoptError(E_SIZE, f"{name} has {x.nbytes} bytes, not {size}")
+    return x.data_ptr()
+
+
+def _dtype_name(dtype):
+    name = _dtype_names.get(dtype)
+    if name is None:
+        name = _dtype_names[dtype] = str(dtype).replace("torch.", "")
+    return name
 
 
 _hp_bytes = struct.Struct("=5dq").pack  # dopt_adamw_hparams
@@ -718,37 +771,46 @@ def dopt_tensors_grad_norm(tensors, inv_loss_scale, max_norm, workspace, workspa
                            d_clip_coef, d_found_inf, stream=None):
     """Grad norm, clip coefficient and non-finite flag (device scalars) of a
     TensorList."""
-    _check(_c["dopt_tensors_grad_norm"](*_listed(tensors), inv_loss_scale, max_norm, _ptr(workspace),
-                                        workspace_bytes, _ptr(d_norm), _ptr(d_clip_coef), _ptr(d_found_inf),
-                                        _stream(stream)))
+    gpu = _gpu_of(tensors)
+    _check(_c["dopt_tensors_grad_norm"](tensors.c, tensors.n, inv_loss_scale, max_norm,
+                                        _workspace(workspace, workspace_bytes, gpu), workspace_bytes,
+                                        _scalar(d_norm, "d_norm", "float32", gpu),
+                                        _scalar(d_clip_coef, "d_clip_coef", "float32", gpu),
+                                        _scalar(d_found_inf, "d_found_inf", "int32", gpu), _stream(stream)))
 
 
 def dopt_tensors_adam_step(tensors, hp, step, inv_loss_scale=1.0, seed=0, d_clip_coef=None,
                            d_found_inf=None, stream=None):
     """AdamW over a TensorList; seed: of the 8-bit second moments' rounding."""
+    gpu = _gpu_of(tensors)
     h = _hp_bytes(hp["lr"], hp["beta1"], hp["beta2"], hp["eps"], hp["weight_decay"], int(step))
-    _check(_c["dopt_tensors_adam_step"](*_listed(tensors), h, inv_loss_scale,
-                                        seed & 0xFFFFFFFF, _ptr(d_clip_coef), _ptr(d_found_inf),
-                                        _stream(stream)))
+    _check(_c["dopt_tensors_adam_step"](tensors.c, tensors.n, h, inv_loss_scale, seed & 0xFFFFFFFF,
+                                        _scalar(d_clip_coef, "d_clip_coef", "float32", gpu),
+                                        _scalar(d_found_inf, "d_found_inf", "int32", gpu), _stream(stream)))
 
 
 def dopt_tensors_step(tensors, hp, step, workspace, workspace_bytes, *, inv_loss_scale=1.0, max_norm=1.0,
                       seed=0, d_step=None, d_lr=None, d_found_inf=None, d_norm=None, stream=None):
     """Grad norm, clip, skip and AdamW over a TensorList, without waiting."""
+    gpu = _gpu_of(tensors)
     h = _hp_bytes(hp["lr"], hp["beta1"], hp["beta2"], hp["eps"], hp["weight_decay"], int(step))
-    _check(_c["dopt_tensors_step"](*_listed(tensors), h, inv_loss_scale, max_norm,
-                                   seed & 0xFFFFFFFF, _ptr(d_step), _ptr(d_lr), _ptr(workspace),
-                                   workspace_bytes, _ptr(d_found_inf), _ptr(d_norm), _stream(stream)))
+    _check(_c["dopt_tensors_step"](tensors.c, tensors.n, h, inv_loss_scale, max_norm, seed & 0xFFFFFFFF,
+                                   _scalar(d_step, "d_step", "int64", gpu), _scalar(d_lr, "d_lr", "float64", gpu),
+                                   _workspace(workspace, workspace_bytes, gpu), workspace_bytes,
+                                   _scalar(d_found_inf, "d_found_inf", "int32", gpu),
+                                   _scalar(d_norm, "d_norm", "float32", gpu), _stream(stream)))
 
 
 def dopt_state8_pack(moments, stream=None):
     """The values of a MomentList into its 8-bit codes and scales."""
-    _check(_c["dopt_state8_pack"](*_listed(moments), _stream(stream)))
+    _gpu_of(moments)
+    _check(_c["dopt_state8_pack"](moments.c, moments.n, _stream(stream)))
 
 
 def dopt_state8_unpack(moments, stream=None):
     """The codes and scales of a MomentList into its values."""
-    _check(_c["dopt_state8_unpack"](*_listed(moments), _stream(stream)))
+    _gpu_of(moments)
+    _check(_c["dopt_state8_unpack"](moments.c, moments.n, _stream(stream)))
 
 
 def exported_symbols():

@@ -55,8 +55,9 @@ class OnGpu:
     def numel(self):
         return self.n
 
-    def element_size(self):
-        return self.dtype.itemsize
+    @property
+    def nbytes(self):
+        return self.n * self.dtype.itemsize
 
     def is_contiguous(self):
         return True
@@ -84,3 +85,44 @@ def test_lists_of_another_gpu_than_the_current(monkeypatch):
     monkeypatch.setattr(dopt, "_current_device", lambda: 1, raising=False)
     assert "hyper-parameters" in refusal(lst)
     assert "one GPU" in refusal(both)
+
+
+def calls_with(lst, name, x):
+    """Every call that takes the device argument `name`, each refused at the latest for what is wrong with the list
+    or the step number."""
+    ws = dopt.dopt_tensors_workspace_bytes(1)
+    step = dict(workspace=4096, workspace_bytes=ws, d_step=None, d_lr=None, d_found_inf=None, d_norm=None)
+    norm = dict(workspace=4096, workspace_bytes=ws, d_norm=None, d_clip_coef=None, d_found_inf=None)
+    adam = dict(d_clip_coef=None, d_found_inf=None)
+    out = []
+    if name in step:
+        out.append(lambda: dopt.dopt_tensors_step(lst, HP, 0, **dict(step, **{name: x})))
+    if name in norm:
+        out.append(lambda: dopt.dopt_tensors_grad_norm(lst, float("inf"), 1.0, **dict(norm, **{name: x})))
+    if name in adam:
+        out.append(lambda: dopt.dopt_tensors_adam_step(lst, HP, 0, **dict(adam, **{name: x})))
+    return out
+
+
+@pytest.mark.parametrize("name,dtype", [
+    ("workspace", torch.uint8), ("d_step", torch.int64), ("d_lr", torch.float64), ("d_found_inf", torch.int32),
+    ("d_norm", torch.float32), ("d_clip_coef", torch.float32)])
+def test_device_arguments(monkeypatch, name, dtype):
+    """The workspace and the scalars go to the kernels too: host memory, another GPU's, another type or fewer bytes
+    are refused."""
+    monkeypatch.setattr(dopt, "_current_device", lambda: 1, raising=False)
+    lst = dopt.TensorList([entry()])
+    need = dopt.dopt_tensors_workspace_bytes(1) if name == "workspace" else 1
+    other = torch.bool if dtype != torch.uint8 else None
+    for good in (4096, OnGpu(1, need, dtype), OnGpu(1, need * 8, torch.uint8)):
+        for call in calls_with(lst, name, good):
+            assert "hyper-parameters" in (text := refused(call)) or "inv_loss_scale" in text
+    for bad, status in ((torch.zeros(need, dtype=dtype), dopt.E_INVALID), (torch.zeros(need, dtype=dtype).numpy(), dopt.E_INVALID),
+                        (OnGpu(0, need, dtype), dopt.E_INVALID), (OnGpu(1, need, other), dopt.E_INVALID),
+                        (OnGpu(1, need - 1, dtype), dopt.E_SIZE)):
+        if getattr(bad, "dtype", 0) is None:
+            continue
+        for call in calls_with(lst, name, bad):
+            with pytest.raises(dopt.DoptError) as err:
+                call()
+            assert err.value.status == status and name in str(err.value), err.value
