@@ -721,7 +721,8 @@ size_t dopt_tensors_workspace_bytes(int32_t n_tensors);
  *   *d_clip_coef = max_norm / (norm + 1e-6) when max_norm > 0 and that is
  *                  < 1, else 1;
  *   *d_found_inf = 1 if any g is non-finite.
- * Any of the three may be NULL.  Only grad, grad_dtype and numel of the
+ * Any of the three may be NULL, and each needs 4-byte alignment only (so too
+ * below).  Only grad, grad_dtype and numel of the
  * tensors are used.  Squares are added in fp32 over 16 elements, those
  * sums with their rounding errors in fp32, then in fp64, in a fixed order: the same list gives the same bits
  * on the same kind of GPU.  Elements whose squares would leave the fp32 range

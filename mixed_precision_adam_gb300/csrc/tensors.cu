@@ -105,6 +105,12 @@ int check_norm_args(int32_t n, float inv_scale, double max_norm, const void* ws,
   return DOPT_OK;
 }
 
+// The 4-byte device scalars of a call (any may be NULL).
+int check_scalars(const float* norm, const float* coef, const int32_t* found, const char* fn) {
+  if (aligned_to(norm, 4) && aligned_to(coef, 4) && aligned_to(found, 4)) return DOPT_OK;
+  return fail(DOPT_E_ALIGN, std::string(fn) + ": a norm, clip coefficient or found_inf not 4-byte aligned");
+}
+
 char* ws_at(void* ws, size_t offset) { return static_cast<char*>(ws) + offset; }
 
 // A table's record of tiles outside their tensor (debug builds).
@@ -338,6 +344,7 @@ int dopt_tensors_grad_norm(const dopt_tensor* tensors, int32_t n_tensors, float 
     int st = check_grads(tensors, n_tensors, fn);
     if (st) return st;
     if ((st = check_norm_args(n_tensors, inv_loss_scale, max_norm, workspace, workspace_bytes, fn))) return st;
+    if ((st = check_scalars(d_norm, d_clip_coef, d_found_inf, fn))) return st;
     FinalizeArgs f{};
     f.max_norm = max_norm;
     f.sc = static_cast<Scalars*>(workspace);
@@ -356,6 +363,7 @@ int dopt_tensors_adam_step(const dopt_tensor* tensors, int32_t n_tensors, const 
     int st = check_states(tensors, n_tensors, fn);
     if (st) return st;
     if ((st = check_hp(hp, inv_loss_scale, fn))) return st;
+    if ((st = check_scalars(nullptr, d_clip_coef, d_found_inf, fn))) return st;
     AdamJob j{hp, inv_loss_scale, seed, d_clip_coef, d_found_inf};
     return run_adamw(tensors, n_tensors, j, (cudaStream_t)stream);
   });
@@ -371,6 +379,7 @@ int dopt_tensors_step(const dopt_tensor* tensors, int32_t n_tensors, const dopt_
     if (st) return st;
     if ((st = check_hp(hp, inv_loss_scale, fn))) return st;
     if ((st = check_norm_args(n_tensors, inv_loss_scale, max_norm, workspace, workspace_bytes, fn))) return st;
+    if ((st = check_scalars(d_norm, nullptr, d_found_inf, fn))) return st;
     if (!aligned_to(d_step, 8) || !aligned_to(d_lr, 8))
       return fail(DOPT_E_ALIGN, std::string(fn) + ": d_step / d_lr not 8-byte aligned");
     FinalizeArgs f{};

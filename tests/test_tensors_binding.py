@@ -126,3 +126,20 @@ def test_device_arguments(monkeypatch, name, dtype):
             with pytest.raises(dopt.DoptError) as err:
                 call()
             assert err.value.status == status and name in str(err.value), err.value
+
+
+@pytest.mark.parametrize("call", ["grad_norm", "adam_step", "step"])
+def test_misaligned_scalars(call):
+    """The kernels write and read the 4-byte scalars whole."""
+    lst, ws = dopt.TensorList([entry()]), dopt.dopt_tensors_workspace_bytes(1)
+    for at in (4097, 4098, 4099):
+        for k in range(dict(grad_norm=3, adam_step=2, step=2)[call]):
+            p = [at if j == k else None for j in range(3)]
+            with pytest.raises(dopt.DoptError) as err:
+                if call == "grad_norm":
+                    dopt.dopt_tensors_grad_norm(lst, 1.0, 1.0, 4096, ws, *p)
+                elif call == "adam_step":
+                    dopt.dopt_tensors_adam_step(lst, HP, 1, d_clip_coef=p[0], d_found_inf=p[1])
+                else:
+                    dopt.dopt_tensors_step(lst, HP, 1, 4096, ws, d_found_inf=p[0], d_norm=p[1])
+            assert err.value.status == dopt.E_ALIGN, err.value
