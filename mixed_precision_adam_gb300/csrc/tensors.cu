@@ -78,9 +78,9 @@ int check_states(const dopt_tensor* ts, int32_t n, const char* fn) {
   return DOPT_OK;
 }
 
-int check_hp(const dopt_adamw_hparams* hp, float inv_scale, const char* fn) {
+int check_hp(const dopt_adamw_hparams* hp, bool device_step, float inv_scale, const char* fn) {
   if (!hp) return fail(DOPT_E_INVALID, std::string(fn) + ": NULL hparams");
-  const bool ok = hp->step >= 1 && std::isfinite(hp->lr) && hp->lr >= 0 && hp->beta1 >= 0 && hp->beta1 < 1 &&
+  const bool ok = (device_step || hp->step >= 1) && std::isfinite(hp->lr) && hp->lr >= 0 && hp->beta1 >= 0 && hp->beta1 < 1 &&
                   hp->beta2 >= 0 && hp->beta2 < 1 && std::isfinite(hp->eps) && hp->eps > 0 &&
                   std::isfinite(hp->weight_decay);
   if (!ok) return fail(DOPT_E_INVALID, std::string(fn) + ": bad AdamW hyper-parameters");
@@ -362,7 +362,7 @@ int dopt_tensors_adam_step(const dopt_tensor* tensors, int32_t n_tensors, const 
   return guarded(fn, [&]() -> int {
     int st = check_states(tensors, n_tensors, fn);
     if (st) return st;
-    if ((st = check_hp(hp, inv_loss_scale, fn))) return st;
+    if ((st = check_hp(hp, false, inv_loss_scale, fn))) return st;
     if ((st = check_scalars(nullptr, d_clip_coef, d_found_inf, fn))) return st;
     AdamJob j{hp, inv_loss_scale, seed, d_clip_coef, d_found_inf};
     return run_adamw(tensors, n_tensors, j, (cudaStream_t)stream);
@@ -377,7 +377,7 @@ int dopt_tensors_step(const dopt_tensor* tensors, int32_t n_tensors, const dopt_
   return guarded(fn, [&]() -> int {
     int st = check_states(tensors, n_tensors, fn);
     if (st) return st;
-    if ((st = check_hp(hp, inv_loss_scale, fn))) return st;
+    if ((st = check_hp(hp, d_step != nullptr, inv_loss_scale, fn))) return st;
     if ((st = check_norm_args(n_tensors, inv_loss_scale, max_norm, workspace, workspace_bytes, fn))) return st;
     if ((st = check_scalars(d_norm, nullptr, d_found_inf, fn))) return st;
     if (!aligned_to(d_step, 8) || !aligned_to(d_lr, 8))

@@ -62,3 +62,17 @@ def test_step_with_subnormal_second_moments(moments, eps, size):
     for step in (1, 2, 3):
         dopt.dopt_tensors_adam_step(case.list, hp, step)
         check_small_step(case, step, hp)
+
+
+@pytest.mark.parametrize("moments", [8, 32])
+@pytest.mark.parametrize("host_step", [0, -7])
+def test_host_step_is_ignored_with_a_device_step(moments, host_step):
+    """With the count on the device the host's is not looked at: the same bits whatever it is."""
+    spec = [dict(numel=5000, param="bf16", grad="bf16", moments=moments)]
+    one, two = Case(spec, seed=18), Case(spec, seed=18)
+    ws = torch.zeros(dopt.dopt_tensors_workspace_bytes(1), dtype=torch.uint8, device="cuda")
+    for case, step in ((one, 1), (two, host_step)):
+        count = torch.tensor([4], dtype=torch.int64, device="cuda")
+        dopt.dopt_tensors_step(case.list, HP, step, ws, ws.numel(), seed=3, d_step=count)
+        assert count.item() == 5
+    assert all(np.array_equal(x, y) for x, y in zip(one.values()[0].values(), two.values()[0].values()))
