@@ -10,6 +10,7 @@ package fails loudly when the library has not been built.
 import ctypes
 import os
 import struct
+import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # DOPT_LIBRARY may name another in-tree build of the same library (the
@@ -608,15 +609,19 @@ def _current_device():
 def _gpu_of(lst):
     """The current GPU, which a list's tensors must be on; None for a list of
     pointers, which are taken as they are."""
-    d = lst.devices
-    if not d:
-        return None
-    if len(d) > 1 or -1 in d:
-        raise DoptError(E_INVALID, "a list's tensors must be on one GPU")
-    gpu = _current_device()
-    if gpu not in d:
-        raise DoptError(E_INVALID, f"the list's tensors are on GPU {min(d)}, not the current one")
+    gpu = lst.gpu
+    if gpu is not None:
+        if gpu < 0:
+            raise DoptError(E_INVALID, "a list's tensors must be on one GPU")
+        if gpu != _current_device():
+            raise DoptError(E_INVALID, f"the list's tensors are on GPU {gpu}, not the current one")
     return gpu
+
+
+def _one_device(devices):
+    """The GPU of a list whose tensors are on these devices: None where there
+    are none (pointers only), -1 where they are not on one GPU."""
+    return None if not devices else min(devices) if len(devices) == 1 else -1
 
 
 def _scalar(x, name, dtype, gpu):
@@ -625,9 +630,9 @@ def _scalar(x, name, dtype, gpu):
     if x is None:
         return None
     try:
-        if x.get_device() == gpu and _dtype_names.get(x.dtype) == dtype and (p := x.data_ptr()):
+        if x.get_device() == gpu and _dtype_names[x.dtype] is dtype and (p := x.data_ptr()):
             return p
-    except AttributeError:
+    except (AttributeError, KeyError):
         pass
     return _device_memory(x, name, dtype, 8 if dtype.endswith("64") else 4)
 
@@ -660,7 +665,7 @@ def _device_memory(x, name, dtype, size):
 def _dtype_name(dtype):
     name = _dtype_names.get(dtype)
     if name is None:
-        name = _dtype_names[dtype] = str(dtype).replace("torch.", "")
+        name = _dtype_names[dtype] = sys.intern(str(dtype).replace("torch.", ""))
     return name
 
 
@@ -680,6 +685,7 @@ class TensorList:
     def __init__(self, entries):
         self.n = len(entries)
         self.c = (dopt_tensor * max(1, self.n))()
+        self.address = ctypes.addressof(self.c)
         self._keep = [dict(e) for e in entries]
         self._state_devices = d = set()  # of all arrays but the grads
         grad_devices = set()
@@ -709,7 +715,7 @@ class TensorList:
             t.exp_avg_scale = _array(e, "exp_avg_scale", blocks, _CODES, k, d)[0]
             t.exp_avg_sq_scale = _array(e, "exp_avg_sq_scale", blocks, _CODES, k, d)[0]
             t.wd_mult = float(e.get("wd_mult", 1.0))
-        self.devices = d | grad_devices
+        self.gpu = _one_device(d | grad_devices)
 
     def set_grads(self, grads):
         """Points the tensors at other grads (same sizes and dtypes)."""
@@ -724,7 +730,7 @@ class TensorList:
         for k, (g, ptr) in enumerate(zip(grads, ptrs)):
             self.c[k].grad = ptr
             self._keep[k]["grad"] = g
-        self.devices = self._state_devices | d
+        self.gpu = _one_device(self._state_devices | d)
 
 
 class MomentList:
@@ -737,8 +743,9 @@ class MomentList:
     def __init__(self, entries):
         self.n = len(entries)
         self.c = (dopt_moment_tensor * max(1, self.n))()
+        self.address = ctypes.addressof(self.c)
         self._keep = [dict(e) for e in entries]
-        self.devices = d = set()
+        d = set()
         for k, e in enumerate(entries):
             t = self.c[k]
             t.exp_avg, n, mdt = _array(e, "exp_avg", e.get("numel"), _VALUES, k, d)
@@ -753,6 +760,7 @@ class MomentList:
             for name in ("exp_avg", "exp_avg_sq"):
                 setattr(t, name + "_codes", _array(e, name + "_codes", t.numel, _CODES, k, d)[0])
                 setattr(t, name + "_scale", _array(e, name + "_scale", blocks, _CODES, k, d)[0])
+        self.gpu = _one_device(d)
 
 
 def dopt_moment_blocks(numel):
@@ -772,7 +780,7 @@ def dopt_tensors_grad_norm(tensors, inv_loss_scale, max_norm, workspace, workspa
     """Grad norm, clip coefficient and non-finite flag (device scalars) of a
     TensorList."""
     gpu = _gpu_of(tensors)
-    _check(_c["dopt_tensors_grad_norm"](tensors.c, tensors.n, inv_loss_scale, max_norm,
+    _check(_c["dopt_tensors_grad_norm"](tensors.address, tensors.n, inv_loss_scale, max_norm,
                                         _workspace(workspace, workspace_bytes, gpu), workspace_bytes,
                                         _scalar(d_norm, "d_norm", "float32", gpu),
                                         _scalar(d_clip_coef, "d_clip_coef", "float32", gpu),
@@ -784,7 +792,7 @@ def dopt_tensors_adam_step(tensors, hp, step, inv_loss_scale=1.0, seed=0, d_clip
     """AdamW over a TensorList; seed: of the 8-bit second moments' rounding."""
     gpu = _gpu_of(tensors)
     h = _hp_bytes(hp["lr"], hp["beta1"], hp["beta2"], hp["eps"], hp["weight_decay"], int(step))
-    _check(_c["dopt_tensors_adam_step"](tensors.c, tensors.n, h, inv_loss_scale, seed & 0xFFFFFFFF,
+    _check(_c["dopt_tensors_adam_step"](tensors.address, tensors.n, h, inv_loss_scale, seed & 0xFFFFFFFF,
                                         _scalar(d_clip_coef, "d_clip_coef", "float32", gpu),
                                         _scalar(d_found_inf, "d_found_inf", "int32", gpu), _stream(stream)))
 
@@ -794,7 +802,7 @@ def dopt_tensors_step(tensors, hp, step, workspace, workspace_bytes, *, inv_loss
     """Grad norm, clip, skip and AdamW over a TensorList, without waiting."""
     gpu = _gpu_of(tensors)
     h = _hp_bytes(hp["lr"], hp["beta1"], hp["beta2"], hp["eps"], hp["weight_decay"], int(step))
-    _check(_c["dopt_tensors_step"](tensors.c, tensors.n, h, inv_loss_scale, max_norm, seed & 0xFFFFFFFF,
+    _check(_c["dopt_tensors_step"](tensors.address, tensors.n, h, inv_loss_scale, max_norm, seed & 0xFFFFFFFF,
                                    _scalar(d_step, "d_step", "int64", gpu), _scalar(d_lr, "d_lr", "float64", gpu),
                                    _workspace(workspace, workspace_bytes, gpu), workspace_bytes,
                                    _scalar(d_found_inf, "d_found_inf", "int32", gpu),
@@ -804,13 +812,13 @@ def dopt_tensors_step(tensors, hp, step, workspace, workspace_bytes, *, inv_loss
 def dopt_state8_pack(moments, stream=None):
     """The values of a MomentList into its 8-bit codes and scales."""
     _gpu_of(moments)
-    _check(_c["dopt_state8_pack"](moments.c, moments.n, _stream(stream)))
+    _check(_c["dopt_state8_pack"](moments.address, moments.n, _stream(stream)))
 
 
 def dopt_state8_unpack(moments, stream=None):
     """The codes and scales of a MomentList into its values."""
     _gpu_of(moments)
-    _check(_c["dopt_state8_unpack"](moments.c, moments.n, _stream(stream)))
+    _check(_c["dopt_state8_unpack"](moments.address, moments.n, _stream(stream)))
 
 
 def exported_symbols():
