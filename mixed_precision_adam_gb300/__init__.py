@@ -718,7 +718,9 @@ class TensorList:
         self.gpu = _one_device(d | grad_devices)
 
     def set_grads(self, grads):
-        """Points the tensors at other grads (same sizes and dtypes)."""
+        """Points the tensors at other grads (same sizes and dtypes, one for
+        every tensor).  The list lets go of the old ones, which a step still
+        queued on a stream other than their own must outlive."""
         if len(grads) != self.n:
             raise DoptError(E_INVALID, f"{len(grads)} grads for {self.n} tensors")
         ptrs, d = [], set()
