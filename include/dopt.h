@@ -647,8 +647,9 @@ int dopt_state_from_model(const dopt_shard_map* map, int32_t buffer, int32_t ran
  * and has `numel` elements; it needs only its own elements' alignment (4
  * bytes for fp32, 2 for bf16/fp16, 1 for codes) -- a tensor whose arrays
  * start at one element offset from 16-byte boundaries (fp32 moments), or on
- * 32-byte boundaries (8-bit moments), is read in vectors, others by element.  Arrays of one
- * call must not overlap, but for the list's read-only grads.
+ * 16-byte boundaries, 32 for fp32 weights (8-bit moments), is read in
+ * vectors, others by element, which takes 1.5 to 1.8 times as long.  Arrays
+ * of one call must not overlap, but for the list's read-only grads.
  *
  * Moments are held in fp32, or in 8 bits per element (DOPT_MOMENTS_8BIT,
  * per tensor; one list may hold both).  The 8-bit moments of a tensor are
@@ -738,8 +739,9 @@ int dopt_tensors_grad_norm(const dopt_tensor* tensors, int32_t n_tensors, float 
  * AdamW over a list of tensors, with
  *   g = (fp32(grad) * inv_loss_scale) * (*d_clip_coef).
  * fp32 moments: per element the arithmetic of dopt_adam_step, bit for bit.
- * 8-bit moments: the same moments' arithmetic on the stored values widened;
- * the new moments step the weight and are then rounded to codes.  The root
+ * 8-bit moments: the same moments' arithmetic on the stored values widened
+ * (bit for bit; with a beta1 below 2^-7, exp_avg to within 2^-141); the new
+ * moments step the weight and are then rounded to codes.  The root
  * and the division of the weight's update are approximate there (a few fp32
  * ulps of the update, subnormal second moments included); an eps that is 0
  * in fp32 counts as 2^-150.  `seed` is the stochastic rounding's.

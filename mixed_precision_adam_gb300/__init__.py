@@ -680,7 +680,9 @@ class TensorList:
     (uint8, dopt_moment_blocks(numel) each); optional wd_mult (1.0).  Arrays
     are contiguous torch tensors, whose sizes and dtypes are checked and
     used, or device pointers; an entry of pointers also gives numel,
-    param_dtype, grad_dtype and moments."""
+    param_dtype, grad_dtype and moments.  The calls refuse tensors, workspaces
+    and scalars that are not on the current GPU; pointers are taken as they
+    are."""
 
     def __init__(self, entries):
         self.n = len(entries)

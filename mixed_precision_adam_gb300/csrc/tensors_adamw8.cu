@@ -10,8 +10,8 @@
 // elements per instruction, codes are made two at a time, and the inputs
 // come through a ring in shared memory.  A warp has a block of 256 elements
 // at a time, so a block's largest moments are one warp reduction each.
-// Measured on 1.35e9 bf16 elements: 3.13 ms, 6.88 TB/s (1.02 of the copy
-// bandwidth); as many fp32 params and grads: 3.05 ms, 7.1 TB/s.
+// Measured on 1.35e9 bf16 elements: 3.14 ms, 6.9 TB/s (1.02 of the copy
+// bandwidth); as many fp32 params and grads: 3.06 ms, 7.05 TB/s.
 #include <cuda_fp8.h>
 
 #include "tensors.cuh"
@@ -212,9 +212,9 @@ __device__ __forceinline__ uint2 narrow_v(const float2* v, uint32_t s, const uin
 // Correctly rounded ones cost half of the kernel's instructions, which then
 // bound it: 5.0 ms against 3.8 on 1.35e9 elements.  The root takes subnormals
 // for 0, and eps may be smaller than theirs (1.1e-19 at 2^-126), so a lane
-// that has such a v (or a zero) takes those roots again, 2^24 times as large:
-// a root that keeps them is 1 % slower on every element, and 11 % on tensors
-// off the vector grid.
+// that has such a v (or a zero) takes those roots again, of v 2^24 times as
+// large (0.1 to 0.5 %; a root that keeps subnormals in every lane costs 0.7 to
+// 1.5 %, and 11 % on tensors off the vector grid).
 struct Adam8 {
   float2 inv_scale, c, decay, b1, b2, omb1, omb2, minus_size, inv_bc2, eps;
 };
@@ -232,8 +232,11 @@ __device__ __forceinline__ float reciprocal(float x) {
 __device__ __forceinline__ float2 sum2(float2 a, float2 b) {
   return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
 }
-// m arrives without its block's unit, which b1 carries (a power of two:
-// the product is the same).  Returns the least v.
+// m arrives without its block's unit, which b1 carries (a power of two: the
+// product is the same, unless b1 times the unit is subnormal, which takes a b1
+// below 2^-7: at most 2^-141 off, where codes are 2^-128 apart or more.
+// Multiplying m by the unit first instead, under a branch on b1, costs 0.3 %,
+// and 7 % off the vector grid).  Returns the least v.
 __device__ __forceinline__ float adamw_pairs(const Adam8& a, float2 b1_unit, float2* g, float2* w, float2* m, float2* v) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
