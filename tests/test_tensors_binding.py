@@ -1,12 +1,13 @@
 """The binding of the step over a list of tensors without a GPU: which GPU's
-memory a call may be given.  Every call here is refused before any launch: a
-step number of 0 is, by the library, where the binding lets a call through."""
+memory a call may be given.  Every call here is refused before any launch: by
+the library, for a negative learning rate, where the binding lets it through."""
 
 import pytest
 import torch
 
 dopt = pytest.importorskip("mixed_precision_adam_gb300")
 HP = dict(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1)
+BAD = dict(HP, lr=-1.0)
 
 
 def entry(**kw):
@@ -25,8 +26,8 @@ def refused(call):
 
 
 def refusal(lst):
-    """Why a step of step number 0 is refused."""
-    return refused(lambda: dopt.dopt_tensors_adam_step(lst, HP, 0))
+    """Why a step with a bad learning rate is refused."""
+    return refused(lambda: dopt.dopt_tensors_adam_step(lst, BAD, 1))
 
 
 def test_good_grads_after_bad_ones():
@@ -77,8 +78,8 @@ def test_lists_of_another_gpu_than_the_current(monkeypatch):
     both = dopt.TensorList([on_gpu(1), on_gpu(0)])
     ws = dopt.dopt_tensors_workspace_bytes(1)
     monkeypatch.setattr(dopt, "_current_device", lambda: 0, raising=False)
-    for call in (lambda: dopt.dopt_tensors_adam_step(lst, HP, 1), lambda: dopt.dopt_tensors_step(lst, HP, 1, 4096, ws),
-                 lambda: dopt.dopt_tensors_grad_norm(lst, 1.0, 1.0, 4096, ws, None, None, None),
+    for call in (lambda: dopt.dopt_tensors_adam_step(lst, BAD, 1), lambda: dopt.dopt_tensors_step(lst, BAD, 1, 4096, ws),
+                 lambda: dopt.dopt_tensors_grad_norm(lst, float("inf"), 1.0, 4096, ws, None, None, None),
                  lambda: dopt.dopt_state8_pack(dopt.MomentList([moments])),
                  lambda: dopt.dopt_state8_unpack(dopt.MomentList([moments]))):
         assert "GPU 1" in refused(call)
@@ -88,19 +89,19 @@ def test_lists_of_another_gpu_than_the_current(monkeypatch):
 
 
 def calls_with(lst, name, x):
-    """Every call that takes the device argument `name`, each refused at the latest for what is wrong with the list
-    or the step number."""
+    """Every call that takes the device argument `name`, each refused at the latest for its learning rate or loss
+    scale."""
     ws = dopt.dopt_tensors_workspace_bytes(1)
     step = dict(workspace=4096, workspace_bytes=ws, d_step=None, d_lr=None, d_found_inf=None, d_norm=None)
     norm = dict(workspace=4096, workspace_bytes=ws, d_norm=None, d_clip_coef=None, d_found_inf=None)
     adam = dict(d_clip_coef=None, d_found_inf=None)
     out = []
     if name in step:
-        out.append(lambda: dopt.dopt_tensors_step(lst, HP, 0, **dict(step, **{name: x})))
+        out.append(lambda: dopt.dopt_tensors_step(lst, BAD, 1, **dict(step, **{name: x})))
     if name in norm:
         out.append(lambda: dopt.dopt_tensors_grad_norm(lst, float("inf"), 1.0, **dict(norm, **{name: x})))
     if name in adam:
-        out.append(lambda: dopt.dopt_tensors_adam_step(lst, HP, 0, **dict(adam, **{name: x})))
+        out.append(lambda: dopt.dopt_tensors_adam_step(lst, BAD, 1, **dict(adam, **{name: x})))
     return out
 
 
