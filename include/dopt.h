@@ -787,6 +787,177 @@ typedef struct {
 int dopt_state8_pack(const dopt_moment_tensor* tensors, int32_t n_tensors, dopt_stream stream);
 int dopt_state8_unpack(const dopt_moment_tensor* tensors, int32_t n_tensors, dopt_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * Training in 8 bits next to the step: matrices of 8-bit codes, their
+ * products, the RMS norm and dropout around them.
+ *
+ * A dopt_matrix8 holds rows x cols numbers as e4m3 codes, row-major, with one
+ * scale byte for each block of DOPT_MATRIX_BLOCK consecutive columns of a row
+ * (the last block of a row may be shorter).  A number is
+ *   e4m3 code x 2^(s - 127),  s = max(E - 8, 8),
+ *   E = (bits(max |x| of the block) + 0x1FFFFF) >> 23,
+ * rounded to nearest even: the encoding of the 8-bit exp_avg.  Where E >= 255
+ * (a number that is infinite, NaN or above the largest value) the block's
+ * codes are 0, its scale byte is 255, and all of it reads as NaN.  With
+ * DOPT_BLOCK_SQUARE the maximum is taken over DOPT_MATRIX_BLOCK rows and
+ * columns, and their rows share the byte: then a matrix and its transpose
+ * hold the same numbers, as weights should.
+ * The scale bytes lie in the order that the matrix unit reads them, 128 rows
+ * by four blocks in 512 bytes: with nb = ceil(cols / 128), the byte of row r
+ * and block b is at
+ *   ((r / 128) * ceil(nb / 4) + b / 4) * 512
+ *     + (r % 32) * 16 + (r % 128 / 32) * 4 + b % 4.
+ * Neither the codes between cols and ld nor the scale bytes of rows and
+ * blocks that are not there are written, or matter.
+ */
+#define DOPT_MATRIX_BLOCK 128
+
+typedef struct {
+  int64_t rows, cols; /* >= 0, below 2^31                                    */
+  int64_t ld;         /* bytes from a row to the next: >= cols, and a
+                         multiple of 16                                      */
+  uint8_t* codes;     /* 16-byte aligned                                     */
+  uint8_t* scales;    /* dopt_matrix8_scale_bytes bytes, 16-byte aligned     */
+} dopt_matrix8;
+
+typedef enum {
+  DOPT_BLOCK_ROW = 0,   /* a scale per 128 columns of a row                  */
+  DOPT_BLOCK_SQUARE = 1 /* a scale per 128 x 128 square                      */
+} dopt_block;
+
+/* Scale bytes of a rows x cols matrix; DOPT_E_INVALID for a negative size,
+ * DOPT_E_SIZE from 2^31 on. */
+int64_t dopt_matrix8_scale_bytes(int64_t rows, int64_t cols);
+
+/* A matrix as values (rows of `ld` elements, aligned to their elements) and
+ * as codes.  out_t receives the transpose: cols x rows, its own blocks along
+ * its own rows.  Either may be left out (codes NULL). */
+typedef struct {
+  int64_t rows, cols, ld;
+  int32_t values_dtype; /* dopt_dtype                                        */
+  int32_t block;        /* dopt_block (pack)                                 */
+  void* values;
+  dopt_matrix8 out, out_t;
+} dopt_matrix_values;
+
+/* Values to codes and scales, each value read once for both orientations;
+ * and codes (of `out`; out_t is not used) to values, which are fp32 or bf16,
+ * exact in both.  A list in one launch, as many as the lists of tensors.
+ * Arrays of one call must not overlap, but for read-only ones. */
+int dopt_matrix8_pack(const dopt_matrix_values* matrices, int32_t n_matrices, dopt_stream stream);
+int dopt_matrix8_unpack(const dopt_matrix_values* matrices, int32_t n_matrices, dopt_stream stream);
+
+/*
+ * d[m][n] = sum over k of a[m][k] * b[n][k], or that added to d: a.rows x
+ * b.rows numbers of d_dtype, `ldd` elements from row to row, from a and b of
+ * the same cols.  Activations (tokens x features) times a weight (outputs x
+ * features); with the packed transposes, the two products of the backward
+ * pass: grads x weight^T's rows, and grads^T x activations^T, which adds to
+ * the fp32 grad that the step reads.
+ * Products of codes are exact, summed in fp32 in the matrix unit in an order
+ * that is fixed for given sizes, and rounded once to d_dtype (with the old d
+ * added in fp32 before).  A term below fp32's normal range may count as 0.
+ * A block that reads as NaN makes its row of d (of a) or column (of b) NaN.
+ * With cols 0 the sums are 0.  d is aligned to its elements only, must not
+ * overlap a or b, and nothing but its rows x b.rows elements is written.
+ * Needs no workspace.  A kernel that gives up waiting for its own copies
+ * writes NaN, so that a step skips it.
+ */
+int dopt_matrix8_multiply(const dopt_matrix8* a, const dopt_matrix8* b, void* d, int32_t d_dtype,
+                          int64_t ldd, int32_t accumulate, dopt_stream stream);
+
+/*
+ * Dropout, whose mask is never stored: element i is dropped where r < T, T =
+ * p * 65536 to the nearest, and else multiplied by 65536 / (65536 - T).  r is
+ * the 16-bit number that the list's step rounds with, for `site` in place of
+ * the tensor's number and t = step + *d_step (d_step NULL: 0), with one more
+ * term for arrays of 2^33 elements and more:
+ *   x = (i / 2 mod 2^32) * 0x9E3779B9 + (i / 2^33) * 0x3C6EF372 + seed
+ *       + site * 0x510E527F + t * 0x6A09E667,
+ * and on as there.  The same call on the gradient is the backward pass: give
+ * it the same numbers (with d_step, before the step counts).  A dropped
+ * element is 0 whatever it was.
+ */
+typedef struct {
+  double p; /* T at most 65535; 0: no dropout                                */
+  uint32_t seed, site;
+  int64_t step;
+  const int64_t* d_step; /* 8-byte aligned device memory, or NULL            */
+} dopt_drop;
+
+typedef struct {
+  int64_t numel;
+  int32_t dtype; /* of x, residual and y                                     */
+  int32_t reserved;
+  const void* x;
+  const void* residual; /* added after the dropout; NULL: none               */
+  void* y;              /* may be x or residual                              */
+  dopt_drop drop;
+} dopt_dropout_args;
+
+/* y = dropout(x) + residual, rounded once; arrays aligned to their elements. */
+int dopt_dropout(const dopt_dropout_args* args, dopt_stream stream);
+
+/* Rows of a matrix: `ld` elements from a row to the next, each aligned to
+ * its elements. */
+typedef struct {
+  void* data;
+  int64_t ld;
+} dopt_rows;
+
+#define DOPT_NORM_MAX_COLS 16384
+
+/*
+ * RMS norm of the rows of h = dropout(x) + residual (rounded to dtype):
+ *   rstd = 1 / sqrt(mean(h^2) + eps);  y = h * rstd * gain,
+ * as values (y), as codes (y8: blocks of rows, rows x cols), or both.  Each
+ * value is read once.  h may be left out (data NULL) without residual and
+ * dropout, when it is x.  Element i of the dropout is row * cols + column.
+ * Squares are added in fp32 in a fixed order; a row whose sum of squares
+ * leaves fp32's range is summed again in fp64.
+ * h and y may be x or residual (the same rows).  cols <= DOPT_NORM_MAX_COLS.
+ */
+typedef struct {
+  int64_t rows, cols;
+  int32_t dtype;      /* of x, residual, h and y                             */
+  int32_t gain_dtype; /* fp32 or dtype                                       */
+  dopt_rows x, residual, h, y; /* residual, h, y: data may be NULL           */
+  const void* gain;   /* cols                                                */
+  const dopt_matrix8* y8; /* or NULL                                         */
+  float* rstd;        /* rows, for the backward pass; or NULL                */
+  double eps;         /* >= 0                                                */
+  dopt_drop drop;
+} dopt_rms_norm_args;
+
+int dopt_rms_norm(const dopt_rms_norm_args* args, dopt_stream stream);
+
+/*
+ * Its backward pass from h and rstd, with g = dy * gain and hat = h * rstd:
+ *   dh = rstd * (g - hat * mean(g * hat)) + dres,
+ * the gradient of the residual (dres: what h's other use gave, or NULL);
+ * dx = dropout(dh), the gradient of x, where it has dropout (else NULL: it
+ * is dh); and dgain = sum over rows of dy * hat (cols floats; or NULL), or
+ * that added to it.  Sums in fp32 in a fixed order.  dh may be dy or dres,
+ * dx too, each another one.  The workspace holds partial sums of dgain,
+ * dopt_rms_norm_workspace_bytes(rows, cols) bytes, 16-byte aligned, and
+ * serves one call at a time; without dgain it may be NULL.
+ */
+typedef struct {
+  int64_t rows, cols;
+  int32_t dtype, gain_dtype; /* dtype: of dy, h, dres, dh, dx                */
+  dopt_rows dy, h, dres, dh, dx;
+  const void* gain;
+  const float* rstd;
+  float* dgain;
+  int32_t accumulate; /* nonzero: dgain is added to                          */
+  int32_t reserved;
+  dopt_drop drop;
+} dopt_rms_norm_backward_args;
+
+size_t dopt_rms_norm_workspace_bytes(int64_t rows, int64_t cols); /* 0: bad sizes */
+int dopt_rms_norm_backward(const dopt_rms_norm_backward_args* args, void* workspace,
+                           size_t workspace_bytes, dopt_stream stream);
+
 #if defined(DOPT_BOUNDS_CHECK) && DOPT_BOUNDS_CHECK
 /* Debug builds only (DOPT_BOUNDS_CHECK=1): the release library neither
  * exports this hook nor tests for it in its kernels.  Test hook for the

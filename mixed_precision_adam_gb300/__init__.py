@@ -30,6 +30,9 @@ GROUP_FP32_FROM_FLOAT16, GROUP_FP32 = 0, 1
 LAYOUT_FULL_BUFFER, LAYOUT_SHARD_ONLY, LAYOUT_BUCKET = 0, 1, 2
 MOMENTS_F32, MOMENTS_8BIT = 0, 1
 MOMENT_BLOCK = 256
+BLOCK_ROW, BLOCK_SQUARE = 0, 1
+MATRIX_BLOCK = 128
+NORM_MAX_COLS = 16384
 ALL_RANKS = -1
 MAX_REPLICAS = 64
 
@@ -106,6 +109,41 @@ class dopt_moment_tensor(ctypes.Structure):
                 ("exp_avg_scale", _P), ("exp_avg_sq_scale", _P)]
 
 
+class dopt_matrix8(ctypes.Structure):
+    _fields_ = [("rows", _I64), ("cols", _I64), ("ld", _I64), ("codes", _P), ("scales", _P)]
+
+
+class dopt_matrix_values(ctypes.Structure):
+    _fields_ = [("rows", _I64), ("cols", _I64), ("ld", _I64), ("values_dtype", _I32), ("block", _I32),
+                ("values", _P), ("out", dopt_matrix8), ("out_t", dopt_matrix8)]
+
+
+class dopt_drop(ctypes.Structure):
+    _fields_ = [("p", _D), ("seed", ctypes.c_uint32), ("site", ctypes.c_uint32), ("step", _I64), ("d_step", _P)]
+
+
+class dopt_dropout_args(ctypes.Structure):
+    _fields_ = [("numel", _I64), ("dtype", _I32), ("reserved", _I32), ("x", _P), ("residual", _P), ("y", _P),
+                ("drop", dopt_drop)]
+
+
+class dopt_rows(ctypes.Structure):
+    _fields_ = [("data", _P), ("ld", _I64)]
+
+
+class dopt_rms_norm_args(ctypes.Structure):
+    _fields_ = [("rows", _I64), ("cols", _I64), ("dtype", _I32), ("gain_dtype", _I32),
+                ("x", dopt_rows), ("residual", dopt_rows), ("h", dopt_rows), ("y", dopt_rows),
+                ("gain", _P), ("y8", ctypes.POINTER(dopt_matrix8)), ("rstd", _P), ("eps", _D), ("drop", dopt_drop)]
+
+
+class dopt_rms_norm_backward_args(ctypes.Structure):
+    _fields_ = [("rows", _I64), ("cols", _I64), ("dtype", _I32), ("gain_dtype", _I32),
+                ("dy", dopt_rows), ("h", dopt_rows), ("dres", dopt_rows), ("dh", dopt_rows), ("dx", dopt_rows),
+                ("gain", _P), ("rstd", _P), ("dgain", _P), ("accumulate", _I32), ("reserved", _I32),
+                ("drop", dopt_drop)]
+
+
 def _proto(name, res, *args):
     fn = getattr(_lib, name)
     fn.restype = res
@@ -177,6 +215,14 @@ _c = {
                                 _SZ, _P, _P, _P),
     "dopt_state8_pack": _proto("dopt_state8_pack", ctypes.c_int, _P, _I32, _P),
     "dopt_state8_unpack": _proto("dopt_state8_unpack", ctypes.c_int, _P, _I32, _P),
+    "dopt_matrix8_scale_bytes": _proto("dopt_matrix8_scale_bytes", _I64, _I64, _I64),
+    "dopt_matrix8_pack": _proto("dopt_matrix8_pack", ctypes.c_int, _P, _I32, _P),
+    "dopt_matrix8_unpack": _proto("dopt_matrix8_unpack", ctypes.c_int, _P, _I32, _P),
+    "dopt_matrix8_multiply": _proto("dopt_matrix8_multiply", ctypes.c_int, _P, _P, _P, _I32, _I64, _I32, _P),
+    "dopt_dropout": _proto("dopt_dropout", ctypes.c_int, _P, _P),
+    "dopt_rms_norm": _proto("dopt_rms_norm", ctypes.c_int, _P, _P),
+    "dopt_rms_norm_workspace_bytes": _proto("dopt_rms_norm_workspace_bytes", _SZ, _I64, _I64),
+    "dopt_rms_norm_backward": _proto("dopt_rms_norm_backward", ctypes.c_int, _P, _P, _SZ, _P),
     "dopt_debug_bounds_record": _proto("dopt_debug_bounds_record", ctypes.c_int, ctypes.POINTER(_I64)),
     "dopt_read_step_stats": _proto("dopt_read_step_stats", ctypes.c_int, _P,
                                    ctypes.POINTER(dopt_step_stats), _P),
@@ -825,10 +871,255 @@ def dopt_state8_unpack(moments, stream=None):
     _check(_c["dopt_state8_unpack"](moments.address, moments.n, _stream(stream)))
 
 
+# ------------------------------------------- 8-bit matrices, norm, dropout --
+
+def dopt_matrix8_scale_bytes(rows, cols):
+    """Scale bytes of a rows x cols 8-bit matrix."""
+    return _check(_c["dopt_matrix8_scale_bytes"](rows, cols))
+
+
+def _tensor(x, name, dtypes, devices, who=""):
+    """(pointer, dtype name) of a torch tensor of one of `dtypes`, its device
+    added to `devices`."""
+    if getattr(x, "get_device", None) is None:
+        raise DoptError(E_INVALID, f"{who}{name} is not a torch tensor")
+    dt = _dtype_name(x.dtype)
+    if dt not in dtypes:
+        raise DoptError(E_INVALID, f"{who}{name} is {dt}, not {' or '.join(dtypes)}")
+    if x.numel():
+        devices.add(x.get_device())
+    return x.data_ptr(), dt
+
+
+def _matrix(x, name, dtypes, devices, shape=None, who=""):
+    """(pointer, elements from row to row, dtype name) of a 2-d torch tensor
+    whose rows are contiguous, of `shape` unless that is None."""
+    ptr, dt = _tensor(x, name, dtypes, devices, who)
+    if x.dim() != 2:
+        raise DoptError(E_INVALID, f"{who}{name} has {x.dim()} dimensions, not 2")
+    rows, cols = x.shape
+    if shape is not None and (rows, cols) != tuple(shape):
+        raise DoptError(E_INVALID, f"{who}{name} is {rows} x {cols}, not {shape[0]} x {shape[1]}")
+    row, one = x.stride()
+    if cols > 1 and one != 1:
+        raise DoptError(E_INVALID, f"{who}{name}: a row's elements are not contiguous")
+    if rows > 1 and row < cols:
+        raise DoptError(E_INVALID, f"{who}{name}: rows overlap")
+    return ptr, row if rows > 1 else max(row, cols), dt
+
+
+def _vector(x, name, dtypes, devices, numel, who=""):
+    ptr, dt = _tensor(x, name, dtypes, devices, who)
+    if x.numel() != numel or not x.is_contiguous():
+        raise DoptError(E_INVALID, f"{who}{name} is not contiguous, or has {x.numel()} elements, not {numel}")
+    return ptr, dt
+
+
+class Matrix8:
+    """An 8-bit matrix: codes, a 2-d uint8 tensor whose rows are contiguous
+    and start on 16-byte boundaries, and scales, a uint8 tensor of
+    dopt_matrix8_scale_bytes(rows, cols) elements."""
+
+    def __init__(self, codes, scales):
+        d = set()
+        ptr, ld, _ = _matrix(codes, "codes", _CODES, d)
+        self.rows, self.cols = codes.shape
+        if self.rows <= 1:
+            ld = -(-ld // 16) * 16  # no row follows
+        need = dopt_matrix8_scale_bytes(self.rows, self.cols)
+        sp, _ = _vector(scales, "scales", _CODES, d, need)
+        self.c = dopt_matrix8(self.rows, self.cols, ld, ptr, sp)
+        self.address = ctypes.addressof(self.c)
+        self.codes, self.scales, self.devices = codes, scales, d
+        self.gpu = _one_device(d)
+
+
+class MatrixList:
+    """A marshalled list of dopt_matrix_values.  entries: one dict per matrix
+    with values (a 2-d float32, bfloat16 or float16 tensor whose rows are
+    contiguous), out (a Matrix8 of its size) and/or out_t (one of the
+    transpose's), and optionally block (BLOCK_ROW)."""
+
+    def __init__(self, entries):
+        self.n = len(entries)
+        self.c = (dopt_matrix_values * max(1, self.n))()
+        self.address = ctypes.addressof(self.c)
+        self._keep = [dict(e) for e in entries]
+        d = set()
+        for k, e in enumerate(entries):
+            t, who = self.c[k], f"matrix {k}: "
+            t.values, t.ld, dt = _matrix(e.get("values"), "values", _DTYPE, d, who=who)
+            t.rows, t.cols = e["values"].shape
+            t.values_dtype, t.block = _DTYPE[dt], int(e.get("block", BLOCK_ROW))
+            for name, shape in (("out", (t.rows, t.cols)), ("out_t", (t.cols, t.rows))):
+                m = e.get(name)
+                if m is None:
+                    continue
+                if (m.rows, m.cols) != shape:
+                    raise DoptError(E_INVALID, f"{who}{name} is {m.rows} x {m.cols}, not {shape[0]} x {shape[1]}")
+                setattr(t, name, m.c)
+                d |= m.devices
+        self.gpu = _one_device(d)
+
+
+def dopt_matrix8_pack(matrices, stream=None):
+    """The values of a MatrixList into codes and scales."""
+    _gpu_of(matrices)
+    _check(_c["dopt_matrix8_pack"](matrices.address, matrices.n, _stream(stream)))
+
+
+def dopt_matrix8_unpack(matrices, stream=None):
+    """The codes and scales (of out) of a MatrixList into values (float32 or bfloat16)."""
+    _gpu_of(matrices)
+    _check(_c["dopt_matrix8_unpack"](matrices.address, matrices.n, _stream(stream)))
+
+
+def dopt_matrix8_multiply(a, b, d, accumulate=False, stream=None):
+    """d = a b^T, or d += a b^T: two Matrix8 of the same cols, and a 2-d
+    float32, bfloat16 or float16 tensor of a.rows x b.rows whose rows are
+    contiguous."""
+    devices = set()
+    ptr, ld, dt = _matrix(d, "d", _DTYPE, devices, (a.rows, b.rows))
+    _gpu_of(_OnGpu(devices | a.devices | b.devices))
+    _check(_c["dopt_matrix8_multiply"](a.address, b.address, ptr, _DTYPE[dt], ld, 1 if accumulate else 0,
+                                       _stream(stream)))
+
+
+class _OnGpu:
+    def __init__(self, devices):
+        self.gpu = _one_device(devices)
+
+
+class Dropout:
+    """The numbers of a dropout: p, seed, site (which dropout of the model),
+    step, and optionally d_step, a device int64 tensor that is added to it."""
+
+    def __init__(self, p, seed, site=0, step=0, d_step=None):
+        self.devices, ptr = set(), None
+        if d_step is not None:
+            ptr, _ = _vector(d_step, "d_step", ("int64",), self.devices, 1)
+        self.c = dopt_drop(float(p), seed & 0xFFFFFFFF, site & 0xFFFFFFFF, int(step), ptr)
+        self.d_step = d_step
+
+
+class _Args:
+    """A call's marshalled arguments, and the owner of its arrays' references."""
+
+    def _close(self, devices, dropout, keep):
+        if dropout is not None:
+            self.c.drop = dropout.c
+            devices = devices | dropout.devices
+        self._keep, self.gpu = (keep, dropout), _one_device(devices)
+        self.address = ctypes.addressof(self.c)
+
+    def set_step(self, step):
+        """The step of the dropout's random numbers."""
+        self.c.drop.step = int(step)
+
+
+class DropoutArgs(_Args):
+    """y = dropout(x) + residual: contiguous tensors of one size and dtype
+    (float32, bfloat16 or float16); y may be x or residual."""
+
+    def __init__(self, x, y, dropout, residual=None):
+        d = set()
+        self.c = dopt_dropout_args()
+        self.c.numel = x.numel()
+        self.c.x, dt = _vector(x, "x", _DTYPE, d, x.numel())
+        self.c.y, _ = _vector(y, "y", (dt,), d, x.numel())
+        if residual is not None:
+            self.c.residual, _ = _vector(residual, "residual", (dt,), d, x.numel())
+        self.c.dtype = _DTYPE[dt]
+        self._close(d, dropout, (x, y, residual))
+
+
+def dopt_dropout(args, stream=None):
+    """Runs a DropoutArgs."""
+    _gpu_of(args)
+    _check(_c["dopt_dropout"](args.address, _stream(stream)))
+
+
+def _gain(c, gain, dt, cols, devices):
+    c.gain, gdt = _vector(gain, "gain", ("float32", dt), devices, cols)
+    c.dtype, c.gain_dtype = _DTYPE[dt], _DTYPE[gdt]
+
+
+class RmsNormArgs(_Args):
+    """The norm of h = dropout(x) + residual: x, residual, h and y 2-d tensors
+    of one dtype whose rows are contiguous; gain float32 or of that dtype;
+    outputs h (with a residual or dropout), y, y8 (a Matrix8), rstd (float32,
+    one per row)."""
+
+    def __init__(self, x, gain, eps, *, residual=None, dropout=None, h=None, y=None, y8=None, rstd=None):
+        d = set()
+        self.c = c = dopt_rms_norm_args()
+        ptr, ld, dt = _matrix(x, "x", _DTYPE, d)
+        c.x = dopt_rows(ptr, ld)
+        c.rows, c.cols = x.shape
+        for name, t in (("residual", residual), ("h", h), ("y", y)):
+            if t is not None:
+                setattr(c, name, dopt_rows(*_matrix(t, name, (dt,), d, x.shape)[:2]))
+        _gain(c, gain, dt, c.cols, d)
+        if y8 is not None:
+            if (y8.rows, y8.cols) != tuple(x.shape):
+                raise DoptError(E_INVALID, f"y8 is {y8.rows} x {y8.cols}, not {c.rows} x {c.cols}")
+            c.y8 = ctypes.pointer(y8.c)
+            d |= y8.devices
+        if rstd is not None:
+            c.rstd, _ = _vector(rstd, "rstd", ("float32",), d, c.rows)
+        c.eps = eps
+        self._close(d, dropout, (x, gain, residual, h, y, y8, rstd))
+
+
+def dopt_rms_norm(args, stream=None):
+    """Runs a RmsNormArgs."""
+    _gpu_of(args)
+    _check(_c["dopt_rms_norm"](args.address, _stream(stream)))
+
+
+def dopt_rms_norm_workspace_bytes(rows, cols):
+    v = _c["dopt_rms_norm_workspace_bytes"](rows, cols)
+    if v == 0:
+        raise DoptError(E_INVALID, dopt_last_error())
+    return v
+
+
+class RmsNormBackwardArgs(_Args):
+    """The norm's backward pass: dy, h, dres, dh and dx 2-d tensors of one
+    dtype whose rows are contiguous; dgain float32, which needs the
+    workspace."""
+
+    def __init__(self, dy, h, gain, rstd, dh, *, dres=None, dropout=None, dx=None, dgain=None, accumulate=False,
+                 workspace=None, workspace_bytes=0):
+        d = set()
+        self.c = c = dopt_rms_norm_backward_args()
+        ptr, ld, dt = _matrix(h, "h", _DTYPE, d)
+        c.h = dopt_rows(ptr, ld)
+        c.rows, c.cols = h.shape
+        for name, t in (("dy", dy), ("dres", dres), ("dh", dh), ("dx", dx)):
+            if t is not None:
+                setattr(c, name, dopt_rows(*_matrix(t, name, (dt,), d, h.shape)[:2]))
+        _gain(c, gain, dt, c.cols, d)
+        c.rstd, _ = _vector(rstd, "rstd", ("float32",), d, c.rows)
+        if dgain is not None:
+            c.dgain, _ = _vector(dgain, "dgain", ("float32",), d, c.cols)
+        c.accumulate = int(bool(accumulate))
+        self._close(d, dropout, (dy, h, gain, rstd, dh, dres, dx, dgain))
+        self.workspace, self.workspace_bytes = workspace, workspace_bytes
+
+
+def dopt_rms_norm_backward(args, stream=None):
+    """Runs a RmsNormBackwardArgs."""
+    gpu = _gpu_of(args)
+    ws = None if args.workspace is None else _workspace(args.workspace, args.workspace_bytes, gpu)
+    _check(_c["dopt_rms_norm_backward"](args.address, ws, args.workspace_bytes, _stream(stream)))
+
+
 def exported_symbols():
     """Names of the C entry points this binding resolved in the library."""
     return sorted(_c)
 
 
 __all__ = [n for n in dir() if n.startswith("dopt_")] + [
-    "ShardMap", "StepArgs", "TensorList", "MomentList", "DoptError", "exported_symbols"]
+    "ShardMap", "StepArgs", "TensorList", "MomentList", "Matrix8", "MatrixList", "Dropout", "DropoutArgs",
+    "RmsNormArgs", "RmsNormBackwardArgs", "DoptError", "exported_symbols"]

@@ -1,0 +1,61 @@
+// entry.h -- what the C entry points next to the step share: checks of
+// pointers, sizes and types, and the guard that keeps exceptions inside.
+#pragma once
+
+#include <cmath>
+#include <new>
+#include <string>
+
+#include "dopt_internal.h"
+
+namespace dopt {
+
+inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline size_t dtype_bytes(int32_t dtype) { return dtype == DOPT_F32 ? 4 : 2; }
+inline bool known_dtype(int32_t dtype) { return dtype == DOPT_F32 || dtype == DOPT_BF16 || dtype == DOPT_F16; }
+
+constexpr int64_t kMaxSide = int64_t(1) << 31;  // rows and columns stay below it
+
+// Sizes of a matrix.
+inline int check_sides(int64_t rows, int64_t cols, const std::string& who) {
+  if (rows < 0 || cols < 0) return fail(DOPT_E_INVALID, who + "negative size");
+  if (rows >= kMaxSide || cols >= kMaxSide) return fail(DOPT_E_SIZE, who + "a size of 2^31 or more");
+  return DOPT_OK;
+}
+
+// An 8-bit matrix with elements: its codes, scales and row distance.
+inline int check_matrix8(const dopt_matrix8& m, const std::string& who) {
+  if (!m.codes || !m.scales) return fail(DOPT_E_INVALID, who + "NULL codes or scales");
+  if (!aligned_to(m.codes, 16) || !aligned_to(m.scales, 16))
+    return fail(DOPT_E_ALIGN, who + "codes or scales not 16-byte aligned");
+  if (m.ld < m.cols) return fail(DOPT_E_INVALID, who + "ld below cols");
+  if (m.ld % 16) return fail(DOPT_E_ALIGN, who + "ld of the codes not a multiple of 16");
+  if (m.ld >= kMaxSide * 2) return fail(DOPT_E_SIZE, who + "ld too large");
+  return DOPT_OK;
+}
+
+// The drop threshold T of a dropout..
+inline int check_drop(const dopt_drop& d, uint32_t* threshold, const std::string& who) {
+  *threshold = 0;
+  if (!(d.p >= 0.0 && d.p < 1.0)) return fail(DOPT_E_INVALID, who + "the dropout's p is not in [0, 1)");
+  const double t = std::nearbyint(d.p * 65536.0);
+  if (t > 65535.0) return fail(DOPT_E_INVALID, who + "the dropout's p is too near to 1");
+  if (!aligned_to(d.d_step, 8)) return fail(DOPT_E_ALIGN, who + "d_step not 8-byte aligned");
+  *threshold = (uint32_t)t;
+  return DOPT_OK;
+}
+
+// Runs an entry point's body: a host allocation that fails (an error
+// message's, say) is a status, not an exception through the C boundary.
+template <typename F>
+int guard_entry(F&& body) noexcept {
+  try {
+    return body();
+  } catch (const std::bad_alloc&) {
+    return DOPT_E_NOMEM;
+  } catch (...) {
+    return DOPT_E_INVALID;
+  }
+}
+
+}  // namespace dopt

@@ -6,6 +6,7 @@
 //   tensors_norm.cu   -- the grad norm, and the finalize
 //   tensors_adamw.cu  -- AdamW with fp32 moments
 //   tensors_adamw8.cu -- AdamW with 8-bit moments, and their pack / unpack
+// The 8-bit matrices (matrix8.cuh) take the encoding and the hash from here.
 #pragma once
 
 #include "kernels.cuh"
@@ -137,6 +138,24 @@ static_assert(sizeof(MomentParamsT<kMomentCap>) <= 32764, "kernel parameter limi
 // The rounding hash's terms, as the header states them.
 constexpr uint32_t kHashPair = 0x9E3779B9u, kHashTensor = 0x510E527Fu, kHashStep = 0x6A09E667u;
 constexpr uint32_t kHashMul1 = 0xBB67AE85u, kHashMul2 = 0xA54FF53Bu;
+__device__ __forceinline__ uint32_t hash_pair(uint32_t x) {
+  uint64_t q = (uint64_t)x * kHashMul1;
+  x = (uint32_t)q ^ (uint32_t)(q >> 32);
+  q = (uint64_t)x * kHashMul2;
+  return (uint32_t)q ^ (uint32_t)(q >> 32);
+}
+
+// A block's scale from the bits of its largest magnitude, 255 where that is
+// not finite or above the largest code; and the number that e4m3 codes count
+// under it.
+__device__ __forceinline__ uint32_t exponent_of(uint32_t bits, uint32_t up) { return (bits + up) >> 23; }
+__device__ __forceinline__ uint32_t m_scale_of(uint32_t top) {
+  const uint32_t e = exponent_of(top, 0x1FFFFFu);
+  return e >= 255u ? 255u : max((int)e - 8, 8);
+}
+__device__ __forceinline__ float m_unit(uint32_t s) {
+  return s == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(s << 23);
+}
 
 // The tensor holding tile t among lo .. hi, by bisection.
 template <typename P>

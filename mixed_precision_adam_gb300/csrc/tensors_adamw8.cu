@@ -26,24 +26,7 @@ namespace dopt {
 constexpr int kRing8 = 3, kCtas8 = 3, kRounds8 = 24;
 static_assert(kMomentBlock == 256 && kAdamTile % kMomentBlock == 0, "one warp per block, 8 elements per lane");
 
-__device__ __forceinline__ uint32_t exponent_of(uint32_t bits, uint32_t up) { return (bits + up) >> 23; }
-
-__device__ __forceinline__ float m_unit(uint32_t s) {
-  return s == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(s << 23);
-}
-__device__ __forceinline__ uint32_t hash_pair(uint32_t x) {
-  uint64_t q = (uint64_t)x * kHashMul1;
-  x = (uint32_t)q ^ (uint32_t)(q >> 32);
-  q = (uint64_t)x * kHashMul2;
-  return (uint32_t)q ^ (uint32_t)(q >> 32);
-}
-
-// A block's scales from the bits of its largest magnitude: 255 where that is
-// not finite or above the largest code.
-__device__ __forceinline__ uint32_t m_scale_of(uint32_t top) {
-  const uint32_t e = exponent_of(top, 0x1FFFFFu);
-  return e >= 255u ? 255u : max((int)e - 8, 8);
-}
+// A second moment's scale; see m_scale_of.
 __device__ __forceinline__ uint32_t v_scale_of(uint32_t top) {
   const uint32_t e = exponent_of(top, 0x0FFFFFu);
   return e >= 255u ? 255u : (uint32_t)max((int)e - 31, 0);
