@@ -1,6 +1,6 @@
 """Builds the in-tree CUDA library lib/libdopt.so for sm_103a.
 
-Fourteen translation units (the host shard map in C++; the device entry points
+Fifteen translation units (the host shard map in C++; the device entry points
 and the finalize kernel; the reduce/prepare kernels for each of the three
 grad dtypes; the AdamW kernel; the step over a list of tensors: entry
 points, grad norm, AdamW with fp32 and with 8-bit moments; the 8-bit
@@ -29,7 +29,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE]
 SOURCES = ["shard_map.cpp", "dopt_cuda.cu", "k1_f32.cu", "k1_bf16.cu", "k1_f16.cu", "k3.cu",
            "tensors.cu", "tensors_norm.cu", "tensors_adamw.cu", "tensors_adamw8.cu",
-           "matrix8.cu", "matrix8_multiply.cu", "rms_norm.cu", "dropout.cu"]
+           "matrix8.cu", "matrix8_multiply.cu", "matrix8_multiply_pair.cu", "rms_norm.cu", "dropout.cu"]
 
 
 def _deps():

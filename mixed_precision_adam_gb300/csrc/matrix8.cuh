@@ -2,7 +2,7 @@
 // consecutive elements of a row in registers, their e4m3 codes, the place of
 // a scale byte, and the dropout's random numbers.
 //   matrix8.cu          -- values to codes and back
-//   matrix8_multiply.cu -- the products
+//   matrix8_multiply*.cu -- the products
 //   rms_norm.cu         -- the norm and its backward pass
 //   dropout.cu
 #pragma once

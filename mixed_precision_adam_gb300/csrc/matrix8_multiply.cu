@@ -1,133 +1,14 @@
-// matrix8_multiply.cu -- products of 8-bit matrices, d = a b^T (+ d).
-//
-// The 5th-generation tensor cores multiply e4m3 codes and apply one scale
-// byte per row and 32 of k themselves (kind::mxf8f6f4, block_scale): a block
-// of 128 columns is four such steps with the same byte.  The bytes lie in
-// memory as the unit wants them in TMEM, so they are copied, never unpacked.
-//
-// The unit's rows ("lanes" of TMEM) are b's rows and its columns are a's: a
-// thread then holds one output column n for many m, and a warp's stores of
-// one m are 32 consecutive elements, whatever the row distance or alignment
-// of d.
+// matrix8_multiply.cu -- products of 8-bit matrices, d = a b^T (+ d), in
+// tiles of one SM, and the choice among the kernels.
 //
 // A CTA has a tile of 128 n by BT m: one warp loads 128 bytes of k of both
 // operands per step by TMA into a ring, one thread issues the products, and
 // eight warps take the sums from TMEM to registers at once, give TMEM back
 // and store while the next tile is being multiplied.
-#include <cuda.h>
-
-#include "matrix8.cuh"
-#include "tma.cuh"
+#include "matrix8_mma.cuh"
 
 namespace dopt {
 
-// ---------------------------------------------------------------- PTX forms --
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t pred;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(pred));
-  return pred != 0;
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          smem_addr(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
-      : "memory");
-}
-__device__ __forceinline__ void scale_load(void* dst, const uint8_t* src, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)),
-      "l"((unsigned long long)__cvta_generic_to_global(src)), "r"(512), "r"(smem_addr(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tmem_alloc(uint32_t* at, uint32_t columns) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(at)), "r"(columns)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-}
-__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t columns) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns));
-}
-__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// The products issued so far arrive on a barrier when they are done.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
-}
-// 512 scale bytes (32 x 16) to four TMEM columns, in all four lane quarters.
-__device__ __forceinline__ void scale_to_tmem(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
-}
-__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, uint32_t sa, uint32_t sb,
-                                           uint32_t add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(instr), "r"(sa), "r"(sb), "r"(add)
-      : "memory");
-}
-// N consecutive columns of the warp's 32 lanes.
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t* r);
-template <>
-__device__ __forceinline__ void tmem_load<8>(uint32_t at, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(at));
-}
-template <>
-__device__ __forceinline__ void tmem_load<16>(uint32_t at, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-      "[%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(at));
-}
-
-// -------------------------------------------------------------- descriptors --
-
-// An operand's tile in shared memory: rows of 128 bytes in the 128-byte
-// swizzle, eight rows to an atom of 1024 bytes; a step of 32 bytes along k
-// starts 32 bytes on in the first row.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t smem) {
-  return (uint64_t)((smem & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-         (uint64_t)2 << 61;
-}
-// 32 rows of 16 scale bytes, no swizzle: eight rows to 128 bytes.
-__device__ __forceinline__ uint64_t scales_desc(uint32_t smem) {
-  return (uint64_t)((smem & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
-}
-// e4m3 both (0), scale bytes as powers of two (bit 23), both operands along
-// k, 128 rows by n columns; which byte of a scale column is per product.
-__host__ __device__ constexpr uint32_t scaled_instr(int n) {
-  return (uint32_t)(n >> 3) << 17 | 1u << 23 | (uint32_t)(128 >> 4) << 24;
-}
-__device__ __forceinline__ uint32_t scale_byte(uint32_t k) { return k << 4 | k << 29; }
-
-// ------------------------------------------------------------------- kernel --
-
-struct MulParams {
-  CUtensorMap b_map, a_map;
-  const uint8_t* b_scales;
-  const uint8_t* a_scales;
-  void* d;
-  int64_t ldd;
-  int32_t m, n;            // rows of a, of b
-  int32_t blocks, groups;  // of k: 128 columns, 512 columns
-  int32_t tiles_n, tiles_m, n_tiles;
-  int32_t split;  // CTAs of a cluster that share a tile's k
-  int32_t dtype, accumulate;
-};
-
-constexpr int kMulThreads = 384;  // load, multiply, TMEM, idle; eight warps of the epilogue
-constexpr int kOperandRow = 128;  // bytes of k per step
 constexpr int kTileN = 128;
 
 // BT: rows of a per tile.  Stages of the ring: as many as leave room for two
@@ -147,43 +28,6 @@ struct MulShape {
   static_assert(kScaleCol + 2 * kScaleCols <= kTmem, "TMEM columns");
   static_assert(kB % 1024 == 0 && (BT < 8 || kA % 1024 == 0), "operand tiles start on an atom");
 };
-
-// A tile's place: tiles are taken in bands of eight along n, so that the
-// CTAs at work share rows of both operands in L2.
-struct MulTile {
-  int n, m;
-};
-constexpr int kBand = 8;
-__device__ __forceinline__ MulTile mul_tile(const MulParams& p, int t) {
-  const int per_band = kBand * p.tiles_m, band = t / per_band, in = t - band * per_band;
-  const int width = min(kBand, p.tiles_n - band * kBand);
-  return MulTile{band * kBand + in % width, in / width};
-}
-
-// One column n of d for N consecutive m, `count` of them there: rounded once,
-// with what d holds added before.
-template <typename T, int N>
-__device__ __forceinline__ void store_sums(const uint32_t (&r)[N], T* d, int64_t ldd, int count, bool accumulate) {
-  constexpr int kAhead = 8;  // loads under way
-#pragma unroll
-  for (int c = 0; c < N; c += kAhead) {
-    float old[kAhead];
-    if (accumulate) {
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) old[j] = c + j < count ? widen<T>(d[(c + j) * ldd]) : 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      float x = __uint_as_float(r[c + j]);
-      if (accumulate) x += old[j];
-      if (c + j < count) d[(c + j) * ldd] = narrow<T>(x);
-    }
-  }
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 template <int BT, bool SPLIT>
 __global__ void __launch_bounds__(kMulThreads) matrix8_multiply(const __grid_constant__ MulParams p) {
@@ -208,7 +52,7 @@ __global__ void __launch_bounds__(kMulThreads) matrix8_multiply(const __grid_con
     *failed = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 2) tmem_alloc(tmem_at, S::kTmem);
+  if (warp == 2) tmem_alloc<1>(tmem_at, S::kTmem);
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
@@ -237,17 +81,16 @@ __global__ void __launch_bounds__(kMulThreads) matrix8_multiply(const __grid_con
           uint8_t* b = smem + stage * (S::kA + S::kB);
           uint8_t* a = b + S::kB;
           const bool scales = k % 4 == 0;
-          // a tile of a may end before its second 128 rows begin
-          const int a_tiles = scales ? min(S::kScaleTiles - 1, (p.m - tile.m * BT + 127) / 128) : 0;
-          mbar_arrive_expect_tx(full + stage, S::kA + S::kB + (scales ? 512 * (1 + a_tiles) : 0));
-          tma_load_2d(b, &p.b_map, k * kOperandRow, tile.n * kTileN, full + stage);
-          tma_load_2d(a, &p.a_map, k * kOperandRow, tile.m * BT, full + stage);
+          const uint32_t bar = smem_addr(full + stage);
+          mbar_arrive_expect_tx(full + stage, S::kA + S::kB + (scales ? 512 * S::kScaleTiles : 0));
+          tma_load_2d<1>(b, &p.b_map, k * kOperandRow, tile.n * kTileN, bar);
+          tma_load_2d<1>(a, &p.a_map, k * kOperandRow, tile.m * BT, bar);
           if (scales) {
             uint8_t* s = smem + S::kScaleAt + stage * S::kScaleTiles * 512;
-            scale_load(s, p.b_scales + ((int64_t)tile.n * p.groups + k / 4) * 512, full + stage);
-            for (int i = 0; i < a_tiles; ++i)
-              scale_load(s + 512 * (i + 1), p.a_scales + (((int64_t)tile.m * BT / 128 + i) * p.groups + k / 4) * 512,
-                         full + stage);
+            tma_load_2d<1>(s, &p.b_scales, 0, tile.n * p.groups + k / 4, bar);
+#pragma unroll
+            for (int i = 1; i < S::kScaleTiles; ++i)
+              tma_load_2d<1>(s + 512 * i, &p.a_scales, 0, (tile.m * BT / 128 + i - 1) * p.groups + k / 4, bar);
           }
           ++loads;
           if (++stage == S::kStages) stage = 0, phase ^= 1;
@@ -262,55 +105,57 @@ __global__ void __launch_bounds__(kMulThreads) matrix8_multiply(const __grid_con
     if (elect_one()) {
       int stage = 0, phase = 0, done = 0, set = 0;
       bool ok = true;
-      for (int t = first; t < p.n_tiles && ok; t += stride, ++done) {
-        if (!(ok = mbar_wait_bounded(taken, (done & 1) ^ 1))) {
-          *failed = 1u;
-          break;
-        }
-        tmem_fence_after();
-        for (int k = k0; k < k1; ++k) {
-          if (!(ok = mbar_wait_bounded(full + stage, phase))) break;
-          tmem_fence_after();
-          const uint32_t b = smem_addr(smem + stage * (S::kA + S::kB)), a = b + S::kB;
-          if (k % 4 == 0) {
-            set ^= 1;
-            const uint32_t s = smem_addr(smem + S::kScaleAt + stage * S::kScaleTiles * 512);
-#pragma unroll
-            for (int i = 0; i < S::kScaleTiles; ++i)
-              scale_to_tmem(tmem + S::kScaleCol + set * S::kScaleCols + 4 * i, scales_desc(s + 512 * i));
+      for (int t = first; t < p.n_tiles && ok; t += stride) {
+        for (int part = k0; part < k1 && ok; part += p.part, ++done) {
+          if (!(ok = mbar_wait_bounded(taken, (done & 1) ^ 1))) {
+            *failed = 1u;
+            break;
           }
-          const uint32_t sb = tmem + S::kScaleCol + set * S::kScaleCols, sa = sb + 4;
-          const uint32_t instr = scaled_instr(BT) | scale_byte(k & 3);
-          const uint64_t bd = operand_desc(b), ad = operand_desc(a);
+          tmem_fence_after();
+          const int end = min(k1, part + p.part);
+          for (int k = part; k < end; ++k) {
+            if (!(ok = mbar_wait_bounded(full + stage, phase))) break;
+            tmem_fence_after();
+            const uint32_t b = smem_addr(smem + stage * (S::kA + S::kB)), a = b + S::kB;
+            if (k % 4 == 0) {
+              set ^= 1;
+              const uint32_t s = smem_addr(smem + S::kScaleAt + stage * S::kScaleTiles * 512);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_scaled(tmem, bd + 2 * j, ad + 2 * j, instr, sb, sa, (k > k0 || j > 0) ? 1u : 0u);
-          mma_commit(empty + stage);
-          if (++stage == S::kStages) stage = 0, phase ^= 1;
+              for (int i = 0; i < S::kScaleTiles; ++i)
+                scale_to_tmem<1>(tmem + S::kScaleCol + set * S::kScaleCols + 4 * i, scales_desc(s + 512 * i));
+            }
+            const uint32_t sb = tmem + S::kScaleCol + set * S::kScaleCols, sa = sb + 4;
+            const uint32_t instr = scaled_instr(kTileN, BT) | scale_byte(k & 3);
+            const uint64_t bd = operand_desc(b), ad = operand_desc(a);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma_scaled<1>(tmem, bd + 2 * j, ad + 2 * j, instr, sb, sa, (k > part || j > 0) ? 1u : 0u);
+            mma_commit<1>(empty + stage);
+            if (++stage == S::kStages) stage = 0, phase ^= 1;
+          }
+          if (!ok) *failed = 1u;
+          mma_commit<1>(sums);  // after what was issued, all of a part's products or not
         }
-        if (!ok) *failed = 1u;
-        mma_commit(sums);  // after what was issued, all of a tile's products or not
       }
     }
     __syncwarp();
   } else if (warp >= 4) {
-    constexpr int kColumns = BT / 2, kChunk = BT == 16 ? 8 : 16;
+    constexpr int kColumns = BT / 2;
     const int quarter = warp % 4, half = (warp - 4) / 4;
     bool ok = true;
     int done = 0;
-    for (int t = first; t < p.n_tiles; t += stride, ++done) {
+    for (int t = first; t < p.n_tiles; t += stride) {
       const MulTile tile = mul_tile(p, t);
       uint32_t r[kColumns];
-      ok = ok && mbar_wait_bounded(sums, done & 1) && !*failed;
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      tmem_fence_after();
-#pragma unroll
-      for (int c = 0; c < kColumns; c += kChunk)
-        tmem_load<kChunk>(tmem + ((uint32_t)quarter << 21) + half * kColumns + c, r + c);
-      tmem_wait_load();
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(taken);
+      for (int part = k0; part < k1; part += p.part, ++done) {
+        ok = ok && mbar_wait_bounded(sums, done & 1) && !*failed;
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tmem_fence_after();
+        take_sums(tmem + ((uint32_t)quarter << 21) + half * kColumns, part == k0, r);
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(taken);
+      }
       if (!ok) {
 #pragma unroll
         for (int c = 0; c < kColumns; ++c) r[c] = 0x7FC00000u;
@@ -325,8 +170,7 @@ __global__ void __launch_bounds__(kMulThreads) matrix8_multiply(const __grid_con
 #pragma unroll
         for (int c = 0; c < kColumns; ++c) {
           const int col = half * kColumns + c, to = col / share, at = rank * share + col - to * share;
-          uint32_t remote;
-          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(mine + (uint32_t)at * 512u), "r"(to));
+          const uint32_t remote = cluster_addr(mine + (uint32_t)at * 512u, to);
           asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(r[c]) : "memory");
         }
         cluster_sync();
@@ -345,17 +189,7 @@ __global__ void __launch_bounds__(kMulThreads) matrix8_multiply(const __grid_con
             store_param(p.d, at, p.dtype, x);
         }
       } else {
-        const int64_t n = (int64_t)tile.n * kTileN + quarter * 32 + lane, m0 = (int64_t)tile.m * BT + half * kColumns;
-        const int count = (int)min((int64_t)kColumns, p.m - m0);
-        if (n < p.n) {
-          const int64_t at = m0 * p.ldd + n;
-          if (p.dtype == DOPT_F32)
-            store_sums(r, static_cast<float*>(p.d) + at, p.ldd, count, p.accumulate);
-          else if (p.dtype == DOPT_BF16)
-            store_sums(r, static_cast<__nv_bfloat16*>(p.d) + at, p.ldd, count, p.accumulate);
-          else
-            store_sums(r, static_cast<__half*>(p.d) + at, p.ldd, count, p.accumulate);
-        }
+        store_column(p, r, (int64_t)tile.n * kTileN + quarter * 32 + lane, (int64_t)tile.m * BT + half * kColumns);
       }
     }
   }
@@ -368,13 +202,13 @@ __global__ void __launch_bounds__(kMulThreads) matrix8_multiply(const __grid_con
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  if (warp == 2) tmem_free(tmem, S::kTmem);
+  if (warp == 2) tmem_free<1>(tmem, S::kTmem);
 }
 
 // --------------------------------------------------------------------- host --
 
-namespace {
 
+namespace {
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -396,7 +230,8 @@ int tensor_map_encoder(EncodeTiled* out) {
   return DOPT_OK;
 }
 
-// Codes in boxes of 128 bytes by `box` rows; what lies outside reads as 0.
+}  // namespace
+
 int operand_map(CUtensorMap* map, const dopt_matrix8& m, int box) {
   EncodeTiled encode;
   if (int st = tensor_map_encoder(&encode)) return st;
@@ -408,6 +243,19 @@ int operand_map(CUtensorMap* map, const dopt_matrix8& m, int box) {
   return r == CUDA_SUCCESS ? DOPT_OK : fail(DOPT_E_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
 }
 
+int scales_map(CUtensorMap* map, const dopt_matrix8& m) {
+  EncodeTiled encode;
+  if (int st = tensor_map_encoder(&encode)) return st;
+  const cuuint64_t size[2] = {128, (cuuint64_t)(scale_size(m.rows, m.cols) / 512)}, stride[1] = {512};
+  const cuuint32_t tile[2] = {128, 1}, step[2] = {1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, m.scales, size, stride, tile, step,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DOPT_OK : fail(DOPT_E_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
+}
+
+namespace {
+
 template <int BT, bool SPLIT>
 int launch_multiply(MulParams& p, const dopt_matrix8& a, const dopt_matrix8& b, cudaStream_t s) {
   const char* what = "matrix8_multiply launch";
@@ -418,6 +266,7 @@ int launch_multiply(MulParams& p, const dopt_matrix8& a, const dopt_matrix8& b, 
   if (st) return st;
   if ((st = operand_map(&p.b_map, b, kTileN))) return st;
   if ((st = operand_map(&p.a_map, a, BT))) return st;
+  if ((st = scales_map(&p.b_scales, b)) || (st = scales_map(&p.a_scales, a))) return st;
   int sms = 0;
   if ((st = device_sms(&sms))) return st;
   cudaLaunchAttribute attr[1];
@@ -486,14 +335,15 @@ extern "C" int dopt_matrix8_multiply(const dopt_matrix8* a, const dopt_matrix8* 
     if ((st = check_matrix8(*a, fn + "a: "))) return st;
     if ((st = check_matrix8(*b, fn + "b: "))) return st;
     MulParams p{};
-    p.b_scales = b->scales;
-    p.a_scales = a->scales;
     p.d = d;
     p.ldd = ldd;
     p.m = (int32_t)a->rows;
     p.n = (int32_t)b->rows;
     p.blocks = (int32_t)row_blocks(a->cols);
     p.groups = (int32_t)scale_groups(a->cols);
+    if (scale_size(std::max(a->rows, b->rows), a->cols) / 512 > INT32_MAX - 1)
+      return fail(DOPT_E_SIZE, fn + "too many elements");
+    p.part = d_dtype == DOPT_F32 ? kPart : p.blocks;
     p.dtype = d_dtype;
     p.accumulate = accumulate ? 1 : 0;
     const int64_t m = a->rows;
@@ -502,7 +352,8 @@ extern "C" int dopt_matrix8_multiply(const dopt_matrix8* a, const dopt_matrix8* 
     if (m <= 64) return multiply_rows<64>(p, *a, *b, s);
     int sms = 0;
     if ((st = device_sms(&sms))) return st;
-    if (m <= 128 || (m + 255) / 256 * ((b->rows + kTileN - 1) / kTileN) < sms) return multiply_rows<128>(p, *a, *b, s);
-    return multiply_rows<256>(p, *a, *b, s);
+    const int64_t pairs = (m + 255) / 256 * ((b->rows + 255) / 256);
+    if (m > 128 && pairs >= sms / 2) return launch_multiply_pair(p, *a, *b, s);
+    return multiply_rows<128>(p, *a, *b, s);
   });
 }

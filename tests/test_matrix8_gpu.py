@@ -158,6 +158,20 @@ def test_product_many_tiles(m, n, k):
     check_product(m, n, k, "bf16")
 
 
+@pytest.mark.parametrize("m,n,k", [(40, 300, 4096), (40, 300, 20000), (100, 300, 40000), (1500, 1000, 4096), (1500, 1000, 4300),
+                                   (2500, 2300, 4097), (2500, 2300, 8500)])
+@pytest.mark.parametrize("dtype,add", [("f32", False), ("f32", True), ("bf16", False)])
+def test_product_long_sums(m, n, k, dtype, add):
+    """Sums that are added up in parts, in every kernel: one tile's, a cluster's and a pair's."""
+    check_product(m, n, k, dtype, add=add)
+
+
+@pytest.mark.parametrize("m", [3, 30, 60, 100])
+def test_product_more_tiles_than_fit(m):
+    """Few rows of a and so many of b that nothing is split."""
+    check_product(m, 39000, 200, "bf16")
+
+
 @pytest.mark.parametrize("m", [7, 100, 300])
 def test_product_is_exact_on_small_integers(m):
     """Whole numbers whose sums fit 24 bits: every product and sum is exact, in any order, in fp32."""
