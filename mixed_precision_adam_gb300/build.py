@@ -1,10 +1,10 @@
 """Builds the in-tree CUDA library lib/libdopt.so for sm_103a.
 
-Fifteen translation units (the host shard map in C++; the device entry points
+Sixteen translation units (the host shard map in C++; the device entry points
 and the finalize kernel; the reduce/prepare kernels for each of the three
 grad dtypes; the AdamW kernel; the step over a list of tensors: entry
 points, grad norm, AdamW with fp32 and with 8-bit moments; the 8-bit
-matrices and their products, the RMS norm, dropout) are compiled in parallel
+matrices and their products, the RMS norm and its backward pass, dropout) are compiled in parallel
 and linked into one shared library with the CUDA runtime linked statically.  Run this file as a script
 (python mixed_precision_adam_gb300/build.py) or call build().
 
@@ -29,7 +29,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE]
 SOURCES = ["shard_map.cpp", "dopt_cuda.cu", "k1_f32.cu", "k1_bf16.cu", "k1_f16.cu", "k3.cu",
            "tensors.cu", "tensors_norm.cu", "tensors_adamw.cu", "tensors_adamw8.cu",
-           "matrix8.cu", "matrix8_multiply.cu", "matrix8_multiply_pair.cu", "rms_norm.cu", "dropout.cu"]
+           "matrix8.cu", "matrix8_multiply.cu", "matrix8_multiply_pair.cu", "rms_norm.cu",
+           "rms_norm_backward.cu", "dropout.cu"]
 
 
 def _deps():

@@ -14,27 +14,58 @@ struct DropoutParams {
   int64_t n;
   Drop drop;
   int32_t n_tiles;
-  bool vec;
 };
-constexpr int kDropTile = kThreads * 8;
+constexpr int kDropEights = 2;  // per thread
+constexpr int kDropTile = kThreads * 8 * kDropEights;
 
-template <typename T>
+// A CTA has a tile; a thread loads all of its elements before it uses one.
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) dropout(const __grid_constant__ DropoutParams p) {
   const uint32_t key = drop_key(p.drop);
-  for (int64_t t = blockIdx.x; t < p.n_tiles; t += gridDim.x) {
-    const int64_t i = t * kDropTile + threadIdx.x * 8;
-    const int n = (int)min((int64_t)8, p.n - i);
-    if (n <= 0) continue;
-    float f[8], r[8];
-    load_some(static_cast<const T*>(p.x) + i, n, p.vec, f);
-    if (p.residual) load_some(static_cast<const T*>(p.residual) + i, n, p.vec, r);
-    if (p.drop.threshold) drop_eight(f, (uint64_t)i, p.drop, key);
-    if (p.residual) {
+  const int64_t tile = (int64_t)blockIdx.x * kDropTile;
+  const T* x = static_cast<const T*>(p.x);
+  const T* residual = static_cast<const T*>(p.residual);
+  T* y = static_cast<T*>(p.y);
+  Eight8<T, VEC> a[kDropEights], r[kDropEights];
+  int64_t at[kDropEights];
+  int n[kDropEights];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] += r[j];
-    }
-    store_some(static_cast<T*>(p.y) + i, n, p.vec, f);
+  for (int v = 0; v < kDropEights; ++v) {
+    at[v] = tile + v * kThreads * 8 + (VEC ? threadIdx.x * 8 : threadIdx.x / 32 * 256 + threadIdx.x % 32);
+    n[v] = (int)max((int64_t)0, min((int64_t)256, p.n - at[v]));
+    if (VEC && n[v] < 8) n[v] = 0;
+    a[v].load(x + at[v], n[v]);
+    if (residual) r[v].load(residual + at[v], n[v]);
   }
+#pragma unroll
+  for (int v = 0; v < kDropEights; ++v) {
+    float f[8], g[8];
+    a[v].widen8(f);
+    if (p.drop.threshold) drop_eight<VEC>(f, (uint64_t)at[v], p.drop, key);
+    if (residual) {
+      r[v].widen8(g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] += g[j];
+    }
+    Eight8<T, VEC>::store(y + at[v], n[v], f);
+  }
+  // fewer than eight elements at the end
+  if (VEC && blockIdx.x == gridDim.x - 1 && threadIdx.x < (p.n & 7)) {
+    const int64_t i = (p.n & ~(int64_t)7) + threadIdx.x;
+    float f = widen<T>(x[i]);
+    if (p.drop.threshold) {
+      const uint32_t h = drop_hash((uint64_t)i >> 1, key);
+      f = (i & 1 ? h >> 16 : h & 0xFFFFu) < p.drop.threshold ? 0.f : f * p.drop.keep;
+    }
+    if (residual) f += widen<T>(residual[i]);
+    y[i] = narrow<T>(f);
+  }
+}
+
+template <typename T>
+int launch_dropout(const DropoutParams& p, bool vec, cudaStream_t s) {
+  const char* what = "dropout launch";
+  return vec ? launch_table<dropout<T, true>>(p, s, what, false, p.n_tiles) : launch_table<dropout<T, false>>(p, s, what, false, p.n_tiles);
 }
 
 }  // namespace dopt
@@ -63,11 +94,10 @@ extern "C" int dopt_dropout(const dopt_dropout_args* a, dopt_stream stream) {
     p.n = a->numel;
     p.drop = make_drop(a->drop, threshold);
     p.n_tiles = (int32_t)tiles;
-    p.vec = aligned_to(a->x, 16) && aligned_to(a->y, 16) && aligned_to(a->residual, 16);
+    const bool vec = aligned_to(a->x, 16) && aligned_to(a->y, 16) && aligned_to(a->residual, 16);
     const cudaStream_t s = (cudaStream_t)stream;
-    const char* what = "dropout launch";
-    return a->dtype == DOPT_F32    ? launch_table<dropout<float>>(p, s, what)
-           : a->dtype == DOPT_BF16 ? launch_table<dropout<__nv_bfloat16>>(p, s, what)
-                                   : launch_table<dropout<__half>>(p, s, what);
+    return a->dtype == DOPT_F32    ? launch_dropout<float>(p, vec, s)
+           : a->dtype == DOPT_BF16 ? launch_dropout<__nv_bfloat16>(p, vec, s)
+                                   : launch_dropout<__half>(p, vec, s);
   });
 }

@@ -22,7 +22,7 @@ struct MatrixSeg {
   int32_t tile0;
   int32_t across;  // tiles per row of tiles
   int16_t square;
-  int16_t vec;  // values are read four at a time
+  int16_t vec;  // the values' rows allow vectors
 };
 constexpr int kMatrixCap = 300, kMatrixSmallCap = 16;
 struct MatrixHead {
@@ -53,184 +53,250 @@ __device__ __forceinline__ MatrixTile place_matrix_tile(const P& p, const Matrix
   return a;
 }
 
+// Four consecutive values of a row as they are loaded, their magnitudes' bits
+// (in the type's own format, which orders them) and what those are in fp32.
 template <typename T>
-__device__ __forceinline__ void load_four(const T* p, float* f);
+struct Four {  // 16-bit types
+  uint2 r;
+  __device__ __forceinline__ void load(const T* p) { r = __ldcs(reinterpret_cast<const uint2*>(p)); }
+  // from shared memory
+  __device__ __forceinline__ void take(const T* p) { r = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void zero() { r = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void widen4(float (&f)[4]) const {
+    const float2 x = widen_pair<T>(r.x), y = widen_pair<T>(r.y);
+    f[0] = x.x, f[1] = x.y, f[2] = y.x, f[3] = y.y;
+  }
+  // Element j alone.
+  __device__ __forceinline__ float at(int j) const {
+    const float2 x = widen_pair<T>(j < 2 ? r.x : r.y);
+    return j & 1 ? x.y : x.x;
+  }
+  struct Top {  // of each of the four
+    uint32_t lo = 0u, hi = 0u;
+    __device__ __forceinline__ void add(const Four& v) {
+      lo = __vmaxu2(lo, v.r.x & 0x7FFF7FFFu);
+      hi = __vmaxu2(hi, v.r.y & 0x7FFF7FFFu);
+    }
+    __device__ __forceinline__ uint32_t all() const {
+      const uint32_t m = __vmaxu2(lo, hi);
+      return max(m & 0xFFFFu, m >> 16);
+    }
+    __device__ __forceinline__ uint4 each() const { return make_uint4(lo & 0xFFFFu, lo >> 16, hi & 0xFFFFu, hi >> 16); }
+  };
+  static __device__ __forceinline__ uint32_t fp32_bits(uint32_t top) { return __float_as_uint(widen_pair<T>(top).x); }
+};
 template <>
-__device__ __forceinline__ void load_four<float>(const float* p, float* f) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-}
-template <>
-__device__ __forceinline__ void load_four<__nv_bfloat16>(const __nv_bfloat16* p, float* f) {
-  const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p));
-  f[0] = __uint_as_float(a.x << 16), f[1] = __uint_as_float(a.x & 0xFFFF0000u);
-  f[2] = __uint_as_float(a.y << 16), f[3] = __uint_as_float(a.y & 0xFFFF0000u);
-}
-template <>
-__device__ __forceinline__ void load_four<__half>(const __half* p, float* f) {
-  const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p));
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a.x));
-  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&a.y));
-  f[0] = x.x, f[1] = x.y, f[2] = y.x, f[3] = y.y;
-}
+struct Four<float> {
+  float4 r;
+  __device__ __forceinline__ void load(const float* p) { r = __ldcs(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void take(const float* p) { r = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void zero() { r = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void widen4(float (&f)[4]) const { f[0] = r.x, f[1] = r.y, f[2] = r.z, f[3] = r.w; }
+  __device__ __forceinline__ float at(int j) const { return j == 0 ? r.x : j == 1 ? r.y : j == 2 ? r.z : r.w; }
+  struct Top {
+    uint4 t = make_uint4(0u, 0u, 0u, 0u);
+    __device__ __forceinline__ void add(const Four& v) {
+      t.x = max(t.x, __float_as_uint(v.r.x) & 0x7FFFFFFFu);
+      t.y = max(t.y, __float_as_uint(v.r.y) & 0x7FFFFFFFu);
+      t.z = max(t.z, __float_as_uint(v.r.z) & 0x7FFFFFFFu);
+      t.w = max(t.w, __float_as_uint(v.r.w) & 0x7FFFFFFFu);
+    }
+    __device__ __forceinline__ uint32_t all() const { return max(max(t.x, t.y), max(t.z, t.w)); }
+    __device__ __forceinline__ uint4 each() const { return t; }
+  };
+  static __device__ __forceinline__ uint32_t fp32_bits(uint32_t top) { return top; }
+};
 
 // Warp w has rows 16 w to 16 w + 15 of a tile, lane l its columns 4 l to
 // 4 l + 3: 64 values per thread, all of them loaded before the first is used.
 constexpr int kRowsPerWarp = 16;
 static_assert(kThreads / 32 * kRowsPerWarp == kBlock8, "a CTA has a tile's rows");
+template <typename T>
+constexpr int kMatrixCtas = sizeof(T) == 2 ? 3 : 2;  // per SM: what the values' registers allow
 
+// A CTA per tile: the next ones' loads then run under this one's stores.
 template <typename T, int CAP>
-__global__ void __launch_bounds__(kThreads, 2) matrix8_pack(const __grid_constant__ MatrixParamsT<CAP> p) {
+__global__ void __launch_bounds__(kThreads, kMatrixCtas<T>) matrix8_pack(const __grid_constant__ MatrixParamsT<CAP> p) {
   __shared__ uint32_t s_top[kThreads / 32][kBlock8];  // largest of each column, by warp
   __shared__ uint32_t s_tile[kThreads / 32];          // and of all of the warp's values
-  __shared__ uint4 s_turn[kBlock8 * kBlock8 / 16];    // transposed codes, 16 of a column at a time
+  // values on their way to their lanes, eight rows of a warp at a time; then
+  // the transposed codes, 16 of a column at a time
+  constexpr int kStageRows = 8;
+  __shared__ union {
+    T stage[kThreads / 32][kStageRows][kBlock8];
+    uint4 turn[kBlock8 * kBlock8 / 16];
+  } s;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  int hop = 1, si = 0;
-  if ((int)blockIdx.x < p.n_tiles) si = find_seg(p, blockIdx.x);
-  for (int t = blockIdx.x; t < p.n_tiles; t += gridDim.x) {
-    si = next_seg(p, si, t, hop);
-    const MatrixSeg& sg = p.seg[si];
-    const MatrixTile a = place_matrix_tile(p, sg, t);
-    const int n = a.cols - lane * 4;  // of this lane's columns
-    float f[kRowsPerWarp][4];
-    const T* src = static_cast<const T*>(sg.values) + (int64_t)(a.r0 + warp * kRowsPerWarp) * sg.ld + a.c0 + lane * 4;
+  const MatrixSeg& sg = p.seg[find_seg(p, blockIdx.x)];
+  const MatrixTile a = place_matrix_tile(p, sg, blockIdx.x);
+  const int rows = min(kRowsPerWarp, a.rows - warp * kRowsPerWarp);  // of the warp
+  Four<T> f[kRowsPerWarp];
+  const T* src = static_cast<const T*>(sg.values) + ((int64_t)a.r0 + warp * kRowsPerWarp) * sg.ld + a.c0;
+  if (sg.vec && a.cols == kBlock8 && rows == kRowsPerWarp) {
+#pragma unroll
+    for (int k = 0; k < kRowsPerWarp; ++k) f[k].load(src + k * sg.ld + lane * 4);
+  } else {
+    // consecutive lanes load consecutive elements, and take four through
+    // shared memory
+#pragma unroll
+    for (int half = 0; half < kRowsPerWarp; half += kStageRows) {
+      T t[kStageRows][4];
+#pragma unroll
+      for (int k = 0; k < kStageRows; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = lane + 32 * j;
+          t[k][j] = half + k < rows && c < a.cols ? __ldcs(src + (half + k) * sg.ld + c) : narrow<T>(0.f);
+        }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kStageRows; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s.stage[warp][k][lane + 32 * j] = t[k][j];
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kStageRows; ++k) f[half + k].take(&s.stage[warp][k][lane * 4]);
+    }
+  }
+  typename Four<T>::Top column;
+#pragma unroll
+  for (int k = 0; k < kRowsPerWarp; ++k) column.add(f[k]);
+  if (sg.square) {
+    const uint32_t all = __reduce_max_sync(0xFFFFFFFFu, column.all());
+    if (lane == 0) s_tile[warp] = all;
+  } else if (sg.codes_t) {
+    *reinterpret_cast<uint4*>(&s_top[warp][lane * 4]) = column.each();
+  }
+  __syncthreads();
+  uint32_t scale = 0u;
+  if (sg.square) {
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) scale = max(scale, s_tile[w]);
+    scale = m_scale_of(Four<T>::fp32_bits(scale));
+  }
+  const float factor = code_factor(scale);
+  if (sg.codes) {
+    uint8_t* dst = sg.codes + ((int64_t)a.r0 + warp * kRowsPerWarp) * sg.ld_out + a.c0 + lane * 4;
+    const int n = a.cols - lane * 4;
+    uint32_t mine = scale;  // lane k: row k's scale
 #pragma unroll
     for (int k = 0; k < kRowsPerWarp; ++k) {
-      const bool in = warp * kRowsPerWarp + k < a.rows;
-      if (in && sg.vec && n >= 4) {
-        load_four<T>(src + k * sg.ld, f[k]);
+      uint32_t sc = scale;
+      float up = factor;
+      if (!sg.square) {
+        typename Four<T>::Top row;
+        row.add(f[k]);
+        sc = m_scale_of(Four<T>::fp32_bits(__reduce_max_sync(0xFFFFFFFFu, row.all())));
+        up = code_factor(sc);
+        if (lane == k) mine = sc;
+      }
+      if (k >= rows) continue;
+      float x[4];
+      f[k].widen4(x);
+      const uint32_t c = four_codes(x, up, sc == 255u);
+      if (n >= 4) {
+        __stcs(reinterpret_cast<uint32_t*>(dst + k * sg.ld_out), c);
       } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[k][j] = in && j < n ? widen<T>(src[k * sg.ld + j]) : 0.f;
+        for (int j = 0; j < n; ++j) dst[k * sg.ld_out + j] = (uint8_t)(c >> (8 * j));
       }
     }
-    uint32_t column[4] = {0u, 0u, 0u, 0u}, row[kRowsPerWarp], all = 0u;
+    if (lane < rows)
+      sg.scales[scale_place((int64_t)a.r0 + warp * kRowsPerWarp + lane, a.c0 / kBlock8, (uint32_t)scale_groups(sg.cols))] =
+          (uint8_t)mine;
+  }
+  if (!sg.codes_t) return;
 #pragma unroll
-    for (int k = 0; k < kRowsPerWarp; ++k) {
+  for (int j = 0; j < 4; ++j) {
+    uint32_t sc = scale;
+    float up = factor;
+    if (!sg.square) {
       uint32_t top = 0u;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t b = __float_as_uint(f[k][j]) & 0x7FFFFFFFu;
-        column[j] = max(column[j], b);
-        top = max(top, b);
-      }
-      row[k] = top;
-      all = max(all, top);
+      for (int w = 0; w < kThreads / 32; ++w) top = max(top, s_top[w][lane * 4 + j]);
+      sc = m_scale_of(Four<T>::fp32_bits(top));
+      up = code_factor(sc);
     }
-    if (sg.square) {
-      all = __reduce_max_sync(0xFFFFFFFFu, all);
-      if (lane == 0) s_tile[warp] = all;
-    } else if (sg.codes_t) {
-      *reinterpret_cast<uint4*>(&s_top[warp][lane * 4]) = make_uint4(column[0], column[1], column[2], column[3]);
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float v[4] = {f[4 * q].at(j), f[4 * q + 1].at(j), f[4 * q + 2].at(j), f[4 * q + 3].at(j)};
+      w[q] = four_codes(v, up, sc == 255u);
     }
-    __syncthreads();
-    uint32_t scale = 0u;
-    if (sg.square) {
+    // column 4 l + j holds eight pieces of 16 codes; turned by l so that
+    // neither the lanes' writes here nor the reads below share banks
+    s.turn[(lane * 4 + j) * 8 + ((warp + lane) & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (warp == 0 && lane * 4 + j < a.cols && a.rows > 0)
+      sg.scales_t[scale_place((int64_t)a.c0 + lane * 4 + j, a.r0 / kBlock8, (uint32_t)scale_groups(sg.rows))] = (uint8_t)sc;
+  }
+  __syncthreads();
+  // eight lanes write the 128 codes of a column
 #pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) scale = max(scale, s_tile[w]);
-      scale = m_scale_of(scale);
+  for (int k = 0; k < kBlock8 * 8 / kThreads; ++k) {
+    const int c = k * (kThreads / 8) + threadIdx.x / 8, piece = threadIdx.x % 8;
+    if (c >= a.cols) continue;
+    const uint4 v = s.turn[c * 8 + ((piece + (c >> 2)) & 7)];
+    uint8_t* dst = sg.codes_t + ((int64_t)a.c0 + c) * sg.ld_t + a.r0 + piece * 16;
+    const int m = a.rows - piece * 16;
+    if (m >= 16) {
+      __stcs(reinterpret_cast<uint4*>(dst), v);
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (j < m) dst[j] = (uint8_t)(w[j / 4] >> (8 * (j & 3)));
     }
-    const float factor = code_factor(scale);
-    if (sg.codes) {
-      uint8_t* dst = sg.codes + (int64_t)(a.r0 + warp * kRowsPerWarp) * sg.ld_out + a.c0 + lane * 4;
-      const uint32_t groups = (uint32_t)scale_groups(sg.cols);
-#pragma unroll
-      for (int k = 0; k < kRowsPerWarp; ++k) {
-        const int r = warp * kRowsPerWarp + k;
-        uint32_t s = scale;
-        float up = factor;
-        if (!sg.square) {
-          s = m_scale_of(__reduce_max_sync(0xFFFFFFFFu, row[k]));
-          up = code_factor(s);
-        }
-        if (r >= a.rows) continue;
-        const uint32_t c = four_codes(f[k], up, s == 255u);
-        if (n >= 4) {
-          *reinterpret_cast<uint32_t*>(dst + k * sg.ld_out) = c;
-        } else {
-          for (int j = 0; j < n; ++j) dst[k * sg.ld_out + j] = (uint8_t)(c >> (8 * j));
-        }
-        if (lane == 0) sg.scales[scale_place(a.r0 + r, a.c0 / kBlock8, groups)] = (uint8_t)s;
-      }
-    }
-    if (sg.codes_t) {
-      const uint32_t groups = (uint32_t)scale_groups(sg.rows);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t s = scale;
-        float up = factor;
-        if (!sg.square) {
-          uint32_t top = 0u;
-#pragma unroll
-          for (int w = 0; w < kThreads / 32; ++w) top = max(top, s_top[w][lane * 4 + j]);
-          s = m_scale_of(top);
-          up = code_factor(s);
-        }
-        uint32_t w[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float v[4] = {f[4 * q][j], f[4 * q + 1][j], f[4 * q + 2][j], f[4 * q + 3][j]};
-          w[q] = four_codes(v, up, s == 255u);
-        }
-        // column 4 l + j holds eight pieces of 16 codes; turned by l so that
-        // neither the lanes' writes here nor the reads below share banks
-        s_turn[(lane * 4 + j) * 8 + ((warp + lane) & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
-        if (warp == 0 && j < n) sg.scales_t[scale_place(a.c0 + lane * 4 + j, a.r0 / kBlock8, groups)] = (uint8_t)s;
-      }
-      __syncthreads();
-      // eight lanes write the 128 codes of a column
-#pragma unroll
-      for (int k = 0; k < kBlock8 * 8 / kThreads; ++k) {
-        const int c = k * (kThreads / 8) + threadIdx.x / 8, piece = threadIdx.x % 8;
-        if (c >= a.cols) continue;
-        const uint4 v = s_turn[c * 8 + ((piece + (c >> 2)) & 7)];
-        uint8_t* dst = sg.codes_t + (int64_t)(a.c0 + c) * sg.ld_t + a.r0 + piece * 16;
-        const int m = a.rows - piece * 16;
-        if (m >= 16) {
-          *reinterpret_cast<uint4*>(dst) = v;
-        } else {
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (j < m) dst[j] = (uint8_t)(w[j / 4] >> (8 * (j & 3)));
-        }
-      }
-    }
-    __syncthreads();  // the tile's shared arrays have been read
   }
 }
 
-// A warp has 16 rows of a tile, as above; lane l its columns 4 l to 4 l + 3.
+// A warp has 16 rows of a tile.  Where the values can be written in vectors
+// and the tile is whole, a lane has 16 codes of every fourth row; else
+// consecutive lanes have consecutive elements.
 template <typename T, int CAP>
-__global__ void __launch_bounds__(kThreads, 2) matrix8_unpack(const __grid_constant__ MatrixParamsT<CAP> p) {
+__global__ void __launch_bounds__(kThreads, 4) matrix8_unpack(const __grid_constant__ MatrixParamsT<CAP> p) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  int hop = 1, si = 0;
-  if ((int)blockIdx.x < p.n_tiles) si = find_seg(p, blockIdx.x);
-  for (int t = blockIdx.x; t < p.n_tiles; t += gridDim.x) {
-    si = next_seg(p, si, t, hop);
-    const MatrixSeg& sg = p.seg[si];
-    const MatrixTile a = place_matrix_tile(p, sg, t);
-    const int n = a.cols - lane * 4;
-    const uint32_t groups = (uint32_t)scale_groups(sg.cols);
-#pragma unroll 4
-    for (int k = 0; k < kRowsPerWarp; ++k) {
-      const int r = warp * kRowsPerWarp + k;
-      if (r >= a.rows || n <= 0) continue;
-      const int64_t at = (int64_t)(a.r0 + r) * sg.ld_out + a.c0 + lane * 4;
-      const float unit = m_unit(sg.scales[scale_place(a.r0 + r, a.c0 / kBlock8, groups)]);
-      uint2 c = make_uint2(0u, 0u);
-      if (n >= 4) {
-        c.x = *reinterpret_cast<const uint32_t*>(sg.codes + at);
-      } else {
-        for (int j = 0; j < n; ++j) c.x |= (uint32_t)sg.codes[at + j] << (8 * j);
-      }
-      float f[8];
-      widen_codes(c, f);
-      T* dst = static_cast<T*>(sg.values) + (int64_t)(a.r0 + r) * sg.ld + a.c0 + lane * 4;
+  const MatrixSeg& sg = p.seg[find_seg(p, blockIdx.x)];
+  const MatrixTile a = place_matrix_tile(p, sg, blockIdx.x);
+  const int rows = min(kRowsPerWarp, a.rows - warp * kRowsPerWarp);
+  const int64_t r0 = (int64_t)a.r0 + warp * kRowsPerWarp;
+  const uint32_t groups = (uint32_t)scale_groups(sg.cols), block = a.c0 / kBlock8;
+  const uint8_t* codes = sg.codes + r0 * sg.ld_out + a.c0;
+  T* values = static_cast<T*>(sg.values) + r0 * sg.ld + a.c0;
+  if (sg.vec && a.cols == kBlock8 && rows == kRowsPerWarp) {
+    const int c = lane % 8 * 16;
+    uint4 code[4];
+    uint32_t s[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < n) dst[j] = narrow<T>(__fmul_rn(f[j], unit));
+    for (int k = 0; k < 4; ++k) {
+      const int r = lane / 8 + 4 * k;
+      code[k] = __ldcs(reinterpret_cast<const uint4*>(codes + r * sg.ld_out + c));
+      s[k] = sg.scales[scale_place(r0 + r, block, groups)];
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float unit = m_unit(s[k]);
+      T* dst = values + (lane / 8 + 4 * k) * sg.ld + c;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float f[8];
+        widen_codes(q ? make_uint2(code[k].z, code[k].w) : make_uint2(code[k].x, code[k].y), f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], unit);
+        Eight8<T, true>::store(dst + 8 * q, 8, f);
+      }
+    }
+    return;
+  }
+#pragma unroll 4
+  for (int r = 0; r < rows; ++r) {
+    const float unit = m_unit(sg.scales[scale_place(r0 + r, block, groups)]);
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = lane + 32 * j < a.cols ? __ldcs(codes + r * sg.ld_out + lane + 32 * j) : 0u;
+    float f[8];
+    widen_codes(make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, 0u), f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (lane + 32 * j < a.cols) __stcs(values + r * sg.ld + lane + 32 * j, narrow<T>(__fmul_rn(f[j], unit)));
   }
 }
 
@@ -239,8 +305,8 @@ namespace {
 template <auto Small, auto Big>
 int launch_matrices(const MatrixParamsT<kMatrixCap>& p, cudaStream_t s, const char* what) {
   if (p.n_seg <= kMatrixSmallCap)
-    return launch_table<Small>(compact_table<MatrixParamsT<kMatrixSmallCap>, MatrixHead>(p), s, what);
-  return launch_table<Big>(p, s, what);
+    return launch_table<Small>(compact_table<MatrixParamsT<kMatrixSmallCap>, MatrixHead>(p), s, what, false, p.n_tiles);
+  return launch_table<Big>(p, s, what, false, p.n_tiles);
 }
 template <typename T>
 int launch_pack(const MatrixParamsT<kMatrixCap>& p, cudaStream_t s) {
@@ -323,7 +389,8 @@ int run_matrices(const dopt_matrix_values* ms, int32_t n, bool pack, cudaStream_
       g.tile0 = p.n_tiles;
       g.across = (int32_t)row_blocks(m.cols);
       g.square = m.block == DOPT_BLOCK_SQUARE;
-      g.vec = aligned_to(m.values, 4 * elem) && m.ld % 4 == 0;
+      // packing reads four values at a time, unpacking writes 16 bytes
+      g.vec = pack ? aligned_to(m.values, 4 * elem) && m.ld % 4 == 0 : eight_vectors(m.values, m.ld, elem);
       p.n_tiles += (int32_t)tiles_of(m);
     }
     if (int st = flush()) return st;

@@ -3,7 +3,7 @@
 // a scale byte, and the dropout's random numbers.
 //   matrix8.cu          -- values to codes and back
 //   matrix8_multiply*.cu -- the products
-//   rms_norm.cu         -- the norm and its backward pass
+//   rms_norm*.cu        -- the norm and its backward pass
 //   dropout.cu
 #pragma once
 
@@ -34,82 +34,103 @@ inline bool eight_vectors(const void* p, int64_t ld, size_t elem) {
   return aligned_to(p, 16) && (ld * (int64_t)elem) % 16 == 0;
 }
 
+// Eight elements of a row as a load leaves them, widened only when they are
+// used, so that a thread's loads are all under way before the first wait.
+// VEC: consecutive elements in one access (two for fp32); else every 32nd,
+// so that a warp's accesses are consecutive.
+template <typename T, bool VEC>
+struct Eight8 {
+  T e[8];
+  // of the elements at p, p + 32, ... those before `n`, zeros after them
+  __device__ __forceinline__ void load(const T* p, int n) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = 32 * j < n ? __ldcs(p + 32 * j) : narrow<T>(0.f);
+  }
+  __device__ __forceinline__ void widen8(float (&f)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = widen<T>(e[j]);
+  }
+  static __device__ __forceinline__ void store(T* p, int n, const float (&f)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (32 * j < n) __stcs(p + 32 * j, narrow<T>(f[j]));
+  }
+};
+template <>
+struct Eight8<float, true> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p, int n) {
+    a = b = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (n > 0) {
+      a = __ldcs(reinterpret_cast<const float4*>(p));
+      b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    }
+  }
+  __device__ __forceinline__ void widen8(float (&f)[8]) const {
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(float* p, int n, const float (&f)[8]) {
+    if (n <= 0) return;
+    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+  }
+};
+// Two 16-bit elements of a word.
 template <typename T>
-__device__ __forceinline__ void load_eight(const T* p, float (&f)[8]);
+__device__ __forceinline__ float2 widen_pair(uint32_t w);
 template <>
-__device__ __forceinline__ void load_eight<float>(const float* p, float (&f)[8]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+__device__ __forceinline__ float2 widen_pair<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 template <>
-__device__ __forceinline__ void load_eight<__nv_bfloat16>(const __nv_bfloat16* p, float (&f)[8]) {
-  const uint4 r = __ldcs(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    f[2 * k] = __uint_as_float(w[k] << 16);
-    f[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-  }
-}
-template <>
-__device__ __forceinline__ void load_eight<__half>(const __half* p, float (&f)[8]) {
-  const uint4 r = __ldcs(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-    f[2 * k] = x.x;
-    f[2 * k + 1] = x.y;
-  }
-}
-template <typename T>
-__device__ __forceinline__ void store_eight(T* p, const float (&f)[8]);
-template <>
-__device__ __forceinline__ void store_eight<float>(float* p, const float (&f)[8]) {
-  __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
-  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
-}
-template <>
-__device__ __forceinline__ void store_eight<__nv_bfloat16>(__nv_bfloat16* p, const float (&f)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const __nv_bfloat162 h = __float22bfloat162_rn(make_float2(f[2 * k], f[2 * k + 1]));
-    w[k] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
-}
-template <>
-__device__ __forceinline__ void store_eight<__half>(__half* p, const float (&f)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const __half2 h = __float22half2_rn(make_float2(f[2 * k], f[2 * k + 1]));
-    w[k] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
-}
-
-// The first n (0 to 8) elements at p, zeros after them: in one access where
-// the rows allow it (vec) and all eight are there.
-template <typename T>
-__device__ __forceinline__ void load_some(const T* p, int n, bool vec, float (&f)[8]) {
-  if (vec && n == 8) {
-    load_eight<T>(p, f);
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = j < n ? widen<T>(p[j]) : 0.f;
+__device__ __forceinline__ float2 widen_pair<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 template <typename T>
-__device__ __forceinline__ void store_some(T* p, int n, bool vec, const float (&f)[8]) {
-  if (vec && n == 8) {
-    store_eight<T>(p, f);
-    return;
+__device__ __forceinline__ uint32_t narrow_pair(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t narrow_pair<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __float22bfloat162_rn(make_float2(a, b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t narrow_pair<__half>(float a, float b) {
+  const __half2 h = __float22half2_rn(make_float2(a, b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T>
+struct Eight8<T, true> {
+  uint4 r;
+  __device__ __forceinline__ void load(const T* p, int n) {
+    r = make_uint4(0u, 0u, 0u, 0u);
+    if (n > 0) r = __ldcs(reinterpret_cast<const uint4*>(p));
   }
+  __device__ __forceinline__ void widen8(float (&f)[8]) const {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < n) p[j] = narrow<T>(f[j]);
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = widen_pair<T>(w[k]);
+      f[2 * k] = x.x;
+      f[2 * k + 1] = x.y;
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, int n, const float (&f)[8]) {
+    if (n <= 0) return;
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(narrow_pair<T>(f[0], f[1]), narrow_pair<T>(f[2], f[3]),
+                                                   narrow_pair<T>(f[4], f[5]), narrow_pair<T>(f[6], f[7])));
+  }
+};
+// f rounded to T and widened again.
+template <typename T>
+__device__ __forceinline__ void round_eight(float (&f)[8]) {
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = widen_pair<T>(narrow_pair<T>(f[2 * k], f[2 * k + 1]));
+      f[2 * k] = x.x;
+      f[2 * k + 1] = x.y;
+    }
+  }
 }
 
 // -------------------------------------------------------------------- codes --
@@ -165,22 +186,27 @@ constexpr uint32_t kHashHigh = 0x3C6EF372u;
 __device__ __forceinline__ uint32_t drop_key(const Drop& d) {
   return d.key + (d.threshold && d.d_step ? (uint32_t)*d.d_step * kHashStep : 0u);
 }
-// Drops among the eight elements from element i on.  A pair of elements (an
-// even one and the next) has one hash; from an odd i the eight lie in five.
+__device__ __forceinline__ uint32_t drop_hash(uint64_t pair, uint32_t key) {
+  return hash_pair((uint32_t)pair * kHashPair + (uint32_t)(pair >> 32) * kHashHigh + key);
+}
+// Drops among eight elements from element i on: consecutive ones with i a
+// multiple of 8 (VEC), two to a hash; or every 32nd.
+template <bool VEC>
 __device__ __forceinline__ void drop_eight(float (&f)[8], uint64_t i, const Drop& d, uint32_t key) {
-  const uint64_t pair = i >> 1;
-  const bool odd = i & 1;
-  uint32_t h = hash_pair((uint32_t)pair * kHashPair + (uint32_t)(pair >> 32) * kHashHigh + key);
-  if (odd) h >>= 16;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint64_t q = pair + k + 1;
-    uint32_t next = 0u;
-    if (k < 3 || odd) next = hash_pair((uint32_t)q * kHashPair + (uint32_t)(q >> 32) * kHashHigh + key);
-    const uint32_t r0 = h & 0xFFFFu, r1 = odd ? next & 0xFFFFu : h >> 16;
-    f[2 * k] = r0 < d.threshold ? 0.f : f[2 * k] * d.keep;
-    f[2 * k + 1] = r1 < d.threshold ? 0.f : f[2 * k + 1] * d.keep;
-    h = odd ? next >> 16 : next;
+  for (int k = 0; k < 8; ++k) {
+    uint32_t r;
+    if constexpr (VEC) {
+      if (k & 1) continue;
+      const uint32_t h = drop_hash((i >> 1) + k / 2, key);
+      f[k + 1] = (h >> 16) < d.threshold ? 0.f : f[k + 1] * d.keep;
+      r = h & 0xFFFFu;
+    } else {
+      const uint64_t at = i + 32 * k;
+      const uint32_t h = drop_hash(at >> 1, key);
+      r = at & 1 ? h >> 16 : h & 0xFFFFu;
+    }
+    f[k] = r < d.threshold ? 0.f : f[k] * d.keep;
   }
 }
 

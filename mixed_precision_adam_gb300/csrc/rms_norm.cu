@@ -1,22 +1,8 @@
-// rms_norm.cu -- the RMS norm with the residual's addition, values or 8-bit
-// codes out, and its backward pass.
-//
-// Both are bound by memory: each value is read once and stays in registers
-// between the row's sum and its use.  G threads have a row, each of them V
-// vectors of eight consecutive columns; a warp where a row fits it, so that
-// its sum needs no shared memory.
-#include "matrix8.cuh"
+// rms_norm.cu -- the RMS norm with dropout and the residual's addition before
+// it, values or 8-bit codes out, and the C entry points of the norm.
+#include "rms_norm.cuh"
 
 namespace dopt {
-
-struct RowsIn {
-  const void* data;
-  int64_t ld;
-};
-struct RowsOut {
-  void* data;
-  int64_t ld;
-};
 
 struct NormRows {
   RowsIn x, residual;
@@ -31,24 +17,10 @@ struct NormRows {
   uint32_t groups;  // of scale bytes
   float eps;
   Drop drop;
-  bool vec, gain_f32;
-  int32_t n_tiles;  // groups of threads' rows, for the launch
+  bool gain_f32;
+  int32_t n_tiles;
 };
 
-// A sum over the G threads that have a row.
-template <int G>
-__device__ __forceinline__ float row_sum(float x, float (&s_sum)[32]) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-  if constexpr (G > 32) {
-    if (threadIdx.x % 32 == 0) s_sum[threadIdx.x / 32] = x;
-    __syncthreads();
-    x = s_sum[0];
-#pragma unroll
-    for (int w = 1; w < G / 32; ++w) x += s_sum[w];
-  }
-  return x;
-}
 template <int G>
 __device__ __noinline__ double row_sum_wide(double x, double (&s_sum)[32]) {
 #pragma unroll
@@ -63,63 +35,94 @@ __device__ __noinline__ double row_sum_wide(double x, double (&s_sum)[32]) {
   return x;
 }
 
-// A gain's eight values from column c on, zeros past the end.
-template <typename T>
-__device__ __forceinline__ void load_gain(const void* gain, bool f32, int c, int cols, float (&g)[8]) {
+// The codes of a thread's eight values and their blocks' scale bytes.
+template <bool VEC>
+__device__ __forceinline__ void store_codes(const NormRows& p, int64_t row, int c, const float (&f)[8]) {
+  uint8_t* dst = p.codes + row * p.ld_codes + c;
+  if constexpr (VEC) {
+    // a block of 128 columns is sixteen threads'
+    uint32_t top = top_of(f);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int at = c + j;
-    g[j] = at < cols ? (f32 ? __ldg(static_cast<const float*>(gain) + at) : widen<T>(static_cast<const T*>(gain)[at])) : 0.f;
+    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const uint32_t s = m_scale_of(top);
+    const float up = code_factor(s);
+    const uint2 code = make_uint2(four_codes(f, up, s == 255u), four_codes(f + 4, up, s == 255u));
+    if (c < p.cols) {
+      *reinterpret_cast<uint2*>(dst) = code;
+      if (threadIdx.x % 16 == 0) p.scales[scale_place(row, c / kBlock8, p.groups)] = (uint8_t)s;
+    }
+  } else {
+    // four values of every lane
+#pragma unroll
+    for (int q = 0; q < 8; q += 4) {
+      uint32_t top = 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(f[q + j]) & 0x7FFFFFFFu);
+      const uint32_t s = m_scale_of(__reduce_max_sync(0xFFFFFFFFu, top));
+      const uint32_t code = four_codes(f + q, code_factor(s), s == 255u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + 32 * (q + j) < p.cols) dst[32 * (q + j)] = (uint8_t)(code >> (8 * j));
+      if (threadIdx.x % 32 == 0 && c + 32 * q < p.cols)
+        p.scales[scale_place(row, (c + 32 * q) / kBlock8, p.groups)] = (uint8_t)s;
+    }
   }
 }
 
-// Rows that a CTA has at once, and its threads.
-template <int G>
-constexpr int kRowsAtOnce = G == 32 ? 8 : 1;
-template <int G>
-constexpr int kRowThreads = G == 32 ? 256 : G;
+// Whether a thread keeps the next row's values under this one's work: where
+// their registers leave room.
+template <typename T, int V>
+constexpr bool kRowAhead = V * sizeof(T) <= 8;
 
-template <typename T, int G, int V>
+template <typename T, int G, int V, bool VEC>
 __global__ void __launch_bounds__(kRowThreads<G>) rms_norm(const __grid_constant__ NormRows p) {
   __shared__ float s_sum[2][32];
   __shared__ double s_wide[32];
+  using Piece = Eight8<T, VEC>;
   const int g = threadIdx.x % G;
   const uint32_t key = drop_key(p.drop);
-  float gain[V][8];
-#pragma unroll
-  for (int v = 0; v < V; ++v) load_gain<T>(p.gain, p.gain_f32, (v * G + g) * 8, p.cols, gain[v]);
+  const T* x = static_cast<const T*>(p.x.data);
+  const T* residual = static_cast<const T*>(p.residual.data);
   const int64_t stride = (int64_t)gridDim.x * kRowsAtOnce<G>;
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * kRowsAtOnce<G> + threadIdx.x / G; row < p.rows; row += stride) {
-    float f[V][8];
+  int64_t row = (int64_t)blockIdx.x * kRowsAtOnce<G> + threadIdx.x / G;
+  Piece xs[V], rs[V];
+  auto load = [&](int64_t at) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (v * G + g) * 8, n = max(0, min(8, p.cols - c));
-      load_some(static_cast<const T*>(p.x.data) + row * p.x.ld + c, n, p.vec, f[v]);
+      const int c = first_column<V, VEC, G>(g, v);
+      xs[v].load(x + at * p.x.ld + c, p.cols - c);
+      if (residual) rs[v].load(residual + at * p.residual.ld + c, p.cols - c);
     }
-    if (p.residual.data || p.drop.threshold) {
+  };
+  if (row < p.rows) load(row);
+  float gain[V][8];
+  load_gain<T, V, VEC, G>(p.gain, p.gain_f32, g, p.cols, gain);
+  int turn = 0;
+  for (; row < p.rows; row += stride) {
+    float f[V][8], sum = 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int c = (v * G + g) * 8, n = max(0, min(8, p.cols - c));
-        if (p.drop.threshold && n > 0) drop_eight(f[v], (uint64_t)row * p.cols + c, p.drop, key);
-        if (p.residual.data) {
-          float r[8];
-          load_some(static_cast<const T*>(p.residual.data) + row * p.residual.ld + c, n, p.vec, r);
+    for (int v = 0; v < V; ++v) {
+      const int c = first_column<V, VEC, G>(g, v);
+      xs[v].widen8(f[v]);
+      if (p.drop.threshold) drop_eight<VEC>(f[v], (uint64_t)row * p.cols + c, p.drop, key);
+      if (residual) {
+        float r[8];
+        rs[v].widen8(r);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[v][j] += r[j];
-        }
-        // what the norm sees is what is stored: the backward pass, and a
-        // norm of h alone, then see the same
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[v][j] = j < n ? widen<T>(narrow<T>(f[v][j])) : 0.f;
-        if (p.h.data) store_some(static_cast<T*>(p.h.data) + row * p.h.ld + c, n, p.vec, f[v]);
+        for (int j = 0; j < 8; ++j) f[v][j] += r[j];
       }
+      // what the norm sees is what is stored: the backward pass, and a norm
+      // of h alone, then see the same
+      round_eight<T>(f[v]);
     }
-    float sum = 0.f;
+    if (kRowAhead<T, V> && row + stride < p.rows) load(row + stride);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+      const int c = first_column<V, VEC, G>(g, v);
+      if (p.h.data) Piece::store(static_cast<T*>(p.h.data) + row * p.h.ld + c, p.cols - c, f[v]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum = fmaf(f[v][j], f[v][j], sum);
+    }
     sum = row_sum<G>(sum, s_sum[turn]);
     turn ^= 1;
     float rstd;
@@ -140,210 +143,42 @@ __global__ void __launch_bounds__(kRowThreads<G>) rms_norm(const __grid_constant
     if (g == 0 && p.rstd) p.rstd[row] = rstd;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (v * G + g) * 8, n = max(0, min(8, p.cols - c));
+      const int c = first_column<V, VEC, G>(g, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[v][j] = j < n ? f[v][j] * rstd * gain[v][j] : 0.f;
-      if (p.y.data) store_some(static_cast<T*>(p.y.data) + row * p.y.ld + c, n, p.vec, f[v]);
-      if (p.codes) {
-        // a block of 128 columns is sixteen threads'
-        uint32_t top = top_of(f[v]);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        const uint32_t s = m_scale_of(top);
-        const float up = code_factor(s);
-        const uint2 code = make_uint2(four_codes(f[v], up, s == 255u), four_codes(f[v] + 4, up, s == 255u));
-        uint8_t* dst = p.codes + row * p.ld_codes + c;
-        if (n == 8) {
-          *reinterpret_cast<uint2*>(dst) = code;
-        } else {
-          for (int j = 0; j < n; ++j) dst[j] = (uint8_t)((j < 4 ? code.x : code.y) >> (8 * (j & 3)));
-        }
-        if (g % 16 == 0 && n > 0) p.scales[scale_place(row, c / kBlock8, p.groups)] = (uint8_t)s;
-      }
+      for (int j = 0; j < 8; ++j) f[v][j] = f[v][j] * rstd * gain[v][j];
+      if (p.y.data) Piece::store(static_cast<T*>(p.y.data) + row * p.y.ld + c, p.cols - c, f[v]);
+      if (p.codes) store_codes<VEC>(p, row, c, f[v]);
     }
+    if (!kRowAhead<T, V> && row + stride < p.rows) load(row + stride);
   }
-}
-
-// ----------------------------------------------------------- backward pass --
-
-struct NormBackRows {
-  RowsIn dy, h, dres;
-  RowsOut dh, dx;
-  const void* gain;
-  const float* rstd;
-  float* partial;  // of dgain, a row of cols per CTA; or NULL
-  int64_t rows;
-  int32_t cols;
-  Drop drop;
-  bool vec, gain_f32;
-  int32_t n_tiles;
-};
-
-// A CTA adds up its rows' dy * hat in registers, a column always in the same
-// thread; the CTAs' sums are added by a launch of its own in a fixed order.
-constexpr int kMaxParts = 608;  // CTAs, at most
-
-template <typename T, int G, int V>
-__global__ void __launch_bounds__(kRowThreads<G>) rms_norm_backward(const __grid_constant__ NormBackRows p) {
-  __shared__ float s_sum[2][32];
-  __shared__ float s_gain[G == 32 ? 8 * 32 * 8 : 1];
-  const int g = threadIdx.x % G;
-  const uint32_t key = drop_key(p.drop);
-  float gain[V][8], acc[V][8];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    load_gain<T>(p.gain, p.gain_f32, (v * G + g) * 8, p.cols, gain[v]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[v][j] = 0.f;
-  }
-  const int64_t stride = (int64_t)gridDim.x * kRowsAtOnce<G>;
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * kRowsAtOnce<G> + threadIdx.x / G; row < p.rows; row += stride) {
-    const float rstd = p.rstd[row];
-    float hat[V][8], dy[V][8], dot = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * G + g) * 8, n = max(0, min(8, p.cols - c));
-      load_some(static_cast<const T*>(p.h.data) + row * p.h.ld + c, n, p.vec, hat[v]);
-      load_some(static_cast<const T*>(p.dy.data) + row * p.dy.ld + c, n, p.vec, dy[v]);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        hat[v][j] *= rstd;
-        acc[v][j] = fmaf(dy[v][j], hat[v][j], acc[v][j]);
-        dy[v][j] *= gain[v][j];
-        dot = fmaf(dy[v][j], hat[v][j], dot);
-      }
-    dot = row_sum<G>(dot, s_sum[turn]) / (float)p.cols;
-    turn ^= 1;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * G + g) * 8, n = max(0, min(8, p.cols - c));
-      if (n == 0) continue;
-      float r[8];
-      if (p.dres.data) load_some(static_cast<const T*>(p.dres.data) + row * p.dres.ld + c, n, p.vec, r);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        dy[v][j] = rstd * fmaf(-hat[v][j], dot, dy[v][j]);
-        if (p.dres.data) dy[v][j] += r[j];
-      }
-      if (p.dh.data) store_some(static_cast<T*>(p.dh.data) + row * p.dh.ld + c, n, p.vec, dy[v]);
-      if (p.dx.data) {
-        drop_eight(dy[v], (uint64_t)row * p.cols + c, p.drop, key);
-        store_some(static_cast<T*>(p.dx.data) + row * p.dx.ld + c, n, p.vec, dy[v]);
-      }
-    }
-  }
-  if (!p.partial) return;
-  float* part = p.partial + (int64_t)blockIdx.x * p.cols;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = (v * G + g) * 8;
-    if constexpr (G == 32) {
-      // the warps' sums of these columns, in the warps' order
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s_gain[(threadIdx.x / 32 * 8 + j) * 32 + g] = acc[v][j];
-      __syncthreads();
-      const int j = threadIdx.x / 32;
-      float sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) sum += s_gain[(w * 8 + j) * 32 + g];
-      if (c + j < p.cols) part[c + j] = sum;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c + j < p.cols) part[c + j] = acc[v][j];
-    }
-  }
-}
-
-struct GainParams {
-  const float* partial;
-  float* dgain;
-  int32_t parts, cols, accumulate;
-  int32_t n_tiles;
-};
-constexpr int kGainColumns = 32;
-// 32 columns per CTA, each warp a share of the partial sums.
-__global__ void __launch_bounds__(kThreads) rms_norm_gain(const __grid_constant__ GainParams p) {
-  __shared__ float s_sum[kThreads / 32][32];
-  const int c = blockIdx.x * kGainColumns + threadIdx.x % 32, w = threadIdx.x / 32;
-  float sum = 0.f;
-  if (c < p.cols)
-    for (int k = w; k < p.parts; k += kThreads / 32) sum += p.partial[(int64_t)k * p.cols + c];
-  s_sum[w][threadIdx.x % 32] = sum;
-  __syncthreads();
-  if (w != 0 || c >= p.cols) return;
-#pragma unroll
-  for (int k = 1; k < kThreads / 32; ++k) sum += s_sum[k][threadIdx.x];
-  p.dgain[c] = p.accumulate ? p.dgain[c] + sum : sum;
 }
 
 namespace {
 
-// The kernel of a row length: a warp per row up to 1024 columns, then CTAs.
+template <typename T, int G, int V, bool VEC>
+int launch_one(const NormRows& p, cudaStream_t s) {
+  const char* what = "rms_norm launch";
+  int grid = 0;
+  if (int st = row_grid<rms_norm<T, G, V, VEC>, kRowThreads<G>>(p, (p.rows + kRowsAtOnce<G> - 1) / kRowsAtOnce<G>, &grid, what))
+    return st;
+  return launch_table<rms_norm<T, G, V, VEC>, 0, kRowThreads<G>>(p, s, what, false, grid);
+}
 static_assert(DOPT_NORM_MAX_COLS == 512 * 4 * 8, "the longest row's kernel");
-template <typename T, template <typename, int, int> class Launch, typename P>
-int launch_rows_t(P& p, cudaStream_t s, int* grid) {
+template <typename T, bool VEC>
+int launch_length(const NormRows& p, cudaStream_t s) {
   const int c = p.cols;
-  if (c <= 256) return Launch<T, 32, 1>::run(p, s, grid);
-  if (c <= 512) return Launch<T, 32, 2>::run(p, s, grid);
-  if (c <= 1024) return Launch<T, 32, 4>::run(p, s, grid);
-  if (c <= 2048) return Launch<T, 256, 1>::run(p, s, grid);
-  if (c <= 4096) return Launch<T, 256, 2>::run(p, s, grid);
-  if (c <= 8192) return Launch<T, 256, 4>::run(p, s, grid);
-  return Launch<T, 512, 4>::run(p, s, grid);
+  if (c <= 256) return launch_one<T, 32, 1, VEC>(p, s);
+  if (c <= 512) return launch_one<T, 32, 2, VEC>(p, s);
+  if (c <= 1024) return launch_one<T, 32, 4, VEC>(p, s);
+  if (c <= 2048) return launch_one<T, 256, 1, VEC>(p, s);
+  if (c <= 4096) return launch_one<T, 256, 2, VEC>(p, s);
+  if (c <= 8192) return launch_one<T, 512, 2, VEC>(p, s);
+  return launch_one<T, 512, 4, VEC>(p, s);
 }
-template <template <typename, int, int> class Launch, typename P>
-int launch_rows(int32_t dtype, P& p, cudaStream_t s, int* grid = nullptr) {
-  return dtype == DOPT_F32    ? launch_rows_t<float, Launch>(p, s, grid)
-         : dtype == DOPT_BF16 ? launch_rows_t<__nv_bfloat16, Launch>(p, s, grid)
-                              : launch_rows_t<__half, Launch>(p, s, grid);
+template <typename T>
+int launch_norm(const NormRows& p, bool vec, cudaStream_t s) {
+  return vec ? launch_length<T, true>(p, s) : launch_length<T, false>(p, s);
 }
-
-// As many CTAs as the device holds at once and the rows ask for.
-template <auto Kern, int THREADS, int ROWS, typename P>
-int row_grid(const P& p, int most, int* grid, const char* what) {
-  static std::atomic<int> known[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return fail(DOPT_E_CUDA, std::string("cudaGetDevice: ") + cudaGetErrorString(e));
-  int ctas = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
-  if (!ctas) {
-    int sms = 0, per_sm = 0;
-    if (int st = device_sms(&sms)) return st;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, Kern, THREADS, 0);
-    if (e != cudaSuccess || per_sm < 1)
-      return fail(DOPT_E_CUDA, std::string(what) + ": occupancy query: " + cudaGetErrorString(e));
-    ctas = per_sm * sms;
-    if (dev < 64) known[dev].store(ctas, std::memory_order_relaxed);
-  }
-  *grid = (int)std::min<int64_t>({(int64_t)ctas, (int64_t)most, (p.rows + ROWS - 1) / ROWS});
-  return DOPT_OK;
-}
-
-template <typename T, int G, int V>
-struct Forward {
-  static int run(const NormRows& p, cudaStream_t s, int*) {
-    const char* what = "rms_norm launch";
-    int grid = 0;
-    if (int st = row_grid<rms_norm<T, G, V>, kRowThreads<G>, kRowsAtOnce<G>>(p, INT32_MAX, &grid, what)) return st;
-    return launch_table<rms_norm<T, G, V>, 0, kRowThreads<G>>(p, s, what, false, grid);
-  }
-};
-template <typename T, int G, int V>
-struct Backward {
-  static int run(const NormBackRows& p, cudaStream_t s, int* parts) {
-    const char* what = "rms_norm_backward launch";
-    int grid = 0;
-    if (int st = row_grid<rms_norm_backward<T, G, V>, kRowThreads<G>, kRowsAtOnce<G>>(p, kMaxParts, &grid, what)) return st;
-    *parts = grid;
-    return launch_table<rms_norm_backward<T, G, V>, 0, kRowThreads<G>>(p, s, what, false, grid);
-  }
-};
 
 int check_rows(const dopt_rows& r, int64_t cols, size_t elem, const char* name, const std::string& fn) {
   if (!aligned_to(r.data, elem)) return fail(DOPT_E_ALIGN, fn + name + " not aligned to its elements");
@@ -412,9 +247,12 @@ int dopt_rms_norm(const dopt_rms_norm_args* a, dopt_stream stream) {
     p.groups = (uint32_t)scale_groups(a->cols);
     p.eps = (float)a->eps;
     p.drop = make_drop(a->drop, threshold);
-    p.vec = rows_vec(a->x, elem) && rows_vec(a->residual, elem) && rows_vec(a->h, elem) && rows_vec(a->y, elem);
+    const bool vec = a->cols % 8 == 0 && rows_vec(a->x, elem) && rows_vec(a->residual, elem) && rows_vec(a->h, elem) && rows_vec(a->y, elem);
     p.gain_f32 = a->gain_dtype == DOPT_F32;
-    return launch_rows<Forward>(a->dtype, p, (cudaStream_t)stream);
+    const cudaStream_t s = (cudaStream_t)stream;
+    return a->dtype == DOPT_F32    ? launch_norm<float>(p, vec, s)
+           : a->dtype == DOPT_BF16 ? launch_norm<__nv_bfloat16>(p, vec, s)
+                                   : launch_norm<__half>(p, vec, s);
   });
 }
 
@@ -475,13 +313,11 @@ int dopt_rms_norm_backward(const dopt_rms_norm_backward_args* a, void* workspace
     p.rows = a->rows;
     p.cols = (int32_t)a->cols;
     p.drop = make_drop(a->drop, threshold);
-    p.vec = rows_vec(a->dy, elem) && rows_vec(a->h, elem) && rows_vec(a->dres, elem) && rows_vec(a->dh, elem) && rows_vec(a->dx, elem);
+    const bool vec = a->cols % 8 == 0 && rows_vec(a->dy, elem) && rows_vec(a->h, elem) && rows_vec(a->dres, elem) && rows_vec(a->dh, elem) && rows_vec(a->dx, elem);
     p.gain_f32 = a->gain_dtype == DOPT_F32;
     int parts = 0;
-    if ((st = launch_rows<Backward>(a->dtype, p, s, &parts))) return st;
-    if (!a->dgain) return DOPT_OK;
-    GainParams g{p.partial, a->dgain, parts, p.cols, a->accumulate ? 1 : 0, 0};
-    return launch_table<rms_norm_gain>(g, s, "rms_norm_gain launch", false, (p.cols + kGainColumns - 1) / kGainColumns);
+    if ((st = launch_norm_backward(a->dtype, vec, p, s, &parts))) return st;
+    return a->dgain ? launch_norm_gain(p.partial, parts, p.cols, a->dgain, a->accumulate != 0, s) : DOPT_OK;
   });
 }
 
