@@ -18,18 +18,17 @@ struct NormRows {
   float eps;
   Drop drop;
   bool gain_f32;
-  int32_t n_tiles;
 };
 
-template <int G>
-__device__ __noinline__ double row_sum_wide(double x, double (&s_sum)[32]) {
+template <bool WARP>
+__device__ __noinline__ double row_sum_wide(double x, double (&s_sum)[kMaxRowThreads / 32]) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-  if constexpr (G > 32) {
+  if constexpr (!WARP) {
     if (threadIdx.x % 32 == 0) s_sum[threadIdx.x / 32] = x;
     __syncthreads();
     x = s_sum[0];
-    for (int w = 1; w < G / 32; ++w) x += s_sum[w];
+    for (int w = 1; w < (int)blockDim.x / 32; ++w) x += s_sum[w];
     __syncthreads();
   }
   return x;
@@ -74,35 +73,35 @@ __device__ __forceinline__ void store_codes(const NormRows& p, int64_t row, int 
 template <typename T, int V>
 constexpr bool kRowAhead = V * sizeof(T) <= 8;
 
-template <typename T, int G, int V, bool VEC>
-__global__ void __launch_bounds__(kRowThreads<G>) rms_norm(const __grid_constant__ NormRows p) {
-  __shared__ float s_sum[2][32];
-  __shared__ double s_wide[32];
+template <typename T, int V, bool VEC, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : kMaxRowThreads) rms_norm(const __grid_constant__ NormRows p) {
+  __shared__ RowSums s_sum[2];
+  __shared__ double s_wide[kMaxRowThreads / 32];
   using Piece = Eight8<T, VEC>;
-  const int g = threadIdx.x % G;
+  const RowShape<WARP> at;
+  clear_sums<WARP>(s_sum);
   const uint32_t key = drop_key(p.drop);
   const T* x = static_cast<const T*>(p.x.data);
   const T* residual = static_cast<const T*>(p.residual.data);
-  const int64_t stride = (int64_t)gridDim.x * kRowsAtOnce<G>;
-  int64_t row = (int64_t)blockIdx.x * kRowsAtOnce<G> + threadIdx.x / G;
+  const int64_t stride = at.stride();
+  int64_t row = at.first();
   Piece xs[V], rs[V];
-  auto load = [&](int64_t at) {
+  auto load = [&](int64_t r) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = first_column<V, VEC, G>(g, v);
-      xs[v].load(x + at * p.x.ld + c, p.cols - c);
-      if (residual) rs[v].load(residual + at * p.residual.ld + c, p.cols - c);
+      const int c = at.template column<V, VEC>(v);
+      xs[v].load(x + r * p.x.ld + c, p.cols - c);
+      if (residual) rs[v].load(residual + r * p.residual.ld + c, p.cols - c);
     }
   };
   if (row < p.rows) load(row);
-  float gain[V][8];
-  load_gain<T, V, VEC, G>(p.gain, p.gain_f32, g, p.cols, gain);
+  const RowGain<T, V, VEC, WARP, V <= 2 || (VEC && sizeof(T) == 2)> gain(p.gain, p.gain_f32, at, p.cols);
   int turn = 0;
   for (; row < p.rows; row += stride) {
     float f[V][8], sum = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = first_column<V, VEC, G>(g, v);
+      const int c = at.template column<V, VEC>(v);
       xs[v].widen8(f[v]);
       if (p.drop.threshold) drop_eight<VEC>(f[v], (uint64_t)row * p.cols + c, p.drop, key);
       if (residual) {
@@ -118,12 +117,12 @@ __global__ void __launch_bounds__(kRowThreads<G>) rms_norm(const __grid_constant
     if (kRowAhead<T, V> && row + stride < p.rows) load(row + stride);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = first_column<V, VEC, G>(g, v);
+      const int c = at.template column<V, VEC>(v);
       if (p.h.data) Piece::store(static_cast<T*>(p.h.data) + row * p.h.ld + c, p.cols - c, f[v]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum = fmaf(f[v][j], f[v][j], sum);
     }
-    sum = row_sum<G>(sum, s_sum[turn]);
+    sum = row_sum<WARP>(sum, s_sum[turn]);
     turn ^= 1;
     float rstd;
     if (isfinite(sum)) {
@@ -137,15 +136,17 @@ __global__ void __launch_bounds__(kRowThreads<G>) rms_norm(const __grid_constant
       for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int j = 0; j < 8; ++j) wide += (double)f[v][j] * (double)f[v][j];
-      wide = row_sum_wide<G>(wide, s_wide);
+      wide = row_sum_wide<WARP>(wide, s_wide);
       rstd = (float)(1.0 / sqrt(wide / (double)p.cols + (double)p.eps));
     }
-    if (g == 0 && p.rstd) p.rstd[row] = rstd;
+    if (at.g == 0 && p.rstd) p.rstd[row] = rstd;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = first_column<V, VEC, G>(g, v);
+      const int c = at.template column<V, VEC>(v);
+      float w[8];
+      gain.of(at, v, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[v][j] = f[v][j] * rstd * gain[v][j];
+      for (int j = 0; j < 8; ++j) f[v][j] = f[v][j] * rstd * w[j];
       if (p.y.data) Piece::store(static_cast<T*>(p.y.data) + row * p.y.ld + c, p.cols - c, f[v]);
       if (p.codes) store_codes<VEC>(p, row, c, f[v]);
     }
@@ -155,25 +156,23 @@ __global__ void __launch_bounds__(kRowThreads<G>) rms_norm(const __grid_constant
 
 namespace {
 
-template <typename T, int G, int V, bool VEC>
+template <typename T, int V, bool VEC, bool WARP>
 int launch_one(const NormRows& p, cudaStream_t s) {
   const char* what = "rms_norm launch";
+  constexpr int kRows = RowShape<WARP>::kAtOnce;
+  const int threads = row_threads<V, WARP>(p.cols);
   int grid = 0;
-  if (int st = row_grid<rms_norm<T, G, V, VEC>, kRowThreads<G>>(p, (p.rows + kRowsAtOnce<G> - 1) / kRowsAtOnce<G>, &grid, what))
-    return st;
-  return launch_table<rms_norm<T, G, V, VEC>, 0, kRowThreads<G>>(p, s, what, false, grid);
+  if (int st = row_grid<rms_norm<T, V, VEC, WARP>>(threads, (p.rows + kRows - 1) / kRows, &grid, what)) return st;
+  return launch_row_kernel<rms_norm<T, V, VEC, WARP>>(p, grid, threads, s, what);
 }
-static_assert(DOPT_NORM_MAX_COLS == 512 * 4 * 8, "the longest row's kernel");
+static_assert(DOPT_NORM_MAX_COLS <= kMaxRowThreads * 4 * 8, "the longest row's kernel");
 template <typename T, bool VEC>
 int launch_length(const NormRows& p, cudaStream_t s) {
   const int c = p.cols;
-  if (c <= 256) return launch_one<T, 32, 1, VEC>(p, s);
-  if (c <= 512) return launch_one<T, 32, 2, VEC>(p, s);
-  if (c <= 1024) return launch_one<T, 32, 4, VEC>(p, s);
-  if (c <= 2048) return launch_one<T, 256, 1, VEC>(p, s);
-  if (c <= 4096) return launch_one<T, 256, 2, VEC>(p, s);
-  if (c <= 8192) return launch_one<T, 512, 2, VEC>(p, s);
-  return launch_one<T, 512, 4, VEC>(p, s);
+  if (c <= 256) return launch_one<T, 1, VEC, true>(p, s);
+  if (c <= 512) return launch_one<T, 2, VEC, true>(p, s);
+  if (c > 8192 || (VEC && sizeof(T) == 2 && c > 2048)) return launch_one<T, 4, VEC, false>(p, s);
+  return launch_one<T, 2, VEC, false>(p, s);
 }
 template <typename T>
 int launch_norm(const NormRows& p, bool vec, cudaStream_t s) {
@@ -199,7 +198,7 @@ int check_norm(int64_t rows, int64_t cols, int32_t dtype, int32_t gain_dtype, co
 
 bool rows_vec(const dopt_rows& r, size_t elem) { return !r.data || eight_vectors(r.data, r.ld, elem); }
 
-int parts_of(int64_t rows) { return (int)std::min<int64_t>(rows, kMaxParts); }
+int64_t parts_of(int64_t rows, int64_t cols) { return std::min<int64_t>(rows, max_parts(cols)); }
 
 }  // namespace
 }  // namespace dopt
@@ -247,7 +246,7 @@ int dopt_rms_norm(const dopt_rms_norm_args* a, dopt_stream stream) {
     p.groups = (uint32_t)scale_groups(a->cols);
     p.eps = (float)a->eps;
     p.drop = make_drop(a->drop, threshold);
-    const bool vec = a->cols % 8 == 0 && rows_vec(a->x, elem) && rows_vec(a->residual, elem) && rows_vec(a->h, elem) && rows_vec(a->y, elem);
+    const bool vec = a->cols % 8 == 0 && aligned_to(a->gain, 16) && rows_vec(a->x, elem) && rows_vec(a->residual, elem) && rows_vec(a->h, elem) && rows_vec(a->y, elem);
     p.gain_f32 = a->gain_dtype == DOPT_F32;
     const cudaStream_t s = (cudaStream_t)stream;
     return a->dtype == DOPT_F32    ? launch_norm<float>(p, vec, s)
@@ -262,7 +261,7 @@ size_t dopt_rms_norm_workspace_bytes(int64_t rows, int64_t cols) {
     if (int bad = check_sides(rows, cols, fn)) return bad;
     return cols > DOPT_NORM_MAX_COLS ? fail(DOPT_E_SIZE, fn + "too many columns") : DOPT_OK;
   });
-  return st ? 0 : std::max<size_t>(16, (size_t)parts_of(rows) * (size_t)cols * sizeof(float));
+  return st ? 0 : std::max<size_t>(16, (size_t)parts_of(rows, cols) * (size_t)cols * sizeof(float));
 }
 
 int dopt_rms_norm_backward(const dopt_rms_norm_backward_args* a, void* workspace, size_t workspace_bytes,
@@ -313,7 +312,7 @@ int dopt_rms_norm_backward(const dopt_rms_norm_backward_args* a, void* workspace
     p.rows = a->rows;
     p.cols = (int32_t)a->cols;
     p.drop = make_drop(a->drop, threshold);
-    const bool vec = a->cols % 8 == 0 && rows_vec(a->dy, elem) && rows_vec(a->h, elem) && rows_vec(a->dres, elem) && rows_vec(a->dh, elem) && rows_vec(a->dx, elem);
+    const bool vec = a->cols % 8 == 0 && aligned_to(a->gain, 16) && rows_vec(a->dy, elem) && rows_vec(a->h, elem) && rows_vec(a->dres, elem) && rows_vec(a->dh, elem) && rows_vec(a->dx, elem);
     p.gain_f32 = a->gain_dtype == DOPT_F32;
     int parts = 0;
     if ((st = launch_norm_backward(a->dtype, vec, p, s, &parts))) return st;

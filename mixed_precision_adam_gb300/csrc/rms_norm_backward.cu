@@ -10,33 +10,34 @@ namespace dopt {
 template <typename T, int V>
 constexpr bool kBackAhead = V * sizeof(T) <= 4;
 
-template <typename T, int G, int V, bool VEC>
-__global__ void __launch_bounds__(kRowThreads<G>) rms_norm_backward(const __grid_constant__ NormBackRows p) {
-  __shared__ float s_sum[2][32];
-  __shared__ float s_gain[G == 32 ? 8 * 32 * 8 : 1];
+template <typename T, int V, bool VEC, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : kMaxRowThreads) rms_norm_backward(const __grid_constant__ NormBackRows p) {
+  __shared__ RowSums s_sum[2];
+  __shared__ float s_gain[WARP ? 8 * 32 * 8 : 1];
   using Piece = Eight8<T, VEC>;
-  const int g = threadIdx.x % G;
+  const RowShape<WARP> at;
+  clear_sums<WARP>(s_sum);
   const uint32_t key = drop_key(p.drop);
   const T* h = static_cast<const T*>(p.h.data);
   const T* dy = static_cast<const T*>(p.dy.data);
   const T* dres = static_cast<const T*>(p.dres.data);
-  const int64_t stride = (int64_t)gridDim.x * kRowsAtOnce<G>;
-  int64_t row = (int64_t)blockIdx.x * kRowsAtOnce<G> + threadIdx.x / G;
+  const int64_t stride = at.stride();
+  int64_t row = at.first();
   Piece hs[V], ys[V], rs[V];
   float rstd = 0.f;
-  auto load = [&](int64_t at) {
-    rstd = p.rstd[at];
+  auto load = [&](int64_t r) {
+    rstd = p.rstd[r];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = first_column<V, VEC, G>(g, v);
-      hs[v].load(h + at * p.h.ld + c, p.cols - c);
-      ys[v].load(dy + at * p.dy.ld + c, p.cols - c);
-      if (dres) rs[v].load(dres + at * p.dres.ld + c, p.cols - c);
+      const int c = at.template column<V, VEC>(v);
+      hs[v].load(h + r * p.h.ld + c, p.cols - c);
+      ys[v].load(dy + r * p.dy.ld + c, p.cols - c);
+      if (dres && kBackAhead<T, V>) rs[v].load(dres + r * p.dres.ld + c, p.cols - c);
     }
   };
   if (row < p.rows) load(row);
-  float gain[V][8], acc[V][8];
-  load_gain<T, V, VEC, G>(p.gain, p.gain_f32, g, p.cols, gain);
+  const RowGain<T, V, VEC, WARP, V <= 2> gain(p.gain, p.gain_f32, at, p.cols);
+  float acc[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -50,27 +51,31 @@ __global__ void __launch_bounds__(kRowThreads<G>) rms_norm_backward(const __grid
     for (int v = 0; v < V; ++v) {
       hs[v].widen8(hat[v]);
       ys[v].widen8(d[v]);
-      if (dres) res[v] = rs[v];
+      if (dres && kBackAhead<T, V>) res[v] = rs[v];
     }
     if (kBackAhead<T, V> && row + stride < p.rows) load(row + stride);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+      float w[8];
+      gain.of(at, v, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         hat[v][j] *= r0;
         acc[v][j] = fmaf(d[v][j], hat[v][j], acc[v][j]);
-        d[v][j] *= gain[v][j];
+        d[v][j] *= w[j];
         dot = fmaf(d[v][j], hat[v][j], dot);
       }
-    dot = row_sum<G>(dot, s_sum[turn]) / (float)p.cols;
+    }
+    dot = row_sum<WARP>(dot, s_sum[turn]) / (float)p.cols;
     turn ^= 1;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = first_column<V, VEC, G>(g, v);
+      const int c = at.template column<V, VEC>(v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) d[v][j] = r0 * fmaf(-hat[v][j], dot, d[v][j]);
       if (dres) {
         float r[8];
+        if (!kBackAhead<T, V>) res[v].load(dres + row * p.dres.ld + c, p.cols - c);
         res[v].widen8(r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[v][j] += r[j];
@@ -88,23 +93,23 @@ __global__ void __launch_bounds__(kRowThreads<G>) rms_norm_backward(const __grid
   float* part = p.partial + (int64_t)blockIdx.x * p.cols;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int c = first_column<V, VEC, G>(g, v);
-    if constexpr (G == 32) {
+    const int c = at.template column<V, VEC>(v);
+    if constexpr (WARP) {
       // the warps' sums of these columns, in the warps' order
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s_gain[(threadIdx.x / 32 * 8 + j) * 32 + g] = acc[v][j];
+      for (int j = 0; j < 8; ++j) s_gain[(threadIdx.x / 32 * 8 + j) * 32 + at.g] = acc[v][j];
       __syncthreads();
-      const int j = threadIdx.x / 32, at = c + j * kColumnStep<VEC>;
+      const int j = threadIdx.x / 32, col = c + j * kColumnStep<VEC>;
       float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) sum += s_gain[(w * 8 + j) * 32 + g];
-      if (at < p.cols) part[at] = sum;
+      for (int w = 0; w < 8; ++w) sum += s_gain[(w * 8 + j) * 32 + at.g];
+      if (col < p.cols) part[col] = sum;
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int at = c + j * kColumnStep<VEC>;
-        if (at < p.cols) part[at] = acc[v][j];
+        const int col = c + j * kColumnStep<VEC>;
+        if (col < p.cols) part[col] = acc[v][j];
       }
     }
   }
@@ -145,31 +150,32 @@ __global__ void __launch_bounds__(kGainThreads) rms_norm_gain(const __grid_const
 
 namespace {
 
-// Each CTA should have rows enough that its partial sums are a small part of
-// what it reads.
-constexpr int kRowsPerPart = 8;
+// CTAs that a call asks for: each should have rows enough that its partial
+// sums are a small part of what it reads and that adding them takes little
+// time, unless that leaves SMs without work.
+int64_t parts_asked(const NormBackRows& p, int rows_at_once) {
+  const int64_t all = (p.rows + rows_at_once - 1) / rows_at_once;
+  if (!p.partial) return std::min<int64_t>(all, max_parts(p.cols));
+  const int64_t few = std::min<int64_t>({all, (p.rows + 7) / 8, 304});
+  return std::min<int64_t>({all, std::max<int64_t>(few, p.rows / 32), max_parts(p.cols)});
+}
 
-template <typename T, int G, int V, bool VEC>
+template <typename T, int V, bool VEC, bool WARP>
 int launch_one(const NormBackRows& p, cudaStream_t s, int* parts) {
   const char* what = "rms_norm_backward launch";
-  const int64_t rows = kRowsAtOnce<G> > kRowsPerPart || !p.partial ? kRowsAtOnce<G> : kRowsPerPart;
-  int grid = 0;
-  if (int st = row_grid<rms_norm_backward<T, G, V, VEC>, kRowThreads<G>>(
-          p, std::min<int64_t>(kMaxParts, (p.rows + rows - 1) / rows), &grid, what))
-    return st;
-  *parts = grid;
-  return launch_table<rms_norm_backward<T, G, V, VEC>, 0, kRowThreads<G>>(p, s, what, false, grid);
+  constexpr int kRows = RowShape<WARP>::kAtOnce;
+  const int threads = row_threads<V, WARP>(p.cols);
+  if (int st = row_grid<rms_norm_backward<T, V, VEC, WARP>>(threads, parts_asked(p, kRows), parts, what)) return st;
+  return launch_row_kernel<rms_norm_backward<T, V, VEC, WARP>>(p, *parts, threads, s, what);
 }
 template <typename T, bool VEC>
 int launch_length(const NormBackRows& p, cudaStream_t s, int* parts) {
   const int c = p.cols;
-  if (c <= 256) return launch_one<T, 32, 1, VEC>(p, s, parts);
-  if (c <= 512) return launch_one<T, 32, 2, VEC>(p, s, parts);
-  if (c <= 1024) return launch_one<T, 128, 1, VEC>(p, s, parts);
-  if (c <= 2048) return launch_one<T, 256, 1, VEC>(p, s, parts);
-  if (c <= 4096) return launch_one<T, 256, 2, VEC>(p, s, parts);
-  if (c <= 8192) return launch_one<T, 512, 2, VEC>(p, s, parts);
-  return launch_one<T, 512, 4, VEC>(p, s, parts);
+  if (c <= 256) return launch_one<T, 1, VEC, true>(p, s, parts);
+  if (c <= 512) return launch_one<T, 2, VEC, true>(p, s, parts);
+  if (c <= (sizeof(T) == 2 ? 2048 : 4096)) return launch_one<T, 1, VEC, false>(p, s, parts);
+  if (c <= 8192) return launch_one<T, 2, VEC, false>(p, s, parts);
+  return launch_one<T, 4, VEC, false>(p, s, parts);
 }
 
 }  // namespace
