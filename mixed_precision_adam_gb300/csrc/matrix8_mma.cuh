@@ -189,9 +189,19 @@ __device__ __forceinline__ MulTile mul_tile(const MulParams& p, int t) {
 }
 
 // One column n of d for N consecutive m, `count` of them there: rounded once,
-// with what d holds added before.
+// with what d holds added before.  fp32 sums are added where d is kept (every
+// element once, so in a fixed order): a load would be waited for, and with it
+// the next tile's sums (11008 x 4096 x 16384 added to fp32: 444 us so).
 template <typename T, int N>
 __device__ __forceinline__ void store_sums(const uint32_t (&r)[N], T* d, int64_t ldd, int count, bool accumulate) {
+  if constexpr (sizeof(T) == 4) {
+    if (accumulate) {
+#pragma unroll
+      for (int c = 0; c < N; ++c)
+        if (c < count) atomicAdd(d + c * ldd, __uint_as_float(r[c]));
+      return;
+    }
+  }
   constexpr int kAhead = 8;  // loads under way
 #pragma unroll
   for (int c = 0; c < N; c += kAhead) {
@@ -209,18 +219,18 @@ __device__ __forceinline__ void store_sums(const uint32_t (&r)[N], T* d, int64_t
   }
 }
 
-// A warp's share of the sums, N columns from TMEM column `at` on, into r:
-// stored at the first part of k, added at the later ones.
-template <int N>
-__device__ __forceinline__ void take_sums(uint32_t at, bool first, uint32_t (&r)[N]) {
+// Columns C0 to C1 of a warp's share of the sums, from TMEM column `at` on,
+// into r: stored at the first part of k, added at the later ones.
+template <int C0, int C1, int N>
+__device__ __forceinline__ void take_range(uint32_t at, bool first, uint32_t (&r)[N]) {
   constexpr int kChunk = N < 16 ? N : 16;
   if (first) {
 #pragma unroll
-    for (int c = 0; c < N; c += kChunk) tmem_load<kChunk>(at + c, r + c);
+    for (int c = C0; c < C1; c += kChunk) tmem_load<kChunk>(at + c, r + c);
     tmem_wait_load();
   } else {
 #pragma unroll
-    for (int c = 0; c < N; c += kChunk) {
+    for (int c = C0; c < C1; c += kChunk) {
       uint32_t t[kChunk];
       tmem_load<kChunk>(at + c, t);
       tmem_wait_load();
@@ -229,6 +239,10 @@ __device__ __forceinline__ void take_sums(uint32_t at, bool first, uint32_t (&r)
         r[c + j] = __float_as_uint(__uint_as_float(r[c + j]) + __uint_as_float(t[j]));
     }
   }
+}
+template <int N>
+__device__ __forceinline__ void take_sums(uint32_t at, bool first, uint32_t (&r)[N]) {
+  take_range<0, N>(at, first, r);
 }
 // The column n of d that a thread has sums of, from row m0 on.
 template <int N>

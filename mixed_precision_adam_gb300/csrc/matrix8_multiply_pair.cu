@@ -18,15 +18,20 @@ struct PairShape {
   static constexpr int kBarAt = kScaleAt + kStages * kScaleTiles * 512;
   static constexpr int kBytes = kBarAt + (2 * kStages + 2) * 8 + 16;
   static constexpr size_t kSmem = kBytes + 1024;
-  static constexpr int kTmem = 512;
-  static constexpr int kScaleCol = kTile, kScaleCols = 4 * kScaleTiles;  // two sets, used in turn
+  // Two sets of sums, used in turn, share 32 columns: the next products may
+  // start when those have been read, and the rest is read under them.
+  static constexpr int kTmem = 512, kShared = 32, kSecond = kTile - kShared;
+  static constexpr int kScaleCol = kSecond + kTile, kScaleCols = 4 * kScaleTiles;  // two sets, used in turn
+  static_assert(kScaleCol + 2 * kScaleCols <= kTmem, "TMEM columns");
 };
 
-// A barrier of the cluster's first CTA, from either; and the wait for one
-// that the other CTA's threads arrive on.
+// An arrival on a barrier of the cluster's first CTA, from either.  It says
+// that TMEM has been read, which the fence before it orders; releasing memory
+// too would wait for the thread's stores of the last tile (1600 cycles).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The wait for a barrier that the other CTA's threads arrive on.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, unsigned parity) {
   uint32_t ok;
   asm volatile(
@@ -124,6 +129,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMulThreads)
           }
           tmem_fence_after();
           const int end = min(p.blocks, part + p.part);
+          const uint32_t acc = tmem + (done & 1 ? S::kSecond : 0);
           for (int k = part; k < end; ++k) {
             if (!(ok = mbar_wait_cluster(full + stage, phase))) break;
             tmem_fence_after();
@@ -140,7 +146,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMulThreads)
             const uint64_t bd = operand_desc(b), ad = operand_desc(b + S::kOperand);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              mma_scaled<2>(tmem, bd + 2 * j, ad + 2 * j, instr, sb, sa, (k > part || j > 0) ? 1u : 0u);
+              mma_scaled<2>(acc, bd + 2 * j, ad + 2 * j, instr, sb, sa, (k > part || j > 0) ? 1u : 0u);
             mma_commit<2>(empty + stage);
             if (++stage == S::kStages) stage = 0, phase ^= 1;
           }
@@ -166,10 +172,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMulThreads)
         ok = ok && mbar_wait_bounded(sums, done & 1) && !*failed;
         ok = __all_sync(0xFFFFFFFFu, ok);
         tmem_fence_after();
-        take_sums(tmem + ((uint32_t)quarter << 21) + half * kColumns, part == 0, r);
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(taken_by);
+        const uint32_t from = tmem + ((uint32_t)quarter << 21) + (done & 1 ? S::kSecond : 0) + half * kColumns;
+        auto release = [&] {
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(taken_by);
+        };
+        // the columns that the other set shares first: the last of the first
+        // set, the first of the second
+        if (done & 1) {
+          if (half == 0) take_range<0, S::kShared>(from, part == 0, r);
+          release();
+          if (half == 1) take_range<0, S::kShared>(from, part == 0, r);
+          take_range<S::kShared, kColumns>(from, part == 0, r);
+        } else {
+          if (half == 1) take_range<kColumns - S::kShared, kColumns>(from, part == 0, r);
+          release();
+          if (half == 0) take_range<kColumns - S::kShared, kColumns>(from, part == 0, r);
+          take_range<0, kColumns - S::kShared>(from, part == 0, r);
+        }
       }
       if (!ok) {
 #pragma unroll
