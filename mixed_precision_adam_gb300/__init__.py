@@ -978,11 +978,23 @@ def dopt_matrix8_multiply(a, b, d, accumulate=False, stream=None):
     """d = a b^T, or d += a b^T: two Matrix8 of the same cols, and a 2-d
     float32, bfloat16 or float16 tensor of a.rows x b.rows whose rows are
     contiguous."""
-    devices = set()
-    ptr, ld, dt = _matrix(d, "d", _DTYPE, devices, (a.rows, b.rows))
-    _gpu_of(_OnGpu(devices | a.devices | b.devices))
-    _check(_c["dopt_matrix8_multiply"](a.address, b.address, ptr, _DTYPE[dt], ld, 1 if accumulate else 0,
-                                       _stream(stream)))
+    try:  # the usual call, with few questions
+        (rows, cols), (ld, one), dt = d.shape, d.stride(), _dtype_codes[d.dtype]
+        fits = rows == a.rows and cols == b.rows and one == 1 and ld >= cols and \
+            d.get_device() == a.gpu == b.gpu == _current_device()
+    except (AttributeError, KeyError, ValueError):
+        fits = False
+    if fits:
+        ptr = d.data_ptr()
+    else:
+        devices = set()
+        ptr, ld, name = _matrix(d, "d", _DTYPE, devices, (a.rows, b.rows))
+        dt = _dtype_codes[d.dtype] = _DTYPE[name]
+        _gpu_of(_OnGpu(devices | a.devices | b.devices))
+    _check(_c["dopt_matrix8_multiply"](a.address, b.address, ptr, dt, ld, 1 if accumulate else 0, _stream(stream)))
+
+
+_dtype_codes = {}  # torch dtype -> dopt_dtype, once seen
 
 
 class _OnGpu:

@@ -107,24 +107,24 @@ struct Four<float> {
   static __device__ __forceinline__ uint32_t fp32_bits(uint32_t top) { return top; }
 };
 
-// Warp w has rows 16 w to 16 w + 15 of a tile, lane l its columns 4 l to
-// 4 l + 3: 64 values per thread, all of them loaded before the first is used.
-constexpr int kRowsPerWarp = 16;
-static_assert(kThreads / 32 * kRowsPerWarp == kBlock8, "a CTA has a tile's rows");
+// Warp w has rows 8 w to 8 w + 7 of a tile, lane l its columns 4 l to 4 l + 3:
+// 32 values per thread, all of them loaded before the first is used.
+constexpr int kRowsPerWarp = 8;
+constexpr int kMatrixThreads = kBlock8 / kRowsPerWarp * 32, kMatrixWarps = kMatrixThreads / 32;
 template <typename T>
 constexpr int kMatrixCtas = sizeof(T) == 2 ? 3 : 2;  // per SM: what the values' registers allow
 
 // A CTA per tile: the next ones' loads then run under this one's stores.
 template <typename T, int CAP>
-__global__ void __launch_bounds__(kThreads, kMatrixCtas<T>) matrix8_pack(const __grid_constant__ MatrixParamsT<CAP> p) {
-  __shared__ uint32_t s_top[kThreads / 32][kBlock8];  // largest of each column, by warp
-  __shared__ uint32_t s_tile[kThreads / 32];          // and of all of the warp's values
-  // values on their way to their lanes, eight rows of a warp at a time; then
-  // the transposed codes, 16 of a column at a time
-  constexpr int kStageRows = 8;
-  __shared__ union {
-    T stage[kThreads / 32][kStageRows][kBlock8];
-    uint4 turn[kBlock8 * kBlock8 / 16];
+__global__ void __launch_bounds__(kMatrixThreads, kMatrixCtas<T>) matrix8_pack(const __grid_constant__ MatrixParamsT<CAP> p) {
+  __shared__ uint32_t s_top[kMatrixWarps][kBlock8];  // largest of each column, by warp
+  __shared__ uint32_t s_tile[kMatrixWarps];          // and of all of the warp's values
+  // values on their way to their lanes, a few rows of a warp at a time; then
+  // the transposed codes, eight of a column at a time
+  constexpr int kStageRows = sizeof(T) == 2 ? 8 : 4;
+  __shared__ union alignas(16) {
+    T stage[kMatrixWarps][kStageRows][kBlock8];
+    uint2 turn[kBlock8 * kBlock8 / 8];
   } s;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const MatrixSeg& sg = p.seg[find_seg(p, blockIdx.x)];
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, kMatrixCtas<T>) matrix8_pack(const _
   uint32_t scale = 0u;
   if (sg.square) {
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) scale = max(scale, s_tile[w]);
+    for (int w = 0; w < kMatrixWarps; ++w) scale = max(scale, s_tile[w]);
     scale = m_scale_of(Four<T>::fp32_bits(scale));
   }
   const float factor = code_factor(scale);
@@ -212,29 +212,29 @@ __global__ void __launch_bounds__(kThreads, kMatrixCtas<T>) matrix8_pack(const _
     if (!sg.square) {
       uint32_t top = 0u;
 #pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) top = max(top, s_top[w][lane * 4 + j]);
+      for (int w = 0; w < kMatrixWarps; ++w) top = max(top, s_top[w][lane * 4 + j]);
       sc = m_scale_of(Four<T>::fp32_bits(top));
       up = code_factor(sc);
     }
-    uint32_t w[4];
+    uint32_t w[2];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 2; ++q) {
       const float v[4] = {f[4 * q].at(j), f[4 * q + 1].at(j), f[4 * q + 2].at(j), f[4 * q + 3].at(j)};
       w[q] = four_codes(v, up, sc == 255u);
     }
-    // column 4 l + j holds eight pieces of 16 codes; turned by l so that
-    // neither the lanes' writes here nor the reads below share banks
-    s.turn[(lane * 4 + j) * 8 + ((warp + lane) & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
+    // column 4 l + j holds sixteen pieces of 8 codes; turned by 2 l, so that
+    // the lanes' writes here spread over the banks and pairs stay together
+    s.turn[(lane * 4 + j) * 16 + ((warp + 2 * lane) & 15)] = make_uint2(w[0], w[1]);
     if (warp == 0 && lane * 4 + j < a.cols && a.rows > 0)
       sg.scales_t[scale_place((int64_t)a.c0 + lane * 4 + j, a.r0 / kBlock8, (uint32_t)scale_groups(sg.rows))] = (uint8_t)sc;
   }
   __syncthreads();
   // eight lanes write the 128 codes of a column
 #pragma unroll
-  for (int k = 0; k < kBlock8 * 8 / kThreads; ++k) {
-    const int c = k * (kThreads / 8) + threadIdx.x / 8, piece = threadIdx.x % 8;
+  for (int k = 0; k < kBlock8 * 8 / kMatrixThreads; ++k) {
+    const int c = k * (kMatrixThreads / 8) + threadIdx.x / 8, piece = threadIdx.x % 8;
     if (c >= a.cols) continue;
-    const uint4 v = s.turn[c * 8 + ((piece + (c >> 2)) & 7)];
+    const uint4 v = *reinterpret_cast<const uint4*>(&s.turn[c * 16 + ((2 * piece + 2 * (c >> 2)) & 15)]);
     uint8_t* dst = sg.codes_t + ((int64_t)a.c0 + c) * sg.ld_t + a.r0 + piece * 16;
     const int m = a.rows - piece * 16;
     if (m >= 16) {
@@ -248,33 +248,36 @@ __global__ void __launch_bounds__(kThreads, kMatrixCtas<T>) matrix8_pack(const _
   }
 }
 
-// A warp has 16 rows of a tile.  Where the values can be written in vectors
-// and the tile is whole, a lane has 16 codes of every fourth row; else
-// consecutive lanes have consecutive elements.
+// Rows of a tile 8 w to 8 w + 7 are warp w's.  Where the values can be written
+// in vectors a lane has 16 codes of every fourth row; else four of each row,
+// which go to the lanes that make consecutive elements of them.
 template <typename T, int CAP>
-__global__ void __launch_bounds__(kThreads, 4) matrix8_unpack(const __grid_constant__ MatrixParamsT<CAP> p) {
+__global__ void __launch_bounds__(kMatrixThreads, 2) matrix8_unpack(const __grid_constant__ MatrixParamsT<CAP> p) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const MatrixSeg& sg = p.seg[find_seg(p, blockIdx.x)];
   const MatrixTile a = place_matrix_tile(p, sg, blockIdx.x);
   const int rows = min(kRowsPerWarp, a.rows - warp * kRowsPerWarp);
+  if (rows <= 0) return;
   const int64_t r0 = (int64_t)a.r0 + warp * kRowsPerWarp;
   const uint32_t groups = (uint32_t)scale_groups(sg.cols), block = a.c0 / kBlock8;
   const uint8_t* codes = sg.codes + r0 * sg.ld_out + a.c0;
   T* values = static_cast<T*>(sg.values) + r0 * sg.ld + a.c0;
-  if (sg.vec && a.cols == kBlock8 && rows == kRowsPerWarp) {
+  // lane k: row k's scale
+  const uint32_t scale = lane < rows ? sg.scales[scale_place(r0 + lane, block, groups)] : 0u;
+  if (sg.vec && a.cols == kBlock8) {
     const int c = lane % 8 * 16;
-    uint4 code[4];
-    uint32_t s[4];
+    uint4 code[kRowsPerWarp / 4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kRowsPerWarp / 4; ++k) {
       const int r = lane / 8 + 4 * k;
-      code[k] = __ldcs(reinterpret_cast<const uint4*>(codes + r * sg.ld_out + c));
-      s[k] = sg.scales[scale_place(r0 + r, block, groups)];
+      if (r < rows) code[k] = __ldcs(reinterpret_cast<const uint4*>(codes + r * sg.ld_out + c));
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float unit = m_unit(s[k]);
-      T* dst = values + (lane / 8 + 4 * k) * sg.ld + c;
+    for (int k = 0; k < kRowsPerWarp / 4; ++k) {
+      const int r = lane / 8 + 4 * k;
+      const float unit = m_unit(__shfl_sync(0xFFFFFFFFu, scale, r));
+      if (r >= rows) continue;
+      T* dst = values + r * sg.ld + c;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         float f[8];
@@ -286,17 +289,32 @@ __global__ void __launch_bounds__(kThreads, 4) matrix8_unpack(const __grid_const
     }
     return;
   }
-#pragma unroll 4
-  for (int r = 0; r < rows; ++r) {
-    const float unit = m_unit(sg.scales[scale_place(r0 + r, block, groups)]);
-    uint32_t c[4];
+  const int n = a.cols - lane * 4;
+  uint32_t code[kRowsPerWarp];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] = lane + 32 * j < a.cols ? __ldcs(codes + r * sg.ld_out + lane + 32 * j) : 0u;
-    float f[8];
-    widen_codes(make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, 0u), f);
+  for (int k = 0; k < kRowsPerWarp; ++k) {
+    code[k] = 0u;
+    if (k >= rows) continue;
+    const uint8_t* src = codes + k * sg.ld_out + lane * 4;
+    if (n >= 4)
+      code[k] = __ldcs(reinterpret_cast<const uint32_t*>(src));
+    else
+      for (int j = 0; j < n; ++j) code[k] |= (uint32_t)src[j] << (8 * j);
+  }
+#pragma unroll
+  for (int k = 0; k < kRowsPerWarp; ++k) {
+    if (k >= rows) break;
+    const float unit = m_unit(__shfl_sync(0xFFFFFFFFu, scale, k));
+    // the codes of columns l, l + 32, l + 64 and l + 96, from lanes l / 4, ...
+    uint32_t mine = 0u;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (lane + 32 * j < a.cols) __stcs(values + r * sg.ld + lane + 32 * j, narrow<T>(__fmul_rn(f[j], unit)));
+      mine |= (__shfl_sync(0xFFFFFFFFu, code[k], lane / 4 + 8 * j) >> (8 * (lane & 3)) & 0xFFu) << (8 * j);
+    float f[8];
+    widen_codes(make_uint2(mine, 0u), f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (lane + 32 * j < a.cols) __stcs(values + k * sg.ld + lane + 32 * j, narrow<T>(__fmul_rn(f[j], unit)));
   }
 }
 
@@ -305,8 +323,9 @@ namespace {
 template <auto Small, auto Big>
 int launch_matrices(const MatrixParamsT<kMatrixCap>& p, cudaStream_t s, const char* what) {
   if (p.n_seg <= kMatrixSmallCap)
-    return launch_table<Small>(compact_table<MatrixParamsT<kMatrixSmallCap>, MatrixHead>(p), s, what, false, p.n_tiles);
-  return launch_table<Big>(p, s, what, false, p.n_tiles);
+    return launch_table<Small, 0, kMatrixThreads>(compact_table<MatrixParamsT<kMatrixSmallCap>, MatrixHead>(p), s, what, false,
+                                                  p.n_tiles);
+  return launch_table<Big, 0, kMatrixThreads>(p, s, what, false, p.n_tiles);
 }
 template <typename T>
 int launch_pack(const MatrixParamsT<kMatrixCap>& p, cudaStream_t s) {

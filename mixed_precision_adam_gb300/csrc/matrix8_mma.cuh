@@ -49,6 +49,9 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 // The address in the cluster of what CTA `rank` has at a shared address.
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t at, uint32_t rank) {
   uint32_t out;
@@ -168,7 +171,7 @@ struct MulParams {
   int32_t m, n;            // rows of a, of b
   int32_t blocks, groups;  // of k: 128 columns, 512 columns
   int32_t tiles_n, tiles_m, n_tiles;
-  int32_t split;  // CTAs of a cluster that share a tile's k
+  int32_t split_log, share_log;  // log2 of the CTAs of a cluster that share a tile's k, and of the rows of a that each then stores
   int32_t part;   // blocks that the matrix unit adds up before its sums are added in registers
   int32_t dtype, accumulate;
 };
@@ -202,7 +205,7 @@ __device__ __forceinline__ void store_sums(const uint32_t (&r)[N], T* d, int64_t
       return;
     }
   }
-  constexpr int kAhead = 8;  // loads under way
+  constexpr int kAhead = N < 8 ? N : 8;  // loads under way
 #pragma unroll
   for (int c = 0; c < N; c += kAhead) {
     float old[kAhead];

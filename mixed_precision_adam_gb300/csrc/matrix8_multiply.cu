@@ -17,12 +17,12 @@ template <int BT>
 struct MulShape {
   static constexpr int kScaleTiles = 1 + (BT + 127) / 128;  // of 512 bytes, per stage
   static constexpr int kB = kTileN * kOperandRow, kA = BT * kOperandRow;
-  static constexpr int kStages = BT <= 64 ? 4 : BT == 128 ? 6 : 4;
+  static constexpr int kStages = BT <= 32 ? 5 : BT == 64 ? 4 : 6;
   static constexpr int kScaleAt = kStages * (kA + kB);
   static constexpr int kBarAt = kScaleAt + kStages * kScaleTiles * 512;
   static constexpr int kBytes = kBarAt + (2 * kStages + 2) * 8 + 16;
   static constexpr size_t kSmem = kBytes + 1024;  // the ring starts on 1024 bytes
-  static constexpr int kTmem = BT <= 64 ? 128 : BT == 128 ? 256 : 512;  // columns
+  static constexpr int kTmem = BT <= 64 ? 128 : 256;  // columns
   static constexpr int kScaleCol = BT;  // first column of the scales: two sets, used in turn
   static constexpr int kScaleCols = 4 * kScaleTiles;
   static_assert(kScaleCol + 2 * kScaleCols <= kTmem, "TMEM columns");
@@ -30,7 +30,7 @@ struct MulShape {
 };
 
 template <int BT, bool SPLIT>
-__global__ void __launch_bounds__(kMulThreads) matrix8_multiply(const __grid_constant__ MulParams p) {
+__global__ void __launch_bounds__(kMulThreads, BT <= 64 ? 2 : 1) matrix8_multiply(const __grid_constant__ MulParams p) {
   using S = MulShape<BT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -53,6 +53,12 @@ __global__ void __launch_bounds__(kMulThreads) matrix8_multiply(const __grid_con
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 2) tmem_alloc<1>(tmem_at, S::kTmem);
+  if (threadIdx.x == 96) {
+    prefetch_map(&p.b_map);
+    prefetch_map(&p.a_map);
+    prefetch_map(&p.b_scales);
+    prefetch_map(&p.a_scales);
+  }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
@@ -62,11 +68,11 @@ __global__ void __launch_bounds__(kMulThreads) matrix8_multiply(const __grid_con
   int first = blockIdx.x, stride = gridDim.x, rank = 0;
   int k0 = 0, k1 = p.blocks;
   if constexpr (SPLIT) {
-    rank = (int)(blockIdx.x % (unsigned)p.split);
-    first = blockIdx.x / p.split;
+    rank = (int)(blockIdx.x & ((1u << p.split_log) - 1u));
+    first = (int)(blockIdx.x >> p.split_log);
     stride = p.n_tiles;  // one tile
-    k0 = (int)((int64_t)p.groups * rank / p.split) * 4;
-    k1 = min(p.blocks, (int)((int64_t)p.groups * (rank + 1) / p.split) * 4);
+    k0 = p.groups * rank >> p.split_log << 2;  // groups < 2^22
+    k1 = min(p.blocks, p.groups * (rank + 1) >> p.split_log << 2);
   }
 
   if (warp == 0) {
@@ -165,28 +171,34 @@ __global__ void __launch_bounds__(kMulThreads) matrix8_multiply(const __grid_con
         // one sends it its own part, through shared memory that no copy and
         // no product uses any more
         cluster_sync();
-        const int share = BT / p.split;
+        const int share = 1 << p.share_log;
         const uint32_t mine = smem_addr(smem) + (uint32_t)(quarter * 32 + lane) * 4u;
 #pragma unroll
         for (int c = 0; c < kColumns; ++c) {
-          const int col = half * kColumns + c, to = col / share, at = rank * share + col - to * share;
+          const int col = half * kColumns + c, to = col >> p.share_log, at = rank * share + (col & (share - 1));
           const uint32_t remote = cluster_addr(mine + (uint32_t)at * 512u, to);
           asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(r[c]) : "memory");
         }
         cluster_sync();
+        // every other column of the share is this thread's, four at a time
         const float* part = reinterpret_cast<const float*>(smem) + (threadIdx.x - 128) % 128;
-        const int64_t n = (int64_t)tile.n * kTileN + (threadIdx.x - 128) % 128;
-        for (int c = (threadIdx.x - 128) / 128; c < share; c += 2) {
-          const int64_t m = (int64_t)tile.m * BT + rank * share + c;
-          float x = part[c * 128];
-          for (int q = 1; q < p.split; ++q) x += part[(q * share + c) * 128];
-          if (m >= p.m || n >= p.n) continue;
-          const int64_t at = m * p.ldd + n;
-          if (p.accumulate) x += load_element(p.d, at, p.dtype);
-          if (p.dtype == DOPT_F32)
-            static_cast<float*>(p.d)[at] = x;
-          else
-            store_param(p.d, at, p.dtype, x);
+        const int64_t n = (int64_t)tile.n * kTileN + (threadIdx.x - 128) % 128, m0 = (int64_t)tile.m * BT + rank * share;
+        for (int c0 = (threadIdx.x - 128) / 128; c0 < share; c0 += 8) {
+          float x[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = c0 + 2 * j < share ? part[(c0 + 2 * j) * 128] : 0.f;
+#pragma unroll
+          for (int q = 1; q < 8; ++q) {
+            if (q >> p.split_log) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (c0 + 2 * j < share) x[j] += part[(q * share + c0 + 2 * j) * 128];
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t one[1] = {__float_as_uint(x[j])};
+            if (c0 + 2 * j < share && m0 + c0 + 2 * j < p.m) store_column(p, one, n, m0 + c0 + 2 * j);
+          }
         }
       } else {
         store_column(p, r, (int64_t)tile.n * kTileN + quarter * 32 + lane, (int64_t)tile.m * BT + half * kColumns);
@@ -271,10 +283,10 @@ int launch_multiply(MulParams& p, const dopt_matrix8& a, const dopt_matrix8& b, 
   if ((st = device_sms(&sms))) return st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = SPLIT ? p.split : 1;
+  attr[0].val.clusterDim.x = SPLIT ? 1u << p.split_log : 1u;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(SPLIT ? p.n_tiles * p.split : std::min(p.n_tiles, sms * (BT <= 64 ? 2 : 1))));
+  cfg.gridDim = dim3((unsigned)(SPLIT ? p.n_tiles << p.split_log : std::min(p.n_tiles, sms * (BT <= 64 ? 2 : 1))));
   cfg.blockDim = dim3(kMulThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = s;
@@ -295,14 +307,13 @@ int multiply_rows(MulParams& p, const dopt_matrix8& a, const dopt_matrix8& b, cu
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   if (tiles > INT32_MAX / 8) return fail(DOPT_E_SIZE, "dopt_matrix8_multiply: too many elements in d");
   p.n_tiles = (int32_t)tiles;
-  p.split = 1;
-  if constexpr (BT <= 128) {
-    int sms = 0;
-    if (int st = device_sms(&sms)) return st;
-    const int slots = sms * (BT <= 64 ? 2 : 1);
-    while (p.split < 8 && p.split * 2 <= p.groups && tiles * p.split * 2 <= slots) p.split *= 2;
-    if (p.split > 1) return launch_multiply<BT, true>(p, a, b, s);
-  }
+  p.split_log = p.share_log = 0;
+  int sms = 0;
+  if (int st = device_sms(&sms)) return st;
+  const int slots = sms * (BT <= 64 ? 2 : 1);
+  while (p.split_log < 3 && (2 << p.split_log) <= p.groups && (tiles << p.split_log) * 2 <= slots) ++p.split_log;
+  while ((1 << p.split_log << p.share_log) < BT) ++p.share_log;
+  if (p.split_log) return launch_multiply<BT, true>(p, a, b, s);
   return launch_multiply<BT, false>(p, a, b, s);
 }
 

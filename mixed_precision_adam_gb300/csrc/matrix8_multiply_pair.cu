@@ -77,6 +77,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMulThreads)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 2) tmem_alloc<2>(tmem_at, S::kTmem);
+  if (threadIdx.x == 96) {
+    prefetch_map(&p.b_map);
+    prefetch_map(&p.a_map);
+    prefetch_map(&p.b_scales);
+    prefetch_map(&p.a_scales);
+  }
   tmem_fence_before();
   __syncthreads();
   cluster_sync();
@@ -223,7 +229,6 @@ int launch_multiply_pair(MulParams& p, const dopt_matrix8& a, const dopt_matrix8
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   if (tiles > INT32_MAX / 8) return fail(DOPT_E_SIZE, "dopt_matrix8_multiply: too many elements in d");
   p.n_tiles = (int32_t)tiles;
-  p.split = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min(p.n_tiles, sms / 2) * 2);
   cfg.blockDim = dim3(kMulThreads);

@@ -156,7 +156,7 @@ namespace {
 int64_t parts_asked(const NormBackRows& p, int rows_at_once) {
   const int64_t all = (p.rows + rows_at_once - 1) / rows_at_once;
   if (!p.partial) return std::min<int64_t>(all, max_parts(p.cols));
-  const int64_t few = std::min<int64_t>({all, (p.rows + 7) / 8, 304});
+  const int64_t few = std::min<int64_t>({all, (p.rows + 7) / 8, 608});
   return std::min<int64_t>({all, std::max<int64_t>(few, p.rows / 32), max_parts(p.cols)});
 }
 
