@@ -117,7 +117,8 @@ constexpr int kMatrixCtas = sizeof(T) == 2 ? 3 : 2;  // per SM: what the values'
 // A CTA per tile: the next ones' loads then run under this one's stores.
 template <typename T, int CAP>
 __global__ void __launch_bounds__(kMatrixThreads, kMatrixCtas<T>) matrix8_pack(const __grid_constant__ MatrixParamsT<CAP> p) {
-  __shared__ uint32_t s_top[kMatrixWarps][kBlock8];  // largest of each column, by warp
+  __shared__ alignas(16) uint32_t s_top[kMatrixWarps][kBlock8];  // largest of each column, by warp
+  __shared__ alignas(16) uint32_t s_scale[kBlock8];    // scale byte of each column
   __shared__ uint32_t s_tile[kMatrixWarps];          // and of all of the warp's values
   // values on their way to their lanes, a few rows of a warp at a time; then
   // the transposed codes, eight of a column at a time
@@ -173,6 +174,12 @@ __global__ void __launch_bounds__(kMatrixThreads, kMatrixCtas<T>) matrix8_pack(c
 #pragma unroll
     for (int w = 0; w < kMatrixWarps; ++w) scale = max(scale, s_tile[w]);
     scale = m_scale_of(Four<T>::fp32_bits(scale));
+  } else if (sg.codes_t && threadIdx.x < kBlock8) {
+    // a thread per column, which the lanes that have it read together below
+    uint32_t top = 0u;
+#pragma unroll
+    for (int w = 0; w < kMatrixWarps; ++w) top = max(top, s_top[w][threadIdx.x]);
+    s_scale[threadIdx.x] = m_scale_of(Four<T>::fp32_bits(top));
   }
   const float factor = code_factor(scale);
   if (sg.codes) {
@@ -205,17 +212,15 @@ __global__ void __launch_bounds__(kMatrixThreads, kMatrixCtas<T>) matrix8_pack(c
           (uint8_t)mine;
   }
   if (!sg.codes_t) return;
+  uint4 scales_t = make_uint4(scale, scale, scale, scale);
+  if (!sg.square) {
+    __syncthreads();
+    scales_t = *reinterpret_cast<const uint4*>(&s_scale[lane * 4]);
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    uint32_t sc = scale;
-    float up = factor;
-    if (!sg.square) {
-      uint32_t top = 0u;
-#pragma unroll
-      for (int w = 0; w < kMatrixWarps; ++w) top = max(top, s_top[w][lane * 4 + j]);
-      sc = m_scale_of(Four<T>::fp32_bits(top));
-      up = code_factor(sc);
-    }
+    const uint32_t sc = j == 0 ? scales_t.x : j == 1 ? scales_t.y : j == 2 ? scales_t.z : scales_t.w;
+    const float up = code_factor(sc);
     uint32_t w[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
