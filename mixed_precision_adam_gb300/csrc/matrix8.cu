@@ -62,10 +62,8 @@ struct Four {  // 16-bit types
   // from shared memory
   __device__ __forceinline__ void take(const T* p) { r = *reinterpret_cast<const uint2*>(p); }
   __device__ __forceinline__ void zero() { r = make_uint2(0u, 0u); }
-  __device__ __forceinline__ void widen4(float (&f)[4]) const {
-    const float2 x = widen_pair<T>(r.x), y = widen_pair<T>(r.y);
-    f[0] = x.x, f[1] = x.y, f[2] = y.x, f[3] = y.y;
-  }
+  __device__ __forceinline__ float2 low() const { return widen_pair<T>(r.x); }
+  __device__ __forceinline__ float2 high() const { return widen_pair<T>(r.y); }
   // Element j alone.
   __device__ __forceinline__ float at(int j) const {
     const float2 x = widen_pair<T>(j < 2 ? r.x : r.y);
@@ -91,7 +89,8 @@ struct Four<float> {
   __device__ __forceinline__ void load(const float* p) { r = __ldcs(reinterpret_cast<const float4*>(p)); }
   __device__ __forceinline__ void take(const float* p) { r = *reinterpret_cast<const float4*>(p); }
   __device__ __forceinline__ void zero() { r = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void widen4(float (&f)[4]) const { f[0] = r.x, f[1] = r.y, f[2] = r.z, f[3] = r.w; }
+  __device__ __forceinline__ float2 low() const { return make_float2(r.x, r.y); }
+  __device__ __forceinline__ float2 high() const { return make_float2(r.z, r.w); }
   __device__ __forceinline__ float at(int j) const { return j == 0 ? r.x : j == 1 ? r.y : j == 2 ? r.z : r.w; }
   struct Top {
     uint4 t = make_uint4(0u, 0u, 0u, 0u);
@@ -114,12 +113,43 @@ constexpr int kMatrixThreads = kBlock8 / kRowsPerWarp * 32, kMatrixWarps = kMatr
 template <typename T>
 constexpr int kMatrixCtas = sizeof(T) == 2 ? 3 : 2;  // per SM: what the values' registers allow
 
+// The codes of a warp's rows (`rows` of them, `n` of this lane's columns),
+// 128 bytes of a row at a time, and their scale bytes.
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void store_rows(const MatrixSeg& sg, const Four<T> (&f)[kRowsPerWarp], const BlockScale& square,
+                                           int64_t r0, int32_t c0, int rows, int n) {
+  const int lane = threadIdx.x % 32;
+  uint8_t* dst = sg.codes + r0 * sg.ld_out + c0 + lane * 4;
+  uint32_t mine = 0u;  // lane k: the bits of row k's largest
+#pragma unroll
+  for (int k = 0; k < kRowsPerWarp; ++k) {
+    BlockScale sc = square;
+    if (!sg.square) {
+      typename Four<T>::Top row;
+      row.add(f[k]);
+      const uint32_t top = Four<T>::fp32_bits(__reduce_max_sync(0xFFFFFFFFu, row.all()));
+      sc = BlockScale(top);
+      if (lane == k) mine = top;
+    }
+    uint32_t c = four_codes(f[k].low(), f[k].high(), sc.up());
+    if (sc.nan) c = 0u;
+    if (WHOLE || (k < rows && n >= 4)) {
+      __stcs(reinterpret_cast<uint32_t*>(dst), c);
+    } else if (k < rows) {
+      for (int j = 0; j < n; ++j) dst[j] = (uint8_t)(c >> (8 * j));
+    }
+    dst += sg.ld_out;
+  }
+  if (lane < (WHOLE ? kRowsPerWarp : rows))
+    sg.scales[scale_place(r0 + lane, c0 / kBlock8, (uint32_t)scale_groups(sg.cols))] =
+        (uint8_t)(sg.square ? square : BlockScale(mine)).byte();
+}
+
 // A CTA per tile: the next ones' loads then run under this one's stores.
 template <typename T, int CAP>
 __global__ void __launch_bounds__(kMatrixThreads, kMatrixCtas<T>) matrix8_pack(const __grid_constant__ MatrixParamsT<CAP> p) {
-  __shared__ alignas(16) uint32_t s_top[kMatrixWarps][kBlock8];  // largest of each column, by warp
-  __shared__ alignas(16) uint32_t s_scale[kBlock8];    // scale byte of each column
-  __shared__ uint32_t s_tile[kMatrixWarps];          // and of all of the warp's values
+  __shared__ alignas(16) uint32_t s_top[kMatrixWarps][kBlock8];  // largest of each column, by warp; then, first, of all
+  __shared__ uint32_t s_tile[kMatrixWarps];                      // and of all of the warp's values
   // values on their way to their lanes, a few rows of a warp at a time; then
   // the transposed codes, eight of a column at a time
   constexpr int kStageRows = sizeof(T) == 2 ? 8 : 4;
@@ -131,23 +161,26 @@ __global__ void __launch_bounds__(kMatrixThreads, kMatrixCtas<T>) matrix8_pack(c
   const MatrixSeg& sg = p.seg[find_seg(p, blockIdx.x)];
   const MatrixTile a = place_matrix_tile(p, sg, blockIdx.x);
   const int rows = min(kRowsPerWarp, a.rows - warp * kRowsPerWarp);  // of the warp
+  const int64_t r0 = (int64_t)a.r0 + warp * kRowsPerWarp;
+  const bool whole = a.rows == kBlock8 && a.cols == kBlock8;
   Four<T> f[kRowsPerWarp];
-  const T* src = static_cast<const T*>(sg.values) + ((int64_t)a.r0 + warp * kRowsPerWarp) * sg.ld + a.c0;
-  if (sg.vec && a.cols == kBlock8 && rows == kRowsPerWarp) {
+  const T* src = static_cast<const T*>(sg.values) + r0 * sg.ld + a.c0;
+  if (sg.vec && whole) {
+    src += lane * 4;
 #pragma unroll
-    for (int k = 0; k < kRowsPerWarp; ++k) f[k].load(src + k * sg.ld + lane * 4);
+    for (int k = 0; k < kRowsPerWarp; ++k, src += sg.ld) f[k].load(src);
   } else {
     // consecutive lanes load consecutive elements, and take four through
     // shared memory
 #pragma unroll
-    for (int half = 0; half < kRowsPerWarp; half += kStageRows) {
+    for (int part = 0; part < kRowsPerWarp; part += kStageRows) {
       T t[kStageRows][4];
 #pragma unroll
-      for (int k = 0; k < kStageRows; ++k)
+      for (int k = 0; k < kStageRows; ++k, src += sg.ld)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int c = lane + 32 * j;
-          t[k][j] = half + k < rows && c < a.cols ? __ldcs(src + (half + k) * sg.ld + c) : narrow<T>(0.f);
+          t[k][j] = part + k < rows && c < a.cols ? __ldcs(src + c) : narrow<T>(0.f);
         }
       __syncwarp();
 #pragma unroll
@@ -156,82 +189,60 @@ __global__ void __launch_bounds__(kMatrixThreads, kMatrixCtas<T>) matrix8_pack(c
         for (int j = 0; j < 4; ++j) s.stage[warp][k][lane + 32 * j] = t[k][j];
       __syncwarp();
 #pragma unroll
-      for (int k = 0; k < kStageRows; ++k) f[half + k].take(&s.stage[warp][k][lane * 4]);
+      for (int k = 0; k < kStageRows; ++k) f[part + k].take(&s.stage[warp][k][lane * 4]);
     }
   }
-  typename Four<T>::Top column;
+  uint32_t top = 0u;  // square: of the tile
+  if (sg.square || sg.codes_t) {
+    typename Four<T>::Top column;
 #pragma unroll
-  for (int k = 0; k < kRowsPerWarp; ++k) column.add(f[k]);
-  if (sg.square) {
-    const uint32_t all = __reduce_max_sync(0xFFFFFFFFu, column.all());
-    if (lane == 0) s_tile[warp] = all;
-  } else if (sg.codes_t) {
-    *reinterpret_cast<uint4*>(&s_top[warp][lane * 4]) = column.each();
+    for (int k = 0; k < kRowsPerWarp; ++k) column.add(f[k]);
+    if (sg.square) {
+      const uint32_t all = __reduce_max_sync(0xFFFFFFFFu, column.all());
+      if (lane == 0) s_tile[warp] = all;
+    } else {
+      *reinterpret_cast<uint4*>(&s_top[warp][lane * 4]) = column.each();
+    }
+    __syncthreads();
+    if (sg.square) {
+#pragma unroll
+      for (int w = 0; w < kMatrixWarps; ++w) top = max(top, s_tile[w]);
+    } else if (threadIdx.x < kBlock8) {
+      // a thread per column, which the lanes that have it read together below
+      uint32_t t = 0u;
+#pragma unroll
+      for (int w = 0; w < kMatrixWarps; ++w) t = max(t, s_top[w][threadIdx.x]);
+      s_top[0][threadIdx.x] = t;
+    }
   }
-  __syncthreads();
-  uint32_t scale = 0u;
-  if (sg.square) {
-#pragma unroll
-    for (int w = 0; w < kMatrixWarps; ++w) scale = max(scale, s_tile[w]);
-    scale = m_scale_of(Four<T>::fp32_bits(scale));
-  } else if (sg.codes_t && threadIdx.x < kBlock8) {
-    // a thread per column, which the lanes that have it read together below
-    uint32_t top = 0u;
-#pragma unroll
-    for (int w = 0; w < kMatrixWarps; ++w) top = max(top, s_top[w][threadIdx.x]);
-    s_scale[threadIdx.x] = m_scale_of(Four<T>::fp32_bits(top));
-  }
-  const float factor = code_factor(scale);
+  const BlockScale square(Four<T>::fp32_bits(top));
   if (sg.codes) {
-    uint8_t* dst = sg.codes + ((int64_t)a.r0 + warp * kRowsPerWarp) * sg.ld_out + a.c0 + lane * 4;
-    const int n = a.cols - lane * 4;
-    uint32_t mine = scale;  // lane k: row k's scale
-#pragma unroll
-    for (int k = 0; k < kRowsPerWarp; ++k) {
-      uint32_t sc = scale;
-      float up = factor;
-      if (!sg.square) {
-        typename Four<T>::Top row;
-        row.add(f[k]);
-        sc = m_scale_of(Four<T>::fp32_bits(__reduce_max_sync(0xFFFFFFFFu, row.all())));
-        up = code_factor(sc);
-        if (lane == k) mine = sc;
-      }
-      if (k >= rows) continue;
-      float x[4];
-      f[k].widen4(x);
-      const uint32_t c = four_codes(x, up, sc == 255u);
-      if (n >= 4) {
-        __stcs(reinterpret_cast<uint32_t*>(dst + k * sg.ld_out), c);
-      } else {
-        for (int j = 0; j < n; ++j) dst[k * sg.ld_out + j] = (uint8_t)(c >> (8 * j));
-      }
-    }
-    if (lane < rows)
-      sg.scales[scale_place((int64_t)a.r0 + warp * kRowsPerWarp + lane, a.c0 / kBlock8, (uint32_t)scale_groups(sg.cols))] =
-          (uint8_t)mine;
+    if (whole)
+      store_rows<T, true>(sg, f, square, r0, a.c0, kRowsPerWarp, 4);
+    else
+      store_rows<T, false>(sg, f, square, r0, a.c0, rows, a.cols - lane * 4);
   }
   if (!sg.codes_t) return;
-  uint4 scales_t = make_uint4(scale, scale, scale, scale);
+  uint4 tops = make_uint4(top, top, top, top);
   if (!sg.square) {
     __syncthreads();
-    scales_t = *reinterpret_cast<const uint4*>(&s_scale[lane * 4]);
+    tops = *reinterpret_cast<const uint4*>(&s_top[0][lane * 4]);
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t sc = j == 0 ? scales_t.x : j == 1 ? scales_t.y : j == 2 ? scales_t.z : scales_t.w;
-    const float up = code_factor(sc);
+    const BlockScale sc(Four<T>::fp32_bits(j == 0 ? tops.x : j == 1 ? tops.y : j == 2 ? tops.z : tops.w));
     uint32_t w[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const float v[4] = {f[4 * q].at(j), f[4 * q + 1].at(j), f[4 * q + 2].at(j), f[4 * q + 3].at(j)};
-      w[q] = four_codes(v, up, sc == 255u);
+      w[q] = four_codes(make_float2(f[4 * q].at(j), f[4 * q + 1].at(j)), make_float2(f[4 * q + 2].at(j), f[4 * q + 3].at(j)), sc.up());
+      if (sc.nan) w[q] = 0u;
     }
     // column 4 l + j holds sixteen pieces of 8 codes; turned by 2 l, so that
     // the lanes' writes here spread over the banks and pairs stay together
     s.turn[(lane * 4 + j) * 16 + ((warp + 2 * lane) & 15)] = make_uint2(w[0], w[1]);
-    if (warp == 0 && lane * 4 + j < a.cols && a.rows > 0)
-      sg.scales_t[scale_place((int64_t)a.c0 + lane * 4 + j, a.r0 / kBlock8, (uint32_t)scale_groups(sg.rows))] = (uint8_t)sc;
+    if (warp == j && lane * 4 + j < a.cols && a.rows > 0)
+      sg.scales_t[scale_place((int64_t)a.c0 + lane * 4 + j, a.r0 / kBlock8, (uint32_t)scale_groups(sg.rows))] =
+          (uint8_t)sc.byte();
   }
   __syncthreads();
   // eight lanes write the 128 codes of a column

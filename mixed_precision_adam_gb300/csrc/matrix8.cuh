@@ -135,20 +135,33 @@ __device__ __forceinline__ void round_eight(float (&f)[8]) {
 
 // -------------------------------------------------------------------- codes --
 
-// What values of a block with scale byte s are multiplied by before they are
-// rounded to codes (0 where the block reads as NaN).
-__device__ __forceinline__ float code_factor(uint32_t s) {
-  return s == 255u ? 0.f : __uint_as_float((254u - s) << 23);
+// What values of a block are multiplied by before they are rounded to codes,
+// 2^(127 - s) as (254 - s) << 23, straight from the bits of the block's
+// largest magnitude; its scale byte, and whether all of it reads as NaN.
+struct BlockScale {
+  uint32_t factor;
+  bool nan;
+  __device__ __forceinline__ explicit BlockScale(uint32_t top) {
+    const uint32_t e = (top + 0x1FFFFFu) & 0xFF800000u;  // m_scale_of's exponent, in place
+    nan = e >= 255u << 23;
+    factor = min((262u << 23) - e, 246u << 23);
+  }
+  __device__ __forceinline__ float2 up() const {
+    const float f = __uint_as_float(factor);
+    return make_float2(f, f);
+  }
+  __device__ __forceinline__ uint32_t byte() const { return nan ? 255u : 254u - (factor >> 23); }
+};
+// Codes of four values, nearest even, before the question whether the block
+// reads as NaN (all its codes are 0 then, whatever the conversion gave).
+__device__ __forceinline__ uint32_t four_codes(float2 a, float2 b, float2 up) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(__fmul2_rn(a, up), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(__fmul2_rn(b, up), __NV_SATFINITE, __NV_E4M3);
+  return __byte_perm(lo, hi, 0x5410);
 }
-// Two codes, nearest even.  Where the block reads as NaN they are 0: a NaN or
-// infinity times 0 is NaN, so that is asked for, not computed.
-__device__ __forceinline__ uint32_t two_codes(float a, float b, float factor, bool nan) {
-  if (nan) return 0u;
-  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(a, factor), __fmul_rn(b, factor)), __NV_SATFINITE,
-                                            __NV_E4M3);
-}
-__device__ __forceinline__ uint32_t four_codes(const float* f, float factor, bool nan) {
-  return two_codes(f[0], f[1], factor, nan) | two_codes(f[2], f[3], factor, nan) << 16;
+__device__ __forceinline__ uint32_t four_codes(const float* f, const BlockScale& s) {
+  const uint32_t c = four_codes(make_float2(f[0], f[1]), make_float2(f[2], f[3]), s.up());
+  return s.nan ? 0u : c;
 }
 // Eight codes' numbers before their block's unit.
 __device__ __forceinline__ void widen_codes(uint2 c, float (&f)[8]) {

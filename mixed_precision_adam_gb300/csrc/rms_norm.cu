@@ -43,12 +43,11 @@ __device__ __forceinline__ void store_codes(const NormRows& p, int64_t row, int 
     uint32_t top = top_of(f);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const uint32_t s = m_scale_of(top);
-    const float up = code_factor(s);
-    const uint2 code = make_uint2(four_codes(f, up, s == 255u), four_codes(f + 4, up, s == 255u));
+    const BlockScale s(top);
+    const uint2 code = make_uint2(four_codes(f, s), four_codes(f + 4, s));
     if (c < p.cols) {
       *reinterpret_cast<uint2*>(dst) = code;
-      if (threadIdx.x % 16 == 0) p.scales[scale_place(row, c / kBlock8, p.groups)] = (uint8_t)s;
+      if (threadIdx.x % 16 == 0) p.scales[scale_place(row, c / kBlock8, p.groups)] = (uint8_t)s.byte();
     }
   } else {
     // four values of every lane
@@ -57,13 +56,13 @@ __device__ __forceinline__ void store_codes(const NormRows& p, int64_t row, int 
       uint32_t top = 0u;
 #pragma unroll
       for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(f[q + j]) & 0x7FFFFFFFu);
-      const uint32_t s = m_scale_of(__reduce_max_sync(0xFFFFFFFFu, top));
-      const uint32_t code = four_codes(f + q, code_factor(s), s == 255u);
+      const BlockScale s(__reduce_max_sync(0xFFFFFFFFu, top));
+      const uint32_t code = four_codes(f + q, s);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (c + 32 * (q + j) < p.cols) dst[32 * (q + j)] = (uint8_t)(code >> (8 * j));
       if (threadIdx.x % 32 == 0 && c + 32 * q < p.cols)
-        p.scales[scale_place(row, (c + 32 * q) / kBlock8, p.groups)] = (uint8_t)s;
+        p.scales[scale_place(row, (c + 32 * q) / kBlock8, p.groups)] = (uint8_t)s.byte();
     }
   }
 }
