@@ -6,6 +6,8 @@
 // blocks end with the tile: a row's maximum is one warp's, a column's is
 // gathered over the warps, and the transposed codes turn in shared memory, so
 // that both are written in whole 128-byte lines.
+#include <type_traits>
+
 #include "matrix8.cuh"
 
 namespace dopt {
@@ -69,14 +71,19 @@ struct Four {  // 16-bit types
     const float2 x = widen_pair<T>(j < 2 ? r.x : r.y);
     return j & 1 ? x.y : x.x;
   }
-  struct Top {  // of each of the four
+  struct Top {  // of each of the four; NaN where one is
     uint32_t lo = 0u, hi = 0u;
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+      using Pair = std::conditional_t<std::is_same<T, __half>::value, __half2, __nv_bfloat162>;
+      const Pair m = __hmax2_nan(*reinterpret_cast<const Pair*>(&a), __habs2(*reinterpret_cast<const Pair*>(&b)));
+      return *reinterpret_cast<const uint32_t*>(&m);
+    }
     __device__ __forceinline__ void add(const Four& v) {
-      lo = __vmaxu2(lo, v.r.x & 0x7FFF7FFFu);
-      hi = __vmaxu2(hi, v.r.y & 0x7FFF7FFFu);
+      lo = larger(lo, v.r.x);
+      hi = larger(hi, v.r.y);
     }
     __device__ __forceinline__ uint32_t all() const {
-      const uint32_t m = __vmaxu2(lo, hi);
+      const uint32_t m = larger(lo, hi);
       return max(m & 0xFFFFu, m >> 16);
     }
     __device__ __forceinline__ uint4 each() const { return make_uint4(lo & 0xFFFFu, lo >> 16, hi & 0xFFFFu, hi >> 16); }
