@@ -113,23 +113,27 @@ struct Four<float> {
   static __device__ __forceinline__ uint32_t fp32_bits(uint32_t top) { return top; }
 };
 
-// Warp w has rows 8 w to 8 w + 7 of a tile, lane l its columns 4 l to 4 l + 3:
-// 32 values per thread, all of them loaded before the first is used.
-constexpr int kRowsPerWarp = 8;
-constexpr int kMatrixThreads = kBlock8 / kRowsPerWarp * 32, kMatrixWarps = kMatrixThreads / 32;
+// A warp has consecutive rows of a tile, 16 of 16-bit values and 8 of fp32
+// ones, lane l its columns 4 l to 4 l + 3: 128 bytes per thread, all of them
+// loaded before the first is used.
 template <typename T>
-constexpr int kMatrixCtas = sizeof(T) == 2 ? 3 : 2;  // per SM: what the values' registers allow
+struct PackShape {
+  static constexpr int kRows = sizeof(T) == 2 ? 16 : 8;
+  static constexpr int kWarps = kBlock8 / kRows, kThreads = kWarps * 32;
+  static constexpr int kCtas = sizeof(T) == 2 ? 4 : 2;  // per SM: what the values' registers allow
+};
 
 // The codes of a warp's rows (`rows` of them, `n` of this lane's columns),
 // 128 bytes of a row at a time, and their scale bytes.
 template <typename T, bool WHOLE>
-__device__ __forceinline__ void store_rows(const MatrixSeg& sg, const Four<T> (&f)[kRowsPerWarp], const BlockScale& square,
+__device__ __forceinline__ void store_rows(const MatrixSeg& sg, const Four<T> (&f)[PackShape<T>::kRows], const BlockScale& square,
                                            int64_t r0, int32_t c0, int rows, int n) {
+  constexpr int kRows = PackShape<T>::kRows;
   const int lane = threadIdx.x % 32;
   uint8_t* dst = sg.codes + r0 * sg.ld_out + c0 + lane * 4;
   uint32_t mine = 0u;  // lane k: the bits of row k's largest
 #pragma unroll
-  for (int k = 0; k < kRowsPerWarp; ++k) {
+  for (int k = 0; k < kRows; ++k) {
     BlockScale sc = square;
     if (!sg.square) {
       typename Four<T>::Top row;
@@ -147,40 +151,41 @@ __device__ __forceinline__ void store_rows(const MatrixSeg& sg, const Four<T> (&
     }
     dst += sg.ld_out;
   }
-  if (lane < (WHOLE ? kRowsPerWarp : rows))
+  if (lane < (WHOLE ? kRows : rows))
     sg.scales[scale_place(r0 + lane, c0 / kBlock8, (uint32_t)scale_groups(sg.cols))] =
         (uint8_t)(sg.square ? square : BlockScale(mine)).byte();
 }
 
 // A CTA per tile: the next ones' loads then run under this one's stores.
 template <typename T, int CAP>
-__global__ void __launch_bounds__(kMatrixThreads, kMatrixCtas<T>) matrix8_pack(const __grid_constant__ MatrixParamsT<CAP> p) {
-  __shared__ alignas(16) uint32_t s_top[kMatrixWarps][kBlock8];  // largest of each column, by warp; then, first, of all
-  __shared__ uint32_t s_tile[kMatrixWarps];                      // and of all of the warp's values
+__global__ void __launch_bounds__(PackShape<T>::kThreads, PackShape<T>::kCtas) matrix8_pack(const __grid_constant__ MatrixParamsT<CAP> p) {
+  constexpr int kRows = PackShape<T>::kRows, kWarps = PackShape<T>::kWarps, kPackThreads = PackShape<T>::kThreads;
+  __shared__ alignas(16) uint32_t s_top[kWarps][kBlock8];  // largest of each column, by warp; then, first, of all
+  __shared__ uint32_t s_tile[kWarps];                      // and of all of the warp's values
   // values on their way to their lanes, a few rows of a warp at a time; then
-  // the transposed codes, eight of a column at a time
+  // the transposed codes, a warp's of a column at a time
   constexpr int kStageRows = sizeof(T) == 2 ? 8 : 4;
   __shared__ union alignas(16) {
-    T stage[kMatrixWarps][kStageRows][kBlock8];
-    uint2 turn[kBlock8 * kBlock8 / 8];
+    T stage[kWarps][kStageRows][kBlock8];
+    uint32_t turn[kBlock8 * kBlock8 / 4];
   } s;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const MatrixSeg& sg = p.seg[find_seg(p, blockIdx.x)];
   const MatrixTile a = place_matrix_tile(p, sg, blockIdx.x);
-  const int rows = min(kRowsPerWarp, a.rows - warp * kRowsPerWarp);  // of the warp
-  const int64_t r0 = (int64_t)a.r0 + warp * kRowsPerWarp;
+  const int rows = min(kRows, a.rows - warp * kRows);  // of the warp
+  const int64_t r0 = (int64_t)a.r0 + warp * kRows;
   const bool whole = a.rows == kBlock8 && a.cols == kBlock8;
-  Four<T> f[kRowsPerWarp];
+  Four<T> f[kRows];
   const T* src = static_cast<const T*>(sg.values) + r0 * sg.ld + a.c0;
   if (sg.vec && whole) {
     src += lane * 4;
 #pragma unroll
-    for (int k = 0; k < kRowsPerWarp; ++k, src += sg.ld) f[k].load(src);
+    for (int k = 0; k < kRows; ++k, src += sg.ld) f[k].load(src);
   } else {
     // consecutive lanes load consecutive elements, and take four through
     // shared memory
 #pragma unroll
-    for (int part = 0; part < kRowsPerWarp; part += kStageRows) {
+    for (int part = 0; part < kRows; part += kStageRows) {
       T t[kStageRows][4];
 #pragma unroll
       for (int k = 0; k < kStageRows; ++k, src += sg.ld)
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(kMatrixThreads, kMatrixCtas<T>) matrix8_pack(c
   if (sg.square || sg.codes_t) {
     typename Four<T>::Top column;
 #pragma unroll
-    for (int k = 0; k < kRowsPerWarp; ++k) column.add(f[k]);
+    for (int k = 0; k < kRows; ++k) column.add(f[k]);
     if (sg.square) {
       const uint32_t all = __reduce_max_sync(0xFFFFFFFFu, column.all());
       if (lane == 0) s_tile[warp] = all;
@@ -213,19 +218,19 @@ __global__ void __launch_bounds__(kMatrixThreads, kMatrixCtas<T>) matrix8_pack(c
     __syncthreads();
     if (sg.square) {
 #pragma unroll
-      for (int w = 0; w < kMatrixWarps; ++w) top = max(top, s_tile[w]);
+      for (int w = 0; w < kWarps; ++w) top = max(top, s_tile[w]);
     } else if (threadIdx.x < kBlock8) {
       // a thread per column, which the lanes that have it read together below
       uint32_t t = 0u;
 #pragma unroll
-      for (int w = 0; w < kMatrixWarps; ++w) t = max(t, s_top[w][threadIdx.x]);
+      for (int w = 0; w < kWarps; ++w) t = max(t, s_top[w][threadIdx.x]);
       s_top[0][threadIdx.x] = t;
     }
   }
   const BlockScale square(Four<T>::fp32_bits(top));
   if (sg.codes) {
     if (whole)
-      store_rows<T, true>(sg, f, square, r0, a.c0, kRowsPerWarp, 4);
+      store_rows<T, true>(sg, f, square, r0, a.c0, kRows, 4);
     else
       store_rows<T, false>(sg, f, square, r0, a.c0, rows, a.cols - lane * 4);
   }
@@ -238,15 +243,19 @@ __global__ void __launch_bounds__(kMatrixThreads, kMatrixCtas<T>) matrix8_pack(c
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const BlockScale sc(Four<T>::fp32_bits(j == 0 ? tops.x : j == 1 ? tops.y : j == 2 ? tops.z : tops.w));
-    uint32_t w[2];
+    uint32_t w[kRows / 4];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < kRows / 4; ++q) {
       w[q] = four_codes(make_float2(f[4 * q].at(j), f[4 * q + 1].at(j)), make_float2(f[4 * q + 2].at(j), f[4 * q + 3].at(j)), sc.up());
       if (sc.nan) w[q] = 0u;
     }
-    // column 4 l + j holds sixteen pieces of 8 codes; turned by 2 l, so that
-    // the lanes' writes here spread over the banks and pairs stay together
-    s.turn[(lane * 4 + j) * 16 + ((warp + 2 * lane) & 15)] = make_uint2(w[0], w[1]);
+    // a column's 128 codes are turned by 16 l, so that the lanes' writes here
+    // spread over the banks and 16 codes stay together
+    uint32_t* at = &s.turn[(lane * 4 + j) * 32 + ((warp * (kRows / 4) + 4 * lane) & 31)];
+    if constexpr (kRows == 16)
+      *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+    else
+      *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
     if (warp == j && lane * 4 + j < a.cols && a.rows > 0)
       sg.scales_t[scale_place((int64_t)a.c0 + lane * 4 + j, a.r0 / kBlock8, (uint32_t)scale_groups(sg.rows))] =
           (uint8_t)sc.byte();
@@ -254,10 +263,10 @@ __global__ void __launch_bounds__(kMatrixThreads, kMatrixCtas<T>) matrix8_pack(c
   __syncthreads();
   // eight lanes write the 128 codes of a column
 #pragma unroll
-  for (int k = 0; k < kBlock8 * 8 / kMatrixThreads; ++k) {
-    const int c = k * (kMatrixThreads / 8) + threadIdx.x / 8, piece = threadIdx.x % 8;
+  for (int k = 0; k < kBlock8 * 8 / kPackThreads; ++k) {
+    const int c = k * (kPackThreads / 8) + threadIdx.x / 8, piece = threadIdx.x % 8;
     if (c >= a.cols) continue;
-    const uint4 v = *reinterpret_cast<const uint4*>(&s.turn[c * 16 + ((2 * piece + 2 * (c >> 2)) & 15)]);
+    const uint4 v = *reinterpret_cast<const uint4*>(&s.turn[c * 32 + ((4 * piece + 4 * (c >> 2)) & 31)]);
     uint8_t* dst = sg.codes_t + ((int64_t)a.c0 + c) * sg.ld_t + a.r0 + piece * 16;
     const int m = a.rows - piece * 16;
     if (m >= 16) {
@@ -271,17 +280,18 @@ __global__ void __launch_bounds__(kMatrixThreads, kMatrixCtas<T>) matrix8_pack(c
   }
 }
 
-// Rows of a tile 8 w to 8 w + 7 are warp w's.  Where the values can be written
+// Warp w has 16 rows of a tile.  Where the values can be written
 // in vectors a lane has 16 codes of every fourth row; else four of each row,
 // which go to the lanes that make consecutive elements of them.
+constexpr int kUnpackRows = kBlock8 / (kThreads / 32);
 template <typename T, int CAP>
-__global__ void __launch_bounds__(kMatrixThreads, 2) matrix8_unpack(const __grid_constant__ MatrixParamsT<CAP> p) {
+__global__ void __launch_bounds__(kThreads, 4) matrix8_unpack(const __grid_constant__ MatrixParamsT<CAP> p) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const MatrixSeg& sg = p.seg[find_seg(p, blockIdx.x)];
   const MatrixTile a = place_matrix_tile(p, sg, blockIdx.x);
-  const int rows = min(kRowsPerWarp, a.rows - warp * kRowsPerWarp);
+  const int rows = min(kUnpackRows, a.rows - warp * kUnpackRows);
   if (rows <= 0) return;
-  const int64_t r0 = (int64_t)a.r0 + warp * kRowsPerWarp;
+  const int64_t r0 = (int64_t)a.r0 + warp * kUnpackRows;
   const uint32_t groups = (uint32_t)scale_groups(sg.cols), block = a.c0 / kBlock8;
   const uint8_t* codes = sg.codes + r0 * sg.ld_out + a.c0;
   T* values = static_cast<T*>(sg.values) + r0 * sg.ld + a.c0;
@@ -289,14 +299,14 @@ __global__ void __launch_bounds__(kMatrixThreads, 2) matrix8_unpack(const __grid
   const uint32_t scale = lane < rows ? sg.scales[scale_place(r0 + lane, block, groups)] : 0u;
   if (sg.vec && a.cols == kBlock8) {
     const int c = lane % 8 * 16;
-    uint4 code[kRowsPerWarp / 4];
+    uint4 code[kUnpackRows / 4];
 #pragma unroll
-    for (int k = 0; k < kRowsPerWarp / 4; ++k) {
+    for (int k = 0; k < kUnpackRows / 4; ++k) {
       const int r = lane / 8 + 4 * k;
       if (r < rows) code[k] = __ldcs(reinterpret_cast<const uint4*>(codes + r * sg.ld_out + c));
     }
 #pragma unroll
-    for (int k = 0; k < kRowsPerWarp / 4; ++k) {
+    for (int k = 0; k < kUnpackRows / 4; ++k) {
       const int r = lane / 8 + 4 * k;
       const float unit = m_unit(__shfl_sync(0xFFFFFFFFu, scale, r));
       if (r >= rows) continue;
@@ -313,9 +323,9 @@ __global__ void __launch_bounds__(kMatrixThreads, 2) matrix8_unpack(const __grid
     return;
   }
   const int n = a.cols - lane * 4;
-  uint32_t code[kRowsPerWarp];
+  uint32_t code[kUnpackRows];
 #pragma unroll
-  for (int k = 0; k < kRowsPerWarp; ++k) {
+  for (int k = 0; k < kUnpackRows; ++k) {
     code[k] = 0u;
     if (k >= rows) continue;
     const uint8_t* src = codes + k * sg.ld_out + lane * 4;
@@ -325,7 +335,7 @@ __global__ void __launch_bounds__(kMatrixThreads, 2) matrix8_unpack(const __grid
       for (int j = 0; j < n; ++j) code[k] |= (uint32_t)src[j] << (8 * j);
   }
 #pragma unroll
-  for (int k = 0; k < kRowsPerWarp; ++k) {
+  for (int k = 0; k < kUnpackRows; ++k) {
     if (k >= rows) break;
     const float unit = m_unit(__shfl_sync(0xFFFFFFFFu, scale, k));
     // the codes of columns l, l + 32, l + 64 and l + 96, from lanes l / 4, ...
@@ -343,20 +353,20 @@ __global__ void __launch_bounds__(kMatrixThreads, 2) matrix8_unpack(const __grid
 
 namespace {
 
-template <auto Small, auto Big>
+template <auto Small, auto Big, int THREADS>
 int launch_matrices(const MatrixParamsT<kMatrixCap>& p, cudaStream_t s, const char* what) {
   if (p.n_seg <= kMatrixSmallCap)
-    return launch_table<Small, 0, kMatrixThreads>(compact_table<MatrixParamsT<kMatrixSmallCap>, MatrixHead>(p), s, what, false,
+    return launch_table<Small, 0, THREADS>(compact_table<MatrixParamsT<kMatrixSmallCap>, MatrixHead>(p), s, what, false,
                                                   p.n_tiles);
-  return launch_table<Big, 0, kMatrixThreads>(p, s, what, false, p.n_tiles);
+  return launch_table<Big, 0, THREADS>(p, s, what, false, p.n_tiles);
 }
 template <typename T>
 int launch_pack(const MatrixParamsT<kMatrixCap>& p, cudaStream_t s) {
-  return launch_matrices<matrix8_pack<T, kMatrixSmallCap>, matrix8_pack<T, kMatrixCap>>(p, s, "matrix8_pack launch");
+  return launch_matrices<matrix8_pack<T, kMatrixSmallCap>, matrix8_pack<T, kMatrixCap>, PackShape<T>::kThreads>(p, s, "matrix8_pack launch");
 }
 template <typename T>
 int launch_unpack(const MatrixParamsT<kMatrixCap>& p, cudaStream_t s) {
-  return launch_matrices<matrix8_unpack<T, kMatrixSmallCap>, matrix8_unpack<T, kMatrixCap>>(p, s, "matrix8_unpack launch");
+  return launch_matrices<matrix8_unpack<T, kMatrixSmallCap>, matrix8_unpack<T, kMatrixCap>, kThreads>(p, s, "matrix8_unpack launch");
 }
 
 int64_t tiles_of(const dopt_matrix_values& m) { return row_blocks(m.rows) * row_blocks(m.cols); }
