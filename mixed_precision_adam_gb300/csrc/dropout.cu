@@ -39,13 +39,13 @@ __global__ void __launch_bounds__(kThreads) dropout(const __grid_constant__ Drop
   }
 #pragma unroll
   for (int v = 0; v < kDropEights; ++v) {
-    float f[8], g[8];
+    float2 f[4], g[4];
     a[v].widen8(f);
     if (p.drop.threshold) drop_eight<VEC>(f, (uint64_t)at[v], p.drop, key);
     if (residual) {
       r[v].widen8(g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] += g[j];
+      for (int k = 0; k < 4; ++k) f[k] = __fadd2_rn(f[k], g[k]);
     }
     Eight8<T, VEC>::store(y + at[v], n[v], f);
   }

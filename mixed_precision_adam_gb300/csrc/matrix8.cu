@@ -313,10 +313,10 @@ __global__ void __launch_bounds__(kThreads, 4) matrix8_unpack(const __grid_const
       T* dst = values + r * sg.ld + c;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        float f[8];
+        float2 f[4];
         widen_codes(q ? make_uint2(code[k].z, code[k].w) : make_uint2(code[k].x, code[k].y), f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], unit);
+        for (int j = 0; j < 4; ++j) f[j] = __fmul2_rn(f[j], both_of(unit));
         Eight8<T, true>::store(dst + 8 * q, 8, f);
       }
     }
@@ -343,11 +343,12 @@ __global__ void __launch_bounds__(kThreads, 4) matrix8_unpack(const __grid_const
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       mine |= (__shfl_sync(0xFFFFFFFFu, code[k], lane / 4 + 8 * j) >> (8 * (lane & 3)) & 0xFFu) << (8 * j);
-    float f[8];
+    float2 f[4];
     widen_codes(make_uint2(mine, 0u), f);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (lane + 32 * j < a.cols) __stcs(values + k * sg.ld + lane + 32 * j, narrow<T>(__fmul_rn(f[j], unit)));
+      if (lane + 32 * j < a.cols)
+        __stcs(values + k * sg.ld + lane + 32 * j, narrow<T>(__fmul_rn(j & 1 ? f[j / 2].y : f[j / 2].x, unit)));
   }
 }
 

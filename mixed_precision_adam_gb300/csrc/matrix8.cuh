@@ -35,7 +35,8 @@ inline bool eight_vectors(const void* p, int64_t ld, size_t elem) {
 }
 
 // Eight elements of a row as a load leaves them, widened only when they are
-// used, so that a thread's loads are all under way before the first wait.
+// used, so that a thread's loads are all under way before the first wait;
+// then four pairs, for instructions on two fp32 numbers.
 // VEC: consecutive elements in one access (two for fp32); else every 32nd,
 // so that a warp's accesses are consecutive.
 template <typename T, bool VEC>
@@ -46,14 +47,14 @@ struct Eight8 {
 #pragma unroll
     for (int j = 0; j < 8; ++j) e[j] = 32 * j < n ? __ldcs(p + 32 * j) : narrow<T>(0.f);
   }
-  __device__ __forceinline__ void widen8(float (&f)[8]) const {
+  __device__ __forceinline__ void widen8(float2 (&f)[4]) const {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = widen<T>(e[j]);
+    for (int k = 0; k < 4; ++k) f[k] = make_float2(widen<T>(e[2 * k]), widen<T>(e[2 * k + 1]));
   }
-  static __device__ __forceinline__ void store(T* p, int n, const float (&f)[8]) {
+  static __device__ __forceinline__ void store(T* p, int n, const float2 (&f)[4]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (32 * j < n) __stcs(p + 32 * j, narrow<T>(f[j]));
+      if (32 * j < n) __stcs(p + 32 * j, narrow<T>(j & 1 ? f[j / 2].y : f[j / 2].x));
   }
 };
 template <>
@@ -66,13 +67,13 @@ struct Eight8<float, true> {
       b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
     }
   }
-  __device__ __forceinline__ void widen8(float (&f)[8]) const {
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  __device__ __forceinline__ void widen8(float2 (&f)[4]) const {
+    f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w), f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
   }
-  static __device__ __forceinline__ void store(float* p, int n, const float (&f)[8]) {
+  static __device__ __forceinline__ void store(float* p, int n, const float2 (&f)[4]) {
     if (n <= 0) return;
-    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
-    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0].x, f[0].y, f[1].x, f[1].y));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[2].x, f[2].y, f[3].x, f[3].y));
   }
 };
 // Two 16-bit elements of a word.
@@ -87,15 +88,15 @@ __device__ __forceinline__ float2 widen_pair<__half>(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 template <typename T>
-__device__ __forceinline__ uint32_t narrow_pair(float a, float b);
+__device__ __forceinline__ uint32_t narrow_pair(float2 x);
 template <>
-__device__ __forceinline__ uint32_t narrow_pair<__nv_bfloat16>(float a, float b) {
-  const __nv_bfloat162 h = __float22bfloat162_rn(make_float2(a, b));
+__device__ __forceinline__ uint32_t narrow_pair<__nv_bfloat16>(float2 x) {
+  const __nv_bfloat162 h = __float22bfloat162_rn(x);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 template <>
-__device__ __forceinline__ uint32_t narrow_pair<__half>(float a, float b) {
-  const __half2 h = __float22half2_rn(make_float2(a, b));
+__device__ __forceinline__ uint32_t narrow_pair<__half>(float2 x) {
+  const __half2 h = __float22half2_rn(x);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 template <typename T>
@@ -105,33 +106,23 @@ struct Eight8<T, true> {
     r = make_uint4(0u, 0u, 0u, 0u);
     if (n > 0) r = __ldcs(reinterpret_cast<const uint4*>(p));
   }
-  __device__ __forceinline__ void widen8(float (&f)[8]) const {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 x = widen_pair<T>(w[k]);
-      f[2 * k] = x.x;
-      f[2 * k + 1] = x.y;
-    }
+  __device__ __forceinline__ void widen8(float2 (&f)[4]) const {
+    f[0] = widen_pair<T>(r.x), f[1] = widen_pair<T>(r.y), f[2] = widen_pair<T>(r.z), f[3] = widen_pair<T>(r.w);
   }
-  static __device__ __forceinline__ void store(T* p, int n, const float (&f)[8]) {
+  static __device__ __forceinline__ void store(T* p, int n, const float2 (&f)[4]) {
     if (n <= 0) return;
-    __stcs(reinterpret_cast<uint4*>(p), make_uint4(narrow_pair<T>(f[0], f[1]), narrow_pair<T>(f[2], f[3]),
-                                                   narrow_pair<T>(f[4], f[5]), narrow_pair<T>(f[6], f[7])));
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(narrow_pair<T>(f[0]), narrow_pair<T>(f[1]), narrow_pair<T>(f[2]), narrow_pair<T>(f[3])));
   }
 };
 // f rounded to T and widened again.
 template <typename T>
-__device__ __forceinline__ void round_eight(float (&f)[8]) {
+__device__ __forceinline__ void round_eight(float2 (&f)[4]) {
   if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 x = widen_pair<T>(narrow_pair<T>(f[2 * k], f[2 * k + 1]));
-      f[2 * k] = x.x;
-      f[2 * k + 1] = x.y;
-    }
+    for (int k = 0; k < 4; ++k) f[k] = widen_pair<T>(narrow_pair<T>(f[k]));
   }
 }
+__device__ __forceinline__ float2 both_of(float x) { return make_float2(x, x); }
 
 // -------------------------------------------------------------------- codes --
 
@@ -159,27 +150,23 @@ __device__ __forceinline__ uint32_t four_codes(float2 a, float2 b, float2 up) {
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(__fmul2_rn(b, up), __NV_SATFINITE, __NV_E4M3);
   return __byte_perm(lo, hi, 0x5410);
 }
-__device__ __forceinline__ uint32_t four_codes(const float* f, const BlockScale& s) {
-  const uint32_t c = four_codes(make_float2(f[0], f[1]), make_float2(f[2], f[3]), s.up());
+__device__ __forceinline__ uint32_t four_codes(float2 a, float2 b, const BlockScale& s) {
+  const uint32_t c = four_codes(a, b, s.up());
   return s.nan ? 0u : c;
 }
 // Eight codes' numbers before their block's unit.
-__device__ __forceinline__ void widen_codes(uint2 c, float (&f)[8]) {
+__device__ __forceinline__ void widen_codes(uint2 c, float2 (&f)[4]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const uint32_t w = k < 2 ? c.x : c.y;
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((k & 1) ? w >> 16 : w & 0xFFFFu), __NV_E4M3);
-    const float2 x = __half22float2(__half2(h));
-    f[2 * k] = x.x;
-    f[2 * k + 1] = x.y;
+    f[k] = __half22float2(__half2(h));
   }
 }
-// The bits of the largest magnitude of eight values (a NaN's are above all).
-__device__ __forceinline__ uint32_t top_of(const float (&f)[8]) {
-  uint32_t top = 0u;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-  return top;
+// The bits of the larger magnitude of two values and `top` (a NaN's are above
+// all).
+__device__ __forceinline__ uint32_t top_of(uint32_t top, float2 f) {
+  return __vimax3_u32(top, __float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu);
 }
 
 // ------------------------------------------------------------------ dropout --
@@ -205,21 +192,22 @@ __device__ __forceinline__ uint32_t drop_hash(uint64_t pair, uint32_t key) {
 // Drops among eight elements from element i on: consecutive ones with i a
 // multiple of 8 (VEC), two to a hash; or every 32nd.
 template <bool VEC>
-__device__ __forceinline__ void drop_eight(float (&f)[8], uint64_t i, const Drop& d, uint32_t key) {
+__device__ __forceinline__ void drop_eight(float2 (&f)[4], uint64_t i, const Drop& d, uint32_t key) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    uint32_t r;
+  for (int k = 0; k < 4; ++k) {
+    uint32_t r0, r1;
     if constexpr (VEC) {
-      if (k & 1) continue;
-      const uint32_t h = drop_hash((i >> 1) + k / 2, key);
-      f[k + 1] = (h >> 16) < d.threshold ? 0.f : f[k + 1] * d.keep;
-      r = h & 0xFFFFu;
+      const uint32_t h = drop_hash((i >> 1) + k, key);
+      r0 = h & 0xFFFFu;
+      r1 = h >> 16;
     } else {
-      const uint64_t at = i + 32 * k;
-      const uint32_t h = drop_hash(at >> 1, key);
-      r = at & 1 ? h >> 16 : h & 0xFFFFu;
+      const uint64_t at = i + 64 * k;  // i + 64 k and i + 64 k + 32 have one parity
+      const uint32_t h0 = drop_hash(at >> 1, key), h1 = drop_hash((at + 32) >> 1, key);
+      r0 = at & 1 ? h0 >> 16 : h0 & 0xFFFFu;
+      r1 = at & 1 ? h1 >> 16 : h1 & 0xFFFFu;
     }
-    f[k] = r < d.threshold ? 0.f : f[k] * d.keep;
+    const float2 kept = __fmul2_rn(f[k], both_of(d.keep));
+    f[k] = make_float2(r0 < d.threshold ? 0.f : kept.x, r1 < d.threshold ? 0.f : kept.y);
   }
 }
 

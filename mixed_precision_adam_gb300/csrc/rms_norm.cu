@@ -36,15 +36,17 @@ __device__ __noinline__ double row_sum_wide(double x, double (&s_sum)[kMaxRowThr
 
 // The codes of a thread's eight values and their blocks' scale bytes.
 template <bool VEC>
-__device__ __forceinline__ void store_codes(const NormRows& p, int64_t row, int c, const float (&f)[8]) {
+__device__ __forceinline__ void store_codes(const NormRows& p, int64_t row, int c, const float2 (&f)[4]) {
   uint8_t* dst = p.codes + row * p.ld_codes + c;
   if constexpr (VEC) {
     // a block of 128 columns is sixteen threads'
-    uint32_t top = top_of(f);
+    uint32_t top = 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = top_of(top, f[k]);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     const BlockScale s(top);
-    const uint2 code = make_uint2(four_codes(f, s), four_codes(f + 4, s));
+    const uint2 code = make_uint2(four_codes(f[0], f[1], s), four_codes(f[2], f[3], s));
     if (c < p.cols) {
       *reinterpret_cast<uint2*>(dst) = code;
       if (threadIdx.x % 16 == 0) p.scales[scale_place(row, c / kBlock8, p.groups)] = (uint8_t)s.byte();
@@ -52,17 +54,15 @@ __device__ __forceinline__ void store_codes(const NormRows& p, int64_t row, int 
   } else {
     // four values of every lane
 #pragma unroll
-    for (int q = 0; q < 8; q += 4) {
-      uint32_t top = 0u;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(f[q + j]) & 0x7FFFFFFFu);
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t top = top_of(top_of(0u, f[2 * q]), f[2 * q + 1]);
       const BlockScale s(__reduce_max_sync(0xFFFFFFFFu, top));
-      const uint32_t code = four_codes(f + q, s);
+      const uint32_t code = four_codes(f[2 * q], f[2 * q + 1], s);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (c + 32 * (q + j) < p.cols) dst[32 * (q + j)] = (uint8_t)(code >> (8 * j));
-      if (threadIdx.x % 32 == 0 && c + 32 * q < p.cols)
-        p.scales[scale_place(row, (c + 32 * q) / kBlock8, p.groups)] = (uint8_t)s.byte();
+        if (c + 32 * (4 * q + j) < p.cols) dst[32 * (4 * q + j)] = (uint8_t)(code >> (8 * j));
+      if (threadIdx.x % 32 == 0 && c + 128 * q < p.cols)
+        p.scales[scale_place(row, (c + 128 * q) / kBlock8, p.groups)] = (uint8_t)s.byte();
     }
   }
 }
@@ -72,13 +72,21 @@ __device__ __forceinline__ void store_codes(const NormRows& p, int64_t row, int 
 template <typename T, int V>
 constexpr bool kRowAhead = V * sizeof(T) <= 8;
 
-template <typename T, int V, bool VEC, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : kMaxRowThreads) rms_norm(const __grid_constant__ NormRows p) {
+// Threads and CTAs per SM that a kernel is compiled for (256 columns of bf16
+// to 8 bits: 60 us with three CTAs, 72 with the two of 96 registers).
+template <typename T, int V, bool VEC, int WARPS>
+constexpr int kRowBound = WARPS == 0 ? 256 : kMaxRowThreads;
+template <typename T, int V, bool VEC, int WARPS>
+constexpr int kRowCtas = WARPS > 0 ? 1 : V == 1 ? 3 : 2;
+
+template <typename T, int V, bool VEC, int WARPS>
+__global__ void __launch_bounds__(kRowBound<T, V, VEC, WARPS>, kRowCtas<T, V, VEC, WARPS>) rms_norm(const __grid_constant__ NormRows p) {
+  constexpr bool WARP = kWarpRows<WARPS>;
   __shared__ RowSums s_sum[2];
   __shared__ double s_wide[kMaxRowThreads / 32];
   using Piece = Eight8<T, VEC>;
   const RowShape<WARP> at;
-  clear_sums<WARP>(s_sum);
+  clear_sums<WARPS>(s_sum);
   const uint32_t key = drop_key(p.drop);
   const T* x = static_cast<const T*>(p.x.data);
   const T* residual = static_cast<const T*>(p.residual.data);
@@ -97,17 +105,17 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxRowThreads) rms_norm(const __
   const RowGain<T, V, VEC, WARP, V <= 2 || (VEC && sizeof(T) == 2)> gain(p.gain, p.gain_f32, at, p.cols);
   int turn = 0;
   for (; row < p.rows; row += stride) {
-    float f[V][8], sum = 0.f;
+    float2 f[V][4], squares = make_float2(0.f, 0.f);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = at.template column<V, VEC>(v);
       xs[v].widen8(f[v]);
       if (p.drop.threshold) drop_eight<VEC>(f[v], (uint64_t)row * p.cols + c, p.drop, key);
       if (residual) {
-        float r[8];
+        float2 r[4];
         rs[v].widen8(r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[v][j] += r[j];
+        for (int k = 0; k < 4; ++k) f[v][k] = __fadd2_rn(f[v][k], r[k]);
       }
       // what the norm sees is what is stored: the backward pass, and a norm
       // of h alone, then see the same
@@ -119,9 +127,9 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxRowThreads) rms_norm(const __
       const int c = at.template column<V, VEC>(v);
       if (p.h.data) Piece::store(static_cast<T*>(p.h.data) + row * p.h.ld + c, p.cols - c, f[v]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(f[v][j], f[v][j], sum);
+      for (int k = 0; k < 4; ++k) squares = __ffma2_rn(f[v][k], f[v][k], squares);
     }
-    sum = row_sum<WARP>(sum, s_sum[turn]);
+    const float sum = row_sum<WARPS>(squares.x + squares.y, s_sum[turn]);
     turn ^= 1;
     float rstd;
     if (isfinite(sum)) {
@@ -134,7 +142,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxRowThreads) rms_norm(const __
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) wide += (double)f[v][j] * (double)f[v][j];
+        for (int k = 0; k < 4; ++k) wide += (double)f[v][k].x * (double)f[v][k].x + (double)f[v][k].y * (double)f[v][k].y;
       wide = row_sum_wide<WARP>(wide, s_wide);
       rstd = (float)(1.0 / sqrt(wide / (double)p.cols + (double)p.eps));
     }
@@ -142,10 +150,10 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxRowThreads) rms_norm(const __
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = at.template column<V, VEC>(v);
-      float w[8];
+      float2 w[4];
       gain.of(at, v, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[v][j] = f[v][j] * rstd * w[j];
+      for (int k = 0; k < 4; ++k) f[v][k] = __fmul2_rn(__fmul2_rn(f[v][k], both_of(rstd)), w[k]);
       if (p.y.data) Piece::store(static_cast<T*>(p.y.data) + row * p.y.ld + c, p.cols - c, f[v]);
       if (p.codes) store_codes<VEC>(p, row, c, f[v]);
     }
@@ -155,23 +163,32 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxRowThreads) rms_norm(const __
 
 namespace {
 
-template <typename T, int V, bool VEC, bool WARP>
+template <typename T, int V, bool VEC, int WARPS>
 int launch_one(const NormRows& p, cudaStream_t s) {
   const char* what = "rms_norm launch";
-  constexpr int kRows = RowShape<WARP>::kAtOnce;
-  const int threads = row_threads<V, WARP>(p.cols);
+  constexpr int kRows = RowShape<kWarpRows<WARPS>>::kAtOnce;
+  const int threads = row_threads<V, kWarpRows<WARPS>>(p.cols);
   int grid = 0;
-  if (int st = row_grid<rms_norm<T, V, VEC, WARP>>(threads, (p.rows + kRows - 1) / kRows, &grid, what)) return st;
-  return launch_row_kernel<rms_norm<T, V, VEC, WARP>>(p, grid, threads, s, what);
+  if (int st = row_grid<rms_norm<T, V, VEC, WARPS>>(threads, (p.rows + kRows - 1) / kRows, &grid, what)) return st;
+  return launch_row_kernel<rms_norm<T, V, VEC, WARPS>>(p, grid, threads, s, what);
 }
 static_assert(DOPT_NORM_MAX_COLS <= kMaxRowThreads * 4 * 8, "the longest row's kernel");
+// Eight columns per thread up to V = 4 times, in the fewest kernels that were
+// best somewhere: few threads with much each for 16-bit vectors (4096 bf16
+// columns to 8 bits: 59 us, with V = 2 67).
 template <typename T, bool VEC>
 int launch_length(const NormRows& p, cudaStream_t s) {
   const int c = p.cols;
-  if (c <= 256) return launch_one<T, 1, VEC, true>(p, s);
-  if (c <= 512) return launch_one<T, 2, VEC, true>(p, s);
-  if (c > 8192 || (VEC && sizeof(T) == 2 && c > 2048)) return launch_one<T, 4, VEC, false>(p, s);
-  return launch_one<T, 2, VEC, false>(p, s);
+  if (c <= 256) return launch_one<T, 1, VEC, 0>(p, s);
+  if (c <= 512) return launch_one<T, 2, VEC, 0>(p, s);
+  if constexpr (VEC && sizeof(T) == 2) {
+    if (c <= 2048) return launch_one<T, 2, VEC, 8>(p, s);
+    if (c <= 8192) return launch_one<T, 4, VEC, 8>(p, s);
+  } else {
+    if (c <= 4096) return launch_one<T, 2, VEC, 8>(p, s);
+    if (c <= 8192) return launch_one<T, 2, VEC, 16>(p, s);
+  }
+  return launch_one<T, 4, VEC, 16>(p, s);
 }
 template <typename T>
 int launch_norm(const NormRows& p, bool vec, cudaStream_t s) {

@@ -42,32 +42,33 @@ template <bool VEC>
 constexpr int kColumnStep = VEC ? 1 : 32;
 constexpr int kMaxRowThreads = 512;
 
+// Rows of at most WARPS warps each, 0: a warp has a row (WARP above).
+template <int WARPS>
+constexpr bool kWarpRows = WARPS == 0;
+
 // A sum over the threads that have a row.  The warps' sums lie in shared
 // memory, zeros for the warps that a CTA does not have, so that all of them
 // are read at once (a loop over the warps took a row 30 cycles for each).
-struct alignas(16) RowSums {
+struct RowSums {
   float of_warp[kMaxRowThreads / 32];
 };
-template <bool WARP>
+template <int WARPS>
 __device__ __forceinline__ void clear_sums(RowSums (&s)[2]) {
-  if constexpr (!WARP) {
+  if constexpr (WARPS > 0) {
     if (threadIdx.x < kMaxRowThreads / 32) s[0].of_warp[threadIdx.x] = s[1].of_warp[threadIdx.x] = 0.f;
     __syncthreads();
   }
 }
-template <bool WARP>
+template <int WARPS>
 __device__ __forceinline__ float row_sum(float x, RowSums& s) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-  if constexpr (!WARP) {
+  if constexpr (WARPS > 0) {
     if (threadIdx.x % 32 == 0) s.of_warp[threadIdx.x / 32] = x;
     __syncthreads();
-    float4 t[kMaxRowThreads / 128];
+    x = s.of_warp[0];
 #pragma unroll
-    for (int w = 0; w < kMaxRowThreads / 128; ++w) t[w] = reinterpret_cast<const float4*>(s.of_warp)[w];
-    x = 0.f;
-#pragma unroll
-    for (int w = 0; w < kMaxRowThreads / 128; ++w) x += (t[w].x + t[w].y) + (t[w].z + t[w].w);
+    for (int w = 1; w < WARPS; ++w) x += s.of_warp[w];
   }
   return x;
 }
@@ -80,14 +81,14 @@ struct RowGain {
   const void* gain;
   bool f32;
   int cols;
-  float kept[kKept ? V : 1][8];
+  float2 kept[kKept ? V : 1][4];
   __device__ __forceinline__ RowGain(const void* gain_, bool f32_, const RowShape<WARP>& at, int cols_)
       : gain(gain_), f32(f32_), cols(cols_) {
     if constexpr (kKept)
 #pragma unroll
       for (int v = 0; v < V; ++v) read(at, v, kept[v]);
   }
-  __device__ __forceinline__ void read(const RowShape<WARP>& at, int v, float (&out)[8]) const {
+  __device__ __forceinline__ void read(const RowShape<WARP>& at, int v, float2 (&out)[4]) const {
     if constexpr (VEC) {
       const int c = at.template column<V, VEC>(v);
       if (f32) {
@@ -99,25 +100,28 @@ struct RowGain {
         r.load(static_cast<const T*>(gain) + c, cols - c);
         r.widen8(out);
       }
-      return;
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = at.template column<V, VEC>(v) + j * kColumnStep<VEC>;
-      out[j] = c < cols ? (f32 ? __ldg(static_cast<const float*>(gain) + c) : widen<T>(static_cast<const T*>(gain)[c])) : 0.f;
+      for (int k = 0; k < 4; ++k) {
+        const int c = at.template column<V, VEC>(v) + 64 * k;
+        out[k] = make_float2(one(c), one(c + 32));
+      }
     }
   }
-  __device__ __forceinline__ void of(const RowShape<WARP>& at, int v, float (&out)[8]) const {
+  __device__ __forceinline__ float one(int c) const {
+    return c < cols ? (f32 ? __ldg(static_cast<const float*>(gain) + c) : widen<T>(static_cast<const T*>(gain)[c])) : 0.f;
+  }
+  __device__ __forceinline__ void of(const RowShape<WARP>& at, int v, float2 (&out)[4]) const {
     if constexpr (kKept) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) out[j] = kept[v][j];
+      for (int k = 0; k < 4; ++k) out[k] = kept[v][k];
     } else {
       read(at, v, out);
     }
   }
 };
 
-// Threads of a row of this length.
+// Threads of a CTA for rows of this length.
 template <int V, bool WARP>
 int row_threads(int32_t cols) {
   return WARP ? 256 : (cols + 256 * V - 1) / (256 * V) * 32;

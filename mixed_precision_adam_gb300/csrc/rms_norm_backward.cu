@@ -10,13 +10,24 @@ namespace dopt {
 template <typename T, int V>
 constexpr bool kBackAhead = V * sizeof(T) <= 4;
 
-template <typename T, int V, bool VEC, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : kMaxRowThreads) rms_norm_backward(const __grid_constant__ NormBackRows p) {
+// Threads and CTAs per SM that a kernel is compiled for: short rows of 16-bit
+// values in 80 registers, for three CTAs (2048 columns: 75 us against 85 with
+// one register more).
+template <typename T, int V, bool VEC, int WARPS>
+constexpr bool kShortRows = V == 1 && VEC && sizeof(T) == 2 && WARPS > 0;
+template <typename T, int V, bool VEC, int WARPS>
+constexpr int kRowBound = WARPS == 0 || kShortRows<T, V, VEC, WARPS> ? 256 : kMaxRowThreads;
+template <typename T, int V, bool VEC, int WARPS>
+constexpr int kRowCtas = V == 1 && VEC && sizeof(T) == 2 ? 3 : WARPS > 0 ? 1 : V == 1 || VEC ? 2 : 1;
+
+template <typename T, int V, bool VEC, int WARPS>
+__global__ void __launch_bounds__(kRowBound<T, V, VEC, WARPS>, kRowCtas<T, V, VEC, WARPS>) rms_norm_backward(const __grid_constant__ NormBackRows p) {
+  constexpr bool WARP = kWarpRows<WARPS>;
   __shared__ RowSums s_sum[2];
   __shared__ float s_gain[WARP ? 8 * 32 * 8 : 1];
   using Piece = Eight8<T, VEC>;
   const RowShape<WARP> at;
-  clear_sums<WARP>(s_sum);
+  clear_sums<WARPS>(s_sum);
   const uint32_t key = drop_key(p.drop);
   const T* h = static_cast<const T*>(p.h.data);
   const T* dy = static_cast<const T*>(p.dy.data);
@@ -37,14 +48,14 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxRowThreads) rms_norm_backward
   };
   if (row < p.rows) load(row);
   const RowGain<T, V, VEC, WARP, V <= 2> gain(p.gain, p.gain_f32, at, p.cols);
-  float acc[V][8];
+  float2 acc[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[v][j] = 0.f;
+    for (int k = 0; k < 4; ++k) acc[v][k] = make_float2(0.f, 0.f);
   int turn = 0;
   for (; row < p.rows; row += stride) {
-    float hat[V][8], d[V][8], dot = 0.f;
+    float2 hat[V][4], d[V][4], dots = make_float2(0.f, 0.f);
     const float r0 = rstd;
     Piece res[V];
 #pragma unroll
@@ -56,29 +67,30 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxRowThreads) rms_norm_backward
     if (kBackAhead<T, V> && row + stride < p.rows) load(row + stride);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float w[8];
+      float2 w[4];
       gain.of(at, v, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        hat[v][j] *= r0;
-        acc[v][j] = fmaf(d[v][j], hat[v][j], acc[v][j]);
-        d[v][j] *= w[j];
-        dot = fmaf(d[v][j], hat[v][j], dot);
+      for (int k = 0; k < 4; ++k) {
+        hat[v][k] = __fmul2_rn(hat[v][k], both_of(r0));
+        acc[v][k] = __ffma2_rn(d[v][k], hat[v][k], acc[v][k]);
+        d[v][k] = __fmul2_rn(d[v][k], w[k]);
+        dots = __ffma2_rn(d[v][k], hat[v][k], dots);
       }
     }
-    dot = row_sum<WARP>(dot, s_sum[turn]) / (float)p.cols;
+    const float mean = row_sum<WARPS>(dots.x + dots.y, s_sum[turn]) / (float)p.cols;
     turn ^= 1;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = at.template column<V, VEC>(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[v][j] = r0 * fmaf(-hat[v][j], dot, d[v][j]);
+      for (int k = 0; k < 4; ++k)
+        d[v][k] = __fmul2_rn(__ffma2_rn(hat[v][k], both_of(-mean), d[v][k]), both_of(r0));
       if (dres) {
-        float r[8];
+        float2 r[4];
         if (!kBackAhead<T, V>) res[v].load(dres + row * p.dres.ld + c, p.cols - c);
         res[v].widen8(r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[v][j] += r[j];
+        for (int k = 0; k < 4; ++k) d[v][k] = __fadd2_rn(d[v][k], r[k]);
       }
       if (p.dh.data) Piece::store(static_cast<T*>(p.dh.data) + row * p.dh.ld + c, p.cols - c, d[v]);
       if (p.dx.data) {
@@ -98,7 +110,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxRowThreads) rms_norm_backward
       // the warps' sums of these columns, in the warps' order
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s_gain[(threadIdx.x / 32 * 8 + j) * 32 + at.g] = acc[v][j];
+      for (int j = 0; j < 8; ++j) s_gain[(threadIdx.x / 32 * 8 + j) * 32 + at.g] = j & 1 ? acc[v][j / 2].y : acc[v][j / 2].x;
       __syncthreads();
       const int j = threadIdx.x / 32, col = c + j * kColumnStep<VEC>;
       float sum = 0.f;
@@ -109,7 +121,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxRowThreads) rms_norm_backward
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int col = c + j * kColumnStep<VEC>;
-        if (col < p.cols) part[col] = acc[v][j];
+        if (col < p.cols) part[col] = j & 1 ? acc[v][j / 2].y : acc[v][j / 2].x;
       }
     }
   }
@@ -160,22 +172,28 @@ int64_t parts_asked(const NormBackRows& p, int rows_at_once) {
   return std::min<int64_t>({all, std::max<int64_t>(few, p.rows / 32), max_parts(p.cols)});
 }
 
-template <typename T, int V, bool VEC, bool WARP>
+template <typename T, int V, bool VEC, int WARPS>
 int launch_one(const NormBackRows& p, cudaStream_t s, int* parts) {
   const char* what = "rms_norm_backward launch";
-  constexpr int kRows = RowShape<WARP>::kAtOnce;
-  const int threads = row_threads<V, WARP>(p.cols);
-  if (int st = row_grid<rms_norm_backward<T, V, VEC, WARP>>(threads, parts_asked(p, kRows), parts, what)) return st;
-  return launch_row_kernel<rms_norm_backward<T, V, VEC, WARP>>(p, *parts, threads, s, what);
+  constexpr int kRows = RowShape<kWarpRows<WARPS>>::kAtOnce;
+  const int threads = row_threads<V, kWarpRows<WARPS>>(p.cols);
+  if (int st = row_grid<rms_norm_backward<T, V, VEC, WARPS>>(threads, parts_asked(p, kRows), parts, what)) return st;
+  return launch_row_kernel<rms_norm_backward<T, V, VEC, WARPS>>(p, *parts, threads, s, what);
 }
 template <typename T, bool VEC>
 int launch_length(const NormBackRows& p, cudaStream_t s, int* parts) {
   const int c = p.cols;
-  if (c <= 256) return launch_one<T, 1, VEC, true>(p, s, parts);
-  if (c <= 512) return launch_one<T, 2, VEC, true>(p, s, parts);
-  if (c <= (sizeof(T) == 2 ? 2048 : 4096)) return launch_one<T, 1, VEC, false>(p, s, parts);
-  if (c <= 8192) return launch_one<T, 2, VEC, false>(p, s, parts);
-  return launch_one<T, 4, VEC, false>(p, s, parts);
+  if (c <= 256) return launch_one<T, 1, VEC, 0>(p, s, parts);
+  if (c <= 512) return launch_one<T, 2, VEC, 0>(p, s, parts);
+  if (c <= 2048) return launch_one<T, 1, VEC, 8>(p, s, parts);
+  if (c <= 4096) {
+    if constexpr (sizeof(T) == 2)
+      return launch_one<T, 2, VEC, 8>(p, s, parts);
+    else
+      return launch_one<T, 1, VEC, 16>(p, s, parts);
+  }
+  if (c <= 8192) return launch_one<T, 2, VEC, 16>(p, s, parts);
+  return launch_one<T, 4, VEC, 16>(p, s, parts);
 }
 
 }  // namespace
