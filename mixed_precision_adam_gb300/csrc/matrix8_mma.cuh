@@ -58,6 +58,11 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t at, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(at), "r"(rank));
   return out;
 }
+__device__ __forceinline__ float4 cluster_load(uint32_t at) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at) : "memory");
+  return x;
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -259,6 +264,26 @@ __device__ __forceinline__ void store_column(const MulParams& p, const uint32_t 
     store_sums(r, static_cast<__nv_bfloat16*>(p.d) + at, p.ldd, count, p.accumulate);
   else
     store_sums(r, static_cast<__half*>(p.d) + at, p.ldd, count, p.accumulate);
+}
+
+// Four consecutive columns n of a row m of d, those that are there.
+template <typename T>
+__device__ __forceinline__ void store_four(const MulParams& p, float4 x, int64_t n, int64_t m) {
+  T* d = static_cast<T*>(p.d) + m * p.ldd + n;
+  const int count = (int)min((int64_t)4, p.n - n);
+  const float f[4] = {x.x, x.y, x.z, x.w};
+  if (!p.accumulate && count == 4 && (reinterpret_cast<uintptr_t>(d) & (4 * sizeof(T) - 1)) == 0) {
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float4*>(d) = x;
+    else
+      *reinterpret_cast<uint2*>(d) = make_uint2(narrow_pair<T>(make_float2(x.x, x.y)), narrow_pair<T>(make_float2(x.z, x.w)));
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t one[1] = {__float_as_uint(f[j])};
+    if (j < count) store_sums(one, d + j, p.ldd, 1, p.accumulate);
+  }
 }
 
 // The matrix unit's sums in fp32 do not round to nearest: over a long k they

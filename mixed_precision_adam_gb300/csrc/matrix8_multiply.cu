@@ -167,39 +167,38 @@ __global__ void __launch_bounds__(kMulThreads, BT <= 64 ? 2 : 1) matrix8_multipl
         for (int c = 0; c < kColumns; ++c) r[c] = 0x7FC00000u;
       }
       if constexpr (SPLIT) {
-        // each CTA of the cluster sums a share of the tile's columns: every
-        // one sends it its own part, through shared memory that no copy and
-        // no product uses any more
+        // a CTA leaves its sums in its own shared memory, which no copy and no
+        // product uses any more; then each of the cluster adds up a share of
+        // the tile's columns, in the CTAs' order
+        float* mine = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
+#pragma unroll
+        for (int c = 0; c < kColumns; ++c) mine[(half * kColumns + c) * 128] = __uint_as_float(r[c]);
         cluster_sync();
-        const int share = 1 << p.share_log;
-        const uint32_t mine = smem_addr(smem) + (uint32_t)(quarter * 32 + lane) * 4u;
+        const int share = 1 << p.share_log, ctas = 1 << p.split_log;
+        for (int c = warp - 4; c < share; c += 8) {
+          const int64_t row = (int64_t)tile.m * BT + rank * share + c, n = (int64_t)tile.n * kTileN + lane * 4;
+          if (row >= p.m) break;
+          const uint32_t at = smem_addr(smem) + (uint32_t)(rank * share + c) * 512u + (uint32_t)lane * 16u;
+          float4 sum = cluster_load(cluster_addr(at, 0));
 #pragma unroll
-        for (int c = 0; c < kColumns; ++c) {
-          const int col = half * kColumns + c, to = col >> p.share_log, at = rank * share + (col & (share - 1));
-          const uint32_t remote = cluster_addr(mine + (uint32_t)at * 512u, to);
-          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(r[c]) : "memory");
-        }
-        cluster_sync();
-        // every other column of the share is this thread's, four at a time
-        const float* part = reinterpret_cast<const float*>(smem) + (threadIdx.x - 128) % 128;
-        const int64_t n = (int64_t)tile.n * kTileN + (threadIdx.x - 128) % 128, m0 = (int64_t)tile.m * BT + rank * share;
-        for (int c0 = (threadIdx.x - 128) / 128; c0 < share; c0 += 8) {
-          float x[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = c0 + 2 * j < share ? part[(c0 + 2 * j) * 128] : 0.f;
-#pragma unroll
-          for (int q = 1; q < 8; ++q) {
-            if (q >> p.split_log) break;
+          for (int q0 = 1; q0 < 8; q0 += 4) {
+            float4 x[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              if (c0 + 2 * j < share) x[j] += part[(q * share + c0 + 2 * j) * 128];
-          }
+              if (q0 + j < ctas) x[j] = cluster_load(cluster_addr(at, q0 + j));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t one[1] = {__float_as_uint(x[j])};
-            if (c0 + 2 * j < share && m0 + c0 + 2 * j < p.m) store_column(p, one, n, m0 + c0 + 2 * j);
+            for (int j = 0; j < 4; ++j)
+              if (q0 + j < ctas) sum = make_float4(sum.x + x[j].x, sum.y + x[j].y, sum.z + x[j].z, sum.w + x[j].w);
           }
+          if (n >= p.n) continue;
+          if (p.dtype == DOPT_F32)
+            store_four<float>(p, sum, n, row);
+          else if (p.dtype == DOPT_BF16)
+            store_four<__nv_bfloat16>(p, sum, n, row);
+          else
+            store_four<__half>(p, sum, n, row);
         }
+        cluster_sync();  // the others have read what lies here
       } else {
         store_column(p, r, (int64_t)tile.n * kTileN + quarter * 32 + lane, (int64_t)tile.m * BT + half * kColumns);
       }
@@ -300,21 +299,46 @@ int launch_multiply(MulParams& p, const dopt_matrix8& a, const dopt_matrix8& b, 
   return check_launch(what);
 }
 
+// What a product takes, in units of 10 ns, by fits to 3 x 11 x 4 sizes of k, m
+// and n (bf16, weights not in L2): a launch, and for each wave of tiles its
+// steps along k and its start and end.
+struct Plan {
+  int64_t cost;
+  int split_log;
+};
+int64_t waves_of(int64_t tiles, int64_t at_once) { return (tiles + at_once - 1) / at_once; }
+int64_t pair_cost(int64_t m, int64_t n, int64_t blocks, int sms) {
+  return 650 + waves_of((m + 255) / 256 * ((n + 255) / 256), sms / 2) * (blocks * 26 + 200);
+}
+// Tiles of one SM, their k split over a cluster of CTAs where that leaves
+// none of them to a second wave and is worth its exchange: 128 x 2048 x 4096
+// takes 7.9 us split in four and 10.2 whole, 128 x 2048 x 1024 7.5 and 5.4.
+// Clusters of eight need eight free SMs of one GPC each, so they are left to
+// few tiles (128 x 2048 x 4096 in eight: 12.9 us).
+Plan one_sm_plan(int bt, int64_t tiles, int64_t blocks, int64_t groups, int sms) {
+  const int64_t slots = sms * (bt <= 64 ? 2 : 1);
+  static const int exchange[2][4] = {{0, 120, 140, 150}, {0, 270, 270, 270}};
+  Plan best{410 + waves_of(tiles, slots) * (blocks * 19 + 100), 0};
+  for (int s = 1; s <= 3; ++s) {
+    const int64_t ctas = tiles << s;
+    if (ctas > (s < 3 ? slots : bt <= 64 ? sms : sms / 2) || groups < (1 << s)) break;
+    const int64_t cost = 510 + (blocks * 19 >> s) + exchange[bt > 32][s];
+    if (cost < best.cost) best = Plan{cost, s};
+  }
+  return best;
+}
+
 template <int BT>
-int multiply_rows(MulParams& p, const dopt_matrix8& a, const dopt_matrix8& b, cudaStream_t s) {
+int multiply_rows(MulParams& p, const dopt_matrix8& a, const dopt_matrix8& b, int sms, cudaStream_t s) {
   p.tiles_m = (int32_t)((a.rows + BT - 1) / BT);
   p.tiles_n = (int32_t)((b.rows + kTileN - 1) / kTileN);
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   if (tiles > INT32_MAX / 8) return fail(DOPT_E_SIZE, "dopt_matrix8_multiply: too many elements in d");
   p.n_tiles = (int32_t)tiles;
-  p.split_log = p.share_log = 0;
-  int sms = 0;
-  if (int st = device_sms(&sms)) return st;
-  const int slots = sms * (BT <= 64 ? 2 : 1);
-  while (p.split_log < 3 && (2 << p.split_log) <= p.groups && (tiles << p.split_log) * 2 <= slots) ++p.split_log;
+  p.split_log = one_sm_plan(BT, tiles, p.blocks, p.groups, sms).split_log;
+  p.share_log = 0;
   while ((1 << p.split_log << p.share_log) < BT) ++p.share_log;
-  if (p.split_log) return launch_multiply<BT, true>(p, a, b, s);
-  return launch_multiply<BT, false>(p, a, b, s);
+  return p.split_log ? launch_multiply<BT, true>(p, a, b, s) : launch_multiply<BT, false>(p, a, b, s);
 }
 
 }  // namespace
@@ -357,14 +381,15 @@ extern "C" int dopt_matrix8_multiply(const dopt_matrix8* a, const dopt_matrix8* 
     p.part = d_dtype == DOPT_F32 ? kPart : p.blocks;
     p.dtype = d_dtype;
     p.accumulate = accumulate ? 1 : 0;
-    const int64_t m = a->rows;
-    if (m <= 16) return multiply_rows<16>(p, *a, *b, s);
-    if (m <= 32) return multiply_rows<32>(p, *a, *b, s);
-    if (m <= 64) return multiply_rows<64>(p, *a, *b, s);
+    const int64_t m = a->rows, n = b->rows;
     int sms = 0;
     if ((st = device_sms(&sms))) return st;
-    const int64_t pairs = (m + 255) / 256 * ((b->rows + 255) / 256);
-    if (m > 128 && pairs >= sms / 2) return launch_multiply_pair(p, *a, *b, s);
-    return multiply_rows<128>(p, *a, *b, s);
+    if (m <= 16) return multiply_rows<16>(p, *a, *b, sms, s);
+    if (m <= 32) return multiply_rows<32>(p, *a, *b, sms, s);
+    if (m <= 64) return multiply_rows<64>(p, *a, *b, sms, s);
+    const int64_t tiles = (m + 127) / 128 * ((n + kTileN - 1) / kTileN);
+    if (m > 128 && pair_cost(m, n, p.blocks, sms) < one_sm_plan(128, tiles, p.blocks, p.groups, sms).cost)
+      return launch_multiply_pair(p, *a, *b, s);
+    return multiply_rows<128>(p, *a, *b, sms, s);
   });
 }
