@@ -825,7 +825,7 @@ typedef enum {
   DOPT_BLOCK_SQUARE = 1 /* a scale per 128 x 128 square                      */
 } dopt_block;
 
-/* Scale bytes of a rows x cols matrix; DOPT_E_INVALID for a negative size,
+/* Scale bytes of a rows x cols matrix: ceil(rows / 128) * ceil(nb / 4) * 512; DOPT_E_INVALID for a negative size,
  * DOPT_E_SIZE from 2^31 on. */
 int64_t dopt_matrix8_scale_bytes(int64_t rows, int64_t cols);
 
@@ -854,9 +854,11 @@ int dopt_matrix8_unpack(const dopt_matrix_values* matrices, int32_t n_matrices, 
  * features); with the packed transposes, the two products of the backward
  * pass: grads x weight^T's rows, and grads^T x activations^T, which adds to
  * the fp32 grad that the step reads.
- * Products of codes are exact, summed in fp32 in the matrix unit in an order
- * that is fixed for given sizes, and rounded once to d_dtype (with the old d
- * added in fp32 before).  A term below fp32's normal range may count as 0.
+ * Products of codes are exact, summed in fp32 in the matrix unit (for fp32
+ * results over 4096 of k at most, then in fp32 rounded to nearest) in an
+ * order that is fixed for given sizes on the same kind of GPU, and rounded
+ * once to d_dtype (with the old d added in fp32 before).  What lies below
+ * fp32's normal range may count as 0.
  * A block that reads as NaN makes its row of d (of a) or column (of b) NaN.
  * With cols 0 the sums are 0.  d is aligned to its elements only, must not
  * overlap a or b, and nothing but its rows x b.rows elements is written.
@@ -915,7 +917,8 @@ typedef struct {
  * dropout, when it is x.  Element i of the dropout is row * cols + column.
  * Squares are added in fp32 in a fixed order; a row whose sum of squares
  * leaves fp32's range is summed again in fp64.
- * h and y may be x or residual (the same rows).  cols <= DOPT_NORM_MAX_COLS.
+ * h and y may be x or residual (the same rows), each another one.
+ * cols <= DOPT_NORM_MAX_COLS.
  */
 typedef struct {
   int64_t rows, cols;
@@ -970,9 +973,10 @@ int dopt_debug_starve_copy(int32_t tile);
 #endif
 
 /* Debug builds only (compiled with DOPT_BOUNDS_CHECK=1; the default build
- * returns DOPT_E_INVALID).  Every kernel of such a build checks each tile's
- * element ranges against the extents of the buffers it reads and writes
- * (each replica, the main grad, master/m/v, the param buffer, the grad-check
+ * returns DOPT_E_INVALID).  Every kernel of the steps in such a build, and
+ * the packing and unpacking of 8-bit matrices, checks each tile's element
+ * ranges against the extents of the buffers it reads and writes (each
+ * replica, the main grad, master/m/v, the param buffer, the grad-check
  * slots) and skips a tile that falls outside them instead of touching it.
  * This call copies the record of such tiles on the current device to out[4]
  * -- the number of failed checks, the first failure's check site, first

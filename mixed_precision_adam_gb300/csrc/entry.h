@@ -15,6 +15,14 @@ inline size_t dtype_bytes(int32_t dtype) { return dtype == DOPT_F32 ? 4 : 2; }
 inline bool known_dtype(int32_t dtype) { return dtype == DOPT_F32 || dtype == DOPT_BF16 || dtype == DOPT_F16; }
 
 constexpr int64_t kMaxSide = int64_t(1) << 31;  // rows and columns stay below it
+constexpr int64_t kMaxLd = int64_t(1) << 40;    // elements from row to row, so that byte distances fit 64 bits
+
+// The distance of rows of values.
+inline int check_ld(int64_t ld, int64_t cols, const std::string& who) {
+  if (ld < cols) return fail(DOPT_E_INVALID, who + "ld below cols");
+  if (ld > kMaxLd) return fail(DOPT_E_SIZE, who + "ld too large");
+  return DOPT_OK;
+}
 
 // Sizes of a matrix.
 inline int check_sides(int64_t rows, int64_t cols, const std::string& who) {

@@ -389,7 +389,7 @@ int check_matrices(const dopt_matrix_values* ms, int32_t n, bool pack, const cha
     if (!m.values) return fail(DOPT_E_INVALID, who + "NULL values");
     if (!aligned_to(m.values, dtype_bytes(m.values_dtype)))
       return fail(DOPT_E_ALIGN, who + "values not aligned to their elements");
-    if (m.ld < m.cols) return fail(DOPT_E_INVALID, who + "ld below cols");
+    if ((st = check_ld(m.ld, m.cols, who))) return st;
     if (!m.out.codes && !(pack && m.out_t.codes)) return fail(DOPT_E_INVALID, who + "NULL codes");
     if (m.out.codes) {
       if (m.out.rows != m.rows || m.out.cols != m.cols) return fail(DOPT_E_INVALID, who + "out has another size");

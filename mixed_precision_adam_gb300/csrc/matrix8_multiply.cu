@@ -360,7 +360,7 @@ extern "C" int dopt_matrix8_multiply(const dopt_matrix8* a, const dopt_matrix8* 
     const size_t elem = dtype_bytes(d_dtype);
     if (!d) return fail(DOPT_E_INVALID, fn + "NULL d");
     if (!aligned_to(d, elem)) return fail(DOPT_E_ALIGN, fn + "d not aligned to its elements");
-    if (ldd < b->rows) return fail(DOPT_E_INVALID, fn + "ldd below b's rows");
+    if ((st = check_ld(ldd, b->rows, fn + "d: "))) return st;
     const cudaStream_t s = (cudaStream_t)stream;
     if (a->cols == 0) {
       if (accumulate) return DOPT_OK;
@@ -376,7 +376,7 @@ extern "C" int dopt_matrix8_multiply(const dopt_matrix8* a, const dopt_matrix8* 
     p.n = (int32_t)b->rows;
     p.blocks = (int32_t)row_blocks(a->cols);
     p.groups = (int32_t)scale_groups(a->cols);
-    if (scale_size(std::max(a->rows, b->rows), a->cols) / 512 > INT32_MAX - 1)
+    if (scale_size(std::max(a->rows, b->rows), a->cols) / 512 > INT32_MAX / 2)
       return fail(DOPT_E_SIZE, fn + "too many elements");
     p.part = d_dtype == DOPT_F32 ? kPart : p.blocks;
     p.dtype = d_dtype;

@@ -197,8 +197,7 @@ int launch_norm(const NormRows& p, bool vec, cudaStream_t s) {
 
 int check_rows(const dopt_rows& r, int64_t cols, size_t elem, const char* name, const std::string& fn) {
   if (!aligned_to(r.data, elem)) return fail(DOPT_E_ALIGN, fn + name + " not aligned to its elements");
-  if (r.data && r.ld < cols) return fail(DOPT_E_INVALID, fn + name + ": ld below cols");
-  return DOPT_OK;
+  return r.data ? check_ld(r.ld, cols, fn + name + ": ") : DOPT_OK;
 }
 
 int check_norm(int64_t rows, int64_t cols, int32_t dtype, int32_t gain_dtype, const void* gain, const std::string& fn) {

@@ -11,6 +11,9 @@ from . import tensors as T
 BLOCK = 128
 U = T.U
 EPS = {"f32": 2.0**-24, "bf16": 2.0**-8, "f16": 2.0**-11}  # half a step, relative
+# From here on nearest rounding gives infinity: half a step past the largest value, (2 - 2^-11) 2^15 of fp16's 11 bits,
+# (2 - 2^-8) 2^127 of bf16's 8, (2 - 2^-24) 2^127 of fp32's 24.
+OVER = {"f32": (2 - 2.0**-24) * 2.0**127, "bf16": (2 - 2.0**-8) * 2.0**127, "f16": (2 - 2.0**-11) * 2.0**15}
 TINY = {"f32": 2.0**-150, "bf16": 2.0**-134, "f16": 2.0**-25}  # half of the smallest value
 
 
@@ -27,11 +30,8 @@ def scale_size(rows, cols):
 def scale_places(rows, cols):
     """Place of the byte of each row and block."""
     groups = -(-blocks_of(cols) // 4)
-    out = np.empty((rows, blocks_of(cols)), np.int64)
-    for r in range(rows):
-        for b in range(blocks_of(cols)):
-            out[r, b] = ((r // 128) * groups + b // 4) * 512 + (r % 32) * 16 + (r % 128 // 32) * 4 + b % 4
-    return out
+    r, b = np.arange(rows)[:, None], np.arange(blocks_of(cols))[None]
+    return ((r // 128) * groups + b // 4) * 512 + (r % 32) * 16 + (r % 128 // 32) * 4 + b % 4
 
 
 def tops(x, square=False):
@@ -161,4 +161,6 @@ def near(got, want, bound, dtype):
     got, want = np.asarray(got, np.float64), np.asarray(want, np.float64)
     with np.errstate(invalid="ignore"):
         tol = bound + (np.abs(want) + bound) * EPS[dtype] + TINY[dtype]
-        return (np.abs(got - want) <= tol) | (np.isnan(got) & np.isnan(want)) | (got == want)
+        close = (np.abs(got - want) <= tol) & (np.abs(want) - bound < OVER[dtype])
+        over = np.isinf(got) & (np.sign(got) == np.sign(want)) & (np.abs(want) + bound >= OVER[dtype])
+        return close | over | (np.isnan(got) & np.isnan(want)) | (got == want)

@@ -158,12 +158,32 @@ def test_product_many_tiles(m, n, k):
     check_product(m, n, k, "bf16")
 
 
+# Tiles of two SMs are for products whose tiles fill the SMs that way and whose k is long: one tile for each pair of
+# them, and several.
+PAIRS = [(1000, 3900, 3100), (2300, 4300, 5000)]
+
+
 @pytest.mark.parametrize("m,n,k", [(40, 300, 4096), (40, 300, 20000), (100, 300, 40000), (1500, 1000, 4096), (1500, 1000, 4300),
-                                   (2500, 2300, 4097), (2500, 2300, 8500)])
+                                   (2500, 2300, 4097)] + PAIRS)
 @pytest.mark.parametrize("dtype,add", [("f32", False), ("f32", True), ("bf16", False)])
 def test_product_long_sums(m, n, k, dtype, add):
     """Sums that are added up in parts, in every kernel: one tile's, a cluster's and a pair's."""
     check_product(m, n, k, dtype, add=add)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_product_of_pairs_added(dtype):
+    """Tiles of two SMs added to what is there, odd rows of d."""
+    check_product(*PAIRS[0], dtype, add=True, pad=3, offset=1)
+
+
+@pytest.mark.parametrize("m", [50, 300])
+def test_product_with_itself(m):
+    a = Codes(m, 900)
+    av = a.fill(numbers(m, 900, m))
+    want, bound = O.product(av, av)
+    got = multiply(a, a, "f32")
+    assert O.near(got, want, bound, "f32").all()
 
 
 @pytest.mark.parametrize("m", [3, 30, 60, 100])
@@ -172,10 +192,10 @@ def test_product_more_tiles_than_fit(m):
     check_product(m, 39000, 200, "bf16")
 
 
-@pytest.mark.parametrize("m", [7, 100, 300])
-def test_product_is_exact_on_small_integers(m):
+@pytest.mark.parametrize("m,n", [(7, 200), (100, 200), (300, 200), (1000, 3900)])
+def test_product_is_exact_on_small_integers(m, n):
     """Whole numbers whose sums fit 24 bits: every product and sum is exact, in any order, in fp32."""
-    n, k = 200, 4096
+    k = 4096
     rng = np.random.default_rng(m)
     a, b = Codes(m, k), Codes(n, k)
     av, bv = rng.integers(-15, 16, (m, k)).astype(float), rng.integers(-15, 16, (n, k)).astype(float)
@@ -202,10 +222,9 @@ def test_product_scales_of_every_block():
     assert O.near(multiply(a, b, "f32"), want, bound, "f32").all()
 
 
-@pytest.mark.parametrize("m", [20, 200, 1000])
-def test_product_nan_blocks(m):
+@pytest.mark.parametrize("m,n,k", [(20, 300, 700), (200, 300, 700), (1000, 300, 700), PAIRS[0]])
+def test_product_nan_blocks(m, n, k):
     """A block that reads as NaN makes its row (of a) or column (of b) NaN, and nothing else."""
-    n, k = 300, 700
     a, b = Codes(m, k), Codes(n, k)
     av, bv = a.fill(numbers(m, k, 1)), b.fill(numbers(n, k, 2))
     sa, sb = a.scale_bytes(), b.scale_bytes()
@@ -279,10 +298,10 @@ def test_far_rows(m):
 def test_two_products_at_once():
     """On two streams, with nothing between them."""
     cases = []
-    for k, m in enumerate((60, 300)):
-        a, b = Codes(m, 3000), Codes(500, 3000)
-        want = O.product(a.fill(numbers(m, 3000, k)), b.fill(numbers(500, 3000, k + 5)))
-        cases.append((a, b, torch.zeros(m, 500, device="cuda"), want, torch.cuda.Stream()))
+    for j, (m, n, k) in enumerate([(60, 500, 3000), (300, 500, 3000), PAIRS[0]]):
+        a, b = Codes(m, k), Codes(n, k)
+        want = O.product(a.fill(numbers(m, k, j)), b.fill(numbers(n, k, j + 5)))
+        cases.append((a, b, torch.zeros(m, n, device="cuda"), want, torch.cuda.Stream()))
     torch.cuda.synchronize()
     for _ in range(20):
         for a, b, d, _, s in cases:
@@ -292,11 +311,11 @@ def test_two_products_at_once():
         assert O.near(d.double().cpu().numpy(), want, bound, "f32").all()
 
 
-@pytest.mark.parametrize("m", [40, 400])
-def test_product_is_the_same_every_time(m):
-    a, b = Codes(m, 5000), Codes(700, 5000)
-    a.fill(numbers(m, 5000, 1))
-    b.fill(numbers(700, 5000, 2))
+@pytest.mark.parametrize("m,n,k", [(40, 700, 5000), (400, 700, 5000), PAIRS[0]])
+def test_product_is_the_same_every_time(m, n, k):
+    a, b = Codes(m, k), Codes(n, k)
+    a.fill(numbers(m, k, 1))
+    b.fill(numbers(n, k, 2))
     first = multiply(a, b, "f32")
     for _ in range(5):
         assert np.array_equal(multiply(a, b, "f32"), first)

@@ -87,6 +87,9 @@ def test_refused_products():
     refused(dopt.E_INVALID, multiply(a, b, d=None))
     refused(dopt.E_INVALID, multiply(a, b, dtype=3))
     refused(dopt.E_INVALID, multiply(a, b, ldd=49))
+    refused(dopt.E_SIZE, multiply(a, b, ldd=2**41))
+    big = dict(rows=2**31 - 1, cols=2**31 - 1, ld=2**31)
+    refused(dopt.E_SIZE, multiply(matrix(**big), matrix(**dict(big, rows=1))))
     refused(dopt.E_ALIGN, multiply(a, b, d=(1 << 20) + 2))
     refused(dopt.E_ALIGN, multiply(a, b, d=(1 << 20) + 1, dtype=1))
     fn = dopt._c["dopt_matrix8_multiply"]
@@ -124,6 +127,7 @@ def test_refused_packs():
     call(values(out_t=matrix(300, 40, 48)), ("dopt_matrix8_unpack",))  # there is nothing to unpack
     call(values(at=(1 << 20) + 2, out=matrix()), status=dopt.E_ALIGN)
     call(values(rows=2**31, out=matrix()), status=dopt.E_SIZE)
+    call(values(ld=2**41, out=matrix()), status=dopt.E_SIZE)
     big = matrix(rows=2**31 - 1, cols=2**31 - 1, ld=2**31)
     call(values(rows=2**31 - 1, cols=2**31 - 1, ld=2**31, out=big), status=dopt.E_SIZE)
     for fn in ("dopt_matrix8_pack", "dopt_matrix8_unpack"):
@@ -167,7 +171,7 @@ def norm_args(**kw):
 @pytest.mark.parametrize("change,status", BAD_DROPS + [
     (dict(rows=-1), "E_INVALID"), (dict(cols=-1), "E_INVALID"), (dict(cols=16385), "E_SIZE"), (dict(rows=2**31), "E_SIZE"),
     (dict(dtype=3), "E_INVALID"), (dict(gain_dtype=2), "E_INVALID"), (dict(x=None), "E_INVALID"), (dict(y=None), "E_INVALID"),
-    (dict(gain=None), "E_INVALID"), (dict(gain=16386), "E_ALIGN"), (dict(x=4097), "E_ALIGN"), (dict(ld=299), "E_INVALID"),
+    (dict(gain=None), "E_INVALID"), (dict(gain=16386), "E_ALIGN"), (dict(x=4097), "E_ALIGN"), (dict(ld=299), "E_INVALID"), (dict(ld=2**41), "E_SIZE"),
     (dict(residual=64), "E_INVALID"), (dict(p=0.1), "E_INVALID"),                       # h has nowhere to go
     (dict(eps=-1.0), "E_INVALID"), (dict(eps=float("inf")), "E_INVALID"), (dict(eps=float("nan")), "E_INVALID"),
     (dict(rstd=2), "E_ALIGN"), (dict(y8=matrix(5, 300)), "E_INVALID"), (dict(y8=matrix(4, 299)), "E_INVALID"),
@@ -269,6 +273,23 @@ def test_rounding_is_to_the_nearest_value():
             v = np.concatenate([O.T.E4M3[:127], -O.T.E4M3[:127]]) * 2.0 ** (int(s[r, c // 128]) - 127)
             assert abs(got[r, c] - x[r, c]) == np.abs(v - x[r, c]).min()
     assert np.array_equal(O.scales(np.tile(x, (50, 1)), True)[:128], np.tile(O.scales(x).max(0), (128, 1)))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_near_is_nearest_rounding(dtype):
+    """Every value of a type is near what rounds to it, infinity too, and its neighbour's is not."""
+    t = dict(f32=torch.float32, bf16=torch.bfloat16, f16=torch.float16)[dtype]
+    x = np.concatenate([np.geomspace(1e-9, 6e4, 5000), O.OVER[dtype] * np.array([0.999, 1 - 2.0**-20, 1, 1.5])])
+    with np.errstate(over="ignore"):
+        x = x.astype(np.float32).astype(np.float64)  # torch narrows by way of fp32
+    got = torch.from_numpy(x).to(t).double().numpy()
+    if dtype == "f32":
+        got[-3] = x[-3] = torch.finfo(t).max
+    assert np.isinf(got[-2:]).all() and np.isfinite(got[-4:-2]).all()
+    assert O.near(got, x, 0.0, dtype).all() and O.near(-got, -x, 0.0, dtype).all()
+    assert not O.near(-got, x, 0.0, dtype)[2000:].any()  # below that fp16 has subnormal numbers
+    assert not O.near(got * (1 + 3 * O.EPS[dtype]), x, 0.0, dtype)[2000:-4].any()
+    assert not O.near(np.full(2, torch.finfo(t).max), x[-2:], 0.0, dtype).any()
 
 
 def test_random_numbers_are_the_steps():
