@@ -37,15 +37,17 @@ inline bool eight_vectors(const void* p, int64_t ld, size_t elem) {
 // Eight elements of a row as a load leaves them, widened only when they are
 // used, so that a thread's loads are all under way before the first wait;
 // then four pairs, for instructions on two fp32 numbers.
-// VEC: consecutive elements in one access (two for fp32); else every 32nd,
-// so that a warp's accesses are consecutive.
+// VEC: consecutive elements in one streaming access (two for fp32); else every
+// 32nd, so that a warp's accesses are consecutive, and not streaming: they
+// share sectors with the next ones (509 bf16 columns to values 90 us against
+// 81 so).
 template <typename T, bool VEC>
 struct Eight8 {
   T e[8];
   // of the elements at p, p + 32, ... those before `n`, zeros after them
   __device__ __forceinline__ void load(const T* p, int n) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = 32 * j < n ? __ldcs(p + 32 * j) : narrow<T>(0.f);
+    for (int j = 0; j < 8; ++j) e[j] = 32 * j < n ? p[32 * j] : narrow<T>(0.f);
   }
   __device__ __forceinline__ void widen8(float2 (&f)[4]) const {
 #pragma unroll
@@ -54,7 +56,7 @@ struct Eight8 {
   static __device__ __forceinline__ void store(T* p, int n, const float2 (&f)[4]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (32 * j < n) __stcs(p + 32 * j, narrow<T>(j & 1 ? f[j / 2].y : f[j / 2].x));
+      if (32 * j < n) p[32 * j] = narrow<T>(j & 1 ? f[j / 2].y : f[j / 2].x);
   }
 };
 template <>
