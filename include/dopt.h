@@ -938,8 +938,8 @@ int dopt_rms_norm(const dopt_rms_norm_args* args, dopt_stream stream);
  * Its backward pass from h and rstd, with g = dy * gain and hat = h * rstd:
  *   dh = rstd * (g - hat * mean(g * hat)) + dres,
  * the gradient of the residual (dres: what h's other use gave, or NULL);
- * dx = dropout(dh), the gradient of x, where it has dropout (else NULL: it
- * is dh); and dgain = sum over rows of dy * hat (cols floats; or NULL), or
+ * dx = dropout(dh), the gradient of x (or NULL: without dropout it is dh);
+ * and dgain = sum over rows of dy * hat (cols floats; or NULL), or
  * that added to it.  Sums in fp32 in a fixed order.  dh may be dy or dres,
  * dx too, each another one.  The workspace holds partial sums of dgain,
  * dopt_rms_norm_workspace_bytes(rows, cols) bytes, 16-byte aligned, and

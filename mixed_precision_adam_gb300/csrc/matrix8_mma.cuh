@@ -58,6 +58,11 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t at, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(at), "r"(rank));
   return out;
 }
+__device__ __forceinline__ uint32_t cluster_word(uint32_t at) {
+  uint32_t x;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
 __device__ __forceinline__ float4 cluster_load(uint32_t at) {
   float4 x;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at) : "memory");
@@ -288,8 +293,10 @@ __device__ __forceinline__ void store_four(const MulParams& p, float4 x, int64_t
 
 // The matrix unit's sums in fp32 do not round to nearest: over a long k they
 // drift, by 3e-6 of the result at 16384 and in proportion.  For fp32 results
-// it adds up kPart blocks at a time and the parts are added in registers.
-constexpr int kPart = 32;
+// it adds up kPart blocks at a time and the parts are added in registers
+// (11008 x 4096 x 16384: an error of 7e-7 for 3e-6, and 2 % of the time);
+// kPart16 for 16-bit results, so that no wait for a part grows with k.
+constexpr int kPart = 32, kPart16 = 1024;
 
 // Products of pairs of SMs; see matrix8_multiply_pair.cu.
 int launch_multiply_pair(MulParams& p, const dopt_matrix8& a, const dopt_matrix8& b, cudaStream_t s);

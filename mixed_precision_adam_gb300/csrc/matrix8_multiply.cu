@@ -173,7 +173,10 @@ __global__ void __launch_bounds__(kMulThreads, BT <= 64 ? 2 : 1) matrix8_multipl
         float* mine = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
 #pragma unroll
         for (int c = 0; c < kColumns; ++c) mine[(half * kColumns + c) * 128] = __uint_as_float(r[c]);
+        if (!ok) *failed = 1u;  // a copy of a CTA that gave up may still land on its sums
         cluster_sync();
+        uint32_t bad = 0u;
+        for (int q = 0; q < 1 << p.split_log; ++q) bad |= cluster_word(cluster_addr(smem_addr(tmem_at + 1), q));
         const int share = 1 << p.share_log, ctas = 1 << p.split_log;
         for (int c = warp - 4; c < share; c += 8) {
           const int64_t row = (int64_t)tile.m * BT + rank * share + c, n = (int64_t)tile.n * kTileN + lane * 4;
@@ -191,6 +194,7 @@ __global__ void __launch_bounds__(kMulThreads, BT <= 64 ? 2 : 1) matrix8_multipl
               if (q0 + j < ctas) sum = make_float4(sum.x + x[j].x, sum.y + x[j].y, sum.z + x[j].z, sum.w + x[j].w);
           }
           if (n >= p.n) continue;
+          if (bad) sum.x = sum.y = sum.z = sum.w = __int_as_float(0x7FC00000);
           if (p.dtype == DOPT_F32)
             store_four<float>(p, sum, n, row);
           else if (p.dtype == DOPT_BF16)
@@ -378,7 +382,7 @@ extern "C" int dopt_matrix8_multiply(const dopt_matrix8* a, const dopt_matrix8* 
     p.groups = (int32_t)scale_groups(a->cols);
     if (scale_size(std::max(a->rows, b->rows), a->cols) / 512 > INT32_MAX / 2)
       return fail(DOPT_E_SIZE, fn + "too many elements");
-    p.part = d_dtype == DOPT_F32 ? kPart : p.blocks;
+    p.part = d_dtype == DOPT_F32 ? kPart : kPart16;
     p.dtype = d_dtype;
     p.accumulate = accumulate ? 1 : 0;
     const int64_t m = a->rows, n = b->rows;

@@ -302,7 +302,6 @@ int dopt_rms_norm_backward(const dopt_rms_norm_backward_args* a, void* workspace
     }
     if (!a->dy.data || !a->h.data || !a->rstd) return fail(DOPT_E_INVALID, fn + "NULL dy, h or rstd");
     if (!a->dh.data && !a->dx.data && !a->dgain) return fail(DOPT_E_INVALID, fn + "no output");
-    if (a->dx.data && !threshold) return fail(DOPT_E_INVALID, fn + "dx without dropout (it is dh)");
     const size_t elem = dtype_bytes(a->dtype);
     if ((st = check_rows(a->dy, a->cols, elem, "dy", fn))) return st;
     if ((st = check_rows(a->h, a->cols, elem, "h", fn))) return st;

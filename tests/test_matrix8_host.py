@@ -191,7 +191,7 @@ def test_norm_of_nothing():
 @pytest.mark.parametrize("change,status", BAD_DROPS + [
     (dict(rows=-1), "E_INVALID"), (dict(cols=16385), "E_SIZE"), (dict(dtype=3), "E_INVALID"), (dict(gain=None), "E_INVALID"),
     (dict(dy=None), "E_INVALID"), (dict(h=None), "E_INVALID"), (dict(rstd=None), "E_INVALID"), (dict(rstd=6), "E_ALIGN"),
-    (dict(dgain=6), "E_ALIGN"), (dict(dx=64), "E_INVALID"),                              # dx without dropout is dh
+    (dict(dgain=6), "E_ALIGN"), (dict(dx=63), "E_ALIGN"),
     (dict(dh=None, dgain=None), "E_INVALID"), (dict(dy=4097), "E_ALIGN"), (dict(dres=3), "E_ALIGN"), (dict(ld=299), "E_INVALID"),
     (dict(ws=None), "E_INVALID"), (dict(ws=24), "E_ALIGN"), (dict(size=4 * 300 * 4 - 1), "E_SIZE")])
 def test_refused_norm_backward(change, status):

@@ -268,6 +268,13 @@ def test_norm_backward_many_rows(rows, cols):
     assert np.array_equal(first, again)
 
 
+def test_norm_backward_with_a_dropout_of_nothing():
+    """p = 0 in both passes: dx is dh."""
+    h, dy = stored(numbers(70, 300, 1), "bf16"), stored(numbers(70, 300, 2), "bf16")
+    a, _ = run_backward(h, dy, "bf16", drop=dict(DROP, p=0.0))
+    assert np.array_equal(a["dx"].numpy(), a["dh"].numpy())
+
+
 def test_norm_backward_of_no_rows():
     gain, dgain = torch.ones(9, device="cuda"), torch.full((9,), 3.0, device="cuda")
     none, r = torch.zeros(0, 9, device="cuda"), torch.zeros(0, device="cuda")
