@@ -4,7 +4,10 @@
 // of the rows of both operands, and the unit of each reads the other's half
 // of a too.  Per step along k a CTA loads 32 KB for as many products as a
 // single CTA's 128 x 256 tile makes of 48 KB, which is what the L2 has to
-// give.  Each CTA has the sums of its 128 n.
+// give.  Each CTA has the sums of its 128 n.  Measured on 16384 x 11008 x 4096
+// to bf16: 365 us, 4.04 PFLOP/s, with constant codes at 2070 MHz; 495 to 515
+// with random ones, where the power limit holds the clock at 1400 to 1480 MHz
+// (tiles of one SM, 128 x 256: 577).
 #include "matrix8_mma.cuh"
 
 namespace dopt {
