@@ -14,7 +14,9 @@ namespace dopt {
 constexpr int kTileN = 128;
 
 // BT: rows of a per tile.  Stages of the ring: as many as leave room for two
-// CTAs per SM up to 64 rows, else for one.
+// CTAs per SM up to 64 rows, else for one.  A CTA's part of TMEM is no larger
+// than its part of the shared memory (or it is alone on its SM), so no CTA of
+// these kernels waits for TMEM that another one of a waiting cluster holds.
 template <int BT>
 struct MulShape {
   static constexpr int kScaleTiles = 1 + (BT + 127) / 128;  // of 512 bytes, per stage
@@ -223,7 +225,6 @@ __global__ void __launch_bounds__(kMulThreads, BT <= 64 ? 2 : 1) matrix8_multipl
 }
 
 // --------------------------------------------------------------------- host --
-
 
 namespace {
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
