@@ -253,6 +253,65 @@ def test_the_binding_refuses_host_memory():
         refused(dopt.E_INVALID, lambda: dopt.dopt_matrix8_multiply(m, m, d))
 
 
+class OnGpu:
+    """A stand-in for a torch tensor on a GPU of this index."""
+
+    def __init__(self, index, *shape, dtype=torch.float32):
+        self.index, self.shape, self.dtype = index, shape, dtype
+
+    def data_ptr(self):
+        return 1 << 20
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+    @property
+    def nbytes(self):
+        return self.numel() * self.dtype.itemsize
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self):
+        return (self.shape[1], 1) if len(self.shape) == 2 else (1,)
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.index
+
+
+def matrix_on(index):
+    return dopt.Matrix8(OnGpu(index, 32, 48, dtype=torch.uint8), OnGpu(index, 512, dtype=torch.uint8))
+
+
+def test_arrays_of_another_gpu_than_the_current(monkeypatch):
+    """Every call is refused before a launch where one of its arrays is on another GPU than the current one: the
+    launches, and the other arrays, are on that."""
+    monkeypatch.setattr(dopt, "_current_device", lambda: 0)
+    x0, x1, g0 = OnGpu(0, 32, 48), OnGpu(1, 32, 48), OnGpu(0, 48)
+    d = lambda k: OnGpu(k, 32, 32)  # noqa: E731
+    step = dopt.Dropout(0.1, 1, d_step=OnGpu(1, 1, dtype=torch.int64))
+    r0, r1 = OnGpu(0, 32), OnGpu(1, 32)
+    back = dict(workspace=OnGpu(1, 1 << 20, dtype=torch.uint8), workspace_bytes=1 << 20, dgain=g0)
+    for call in (lambda: dopt.dopt_matrix8_multiply(matrix_on(1), matrix_on(1), d(1)),
+                 lambda: dopt.dopt_matrix8_multiply(matrix_on(0), matrix_on(0), d(1)),
+                 lambda: dopt.dopt_matrix8_multiply(matrix_on(0), matrix_on(1), d(0)),
+                 lambda: dopt.dopt_matrix8_pack(dopt.MatrixList([dict(values=x1, out=matrix_on(0))])),
+                 lambda: dopt.dopt_matrix8_unpack(dopt.MatrixList([dict(values=x1, out=matrix_on(1))])),
+                 lambda: dopt.dopt_dropout(dopt.DropoutArgs(x1, x1, dopt.Dropout(0.1, 1))),
+                 lambda: dopt.dopt_dropout(dopt.DropoutArgs(x0, x0, step)),
+                 lambda: dopt.dopt_rms_norm(dopt.RmsNormArgs(x0, g0, 1e-6, y=x1)),
+                 lambda: dopt.dopt_rms_norm(dopt.RmsNormArgs(x0, g0, 1e-6, y8=matrix_on(1))),
+                 lambda: dopt.dopt_rms_norm(dopt.RmsNormArgs(x0, g0, 1e-6, y=x0, rstd=r1)),
+                 lambda: dopt.dopt_rms_norm(dopt.RmsNormArgs(x0, g0, 1e-6, y=x0, h=x0, dropout=step)),
+                 lambda: dopt.dopt_rms_norm_backward(dopt.RmsNormBackwardArgs(x0, x1, g0, r0, x0)),
+                 lambda: dopt.dopt_rms_norm_backward(dopt.RmsNormBackwardArgs(x0, x0, g0, r0, x0, **back))):
+        text = refused(dopt.E_INVALID, call)
+        assert "GPU" in text
+
+
 # -------------------------------------------------- the 64-bit restatement --
 
 def test_places_are_a_permutation():

@@ -189,6 +189,29 @@ def test_norm_extremes():
     assert (m.scale_bytes()[6] == 255).all() and m.scale_bytes()[5].tolist() == [255] + [8] * 5
 
 
+def test_norm_of_far_rows():
+    """Rows more than 2^31 bytes apart, in place, forward and backward."""
+    rows, cols, ld = 3, 301, 2**30 + 512
+    x, dy = stored(numbers(rows, cols, 1), "bf16"), stored(numbers(rows, cols, 2), "bf16")
+    whole = torch.zeros(2 * ld + cols + 64, dtype=torch.bfloat16, device="cuda")
+    far = whole.as_strided((rows, cols), (ld, 1))
+    far.copy_(torch.from_numpy(x))
+    m, rstd = Codes(rows, cols), torch.zeros(rows, device="cuda")
+    gain = torch.ones(cols, device="cuda")
+    dopt.dopt_rms_norm(dopt.RmsNormArgs(far, gain, EPS, y=far, y8=m.m, rstd=rstd), stream=stream())
+    (r, dr), (y, d) = O.norm(x, np.ones(cols), EPS)
+    assert_near(far.double().cpu().numpy(), y, d, "bf16")
+    check_codes(m.numpy(), m.scale_bytes(), y, d)
+    assert_near(rstd.double().cpu().numpy(), r, dr, "f32")
+    far.copy_(torch.from_numpy(dy))
+    h = torch.from_numpy(x).bfloat16().cuda()
+    dopt.dopt_rms_norm_backward(dopt.RmsNormBackwardArgs(far, h, gain, rstd, far), stream=stream())
+    (dh, b), _ = O.norm_backward(dy, x, np.ones(cols), rstd.double().cpu().numpy(), None)
+    assert_near(far.double().cpu().numpy(), dh, b, "bf16")
+    far.zero_()
+    assert not bool(whole.any())
+
+
 def test_norm_in_place():
     rows, cols = 50, 300
     x, res = stored(numbers(rows, cols, 1), "bf16"), stored(numbers(rows, cols, 2), "bf16")
