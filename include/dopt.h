@@ -916,7 +916,10 @@ typedef struct {
  * value is read once.  h may be left out (data NULL) without residual and
  * dropout, when it is x.  Element i of the dropout is row * cols + column.
  * Squares are added in fp32 in a fixed order; a row whose sum of squares
- * leaves fp32's range is summed again in fp64.
+ * leaves fp32's range, or is so small that squares lost below it may count
+ * (with eps: a mean under 1e-30), is summed again in fp64, with eps as it is
+ * given.  rstd is infinite where fp32 has no such number; y and the codes are
+ * those of the formula all the same.  A row of zeros with eps 0 gives NaN.
  * h and y may be x or residual (the same rows), each another one.
  * cols <= DOPT_NORM_MAX_COLS.
  */

@@ -3,6 +3,8 @@
 // 32768 x 4096 bf16 with a residual to codes: 152 us, 6.2 TB/s of 7 bytes per
 // element; in rows of 4097 to 8192 elements that are no multiple of 8, each
 // element is its own access, and it runs at a third of that.
+#include <cfloat>
+
 #include "rms_norm.cuh"
 
 namespace dopt {
@@ -19,6 +21,7 @@ struct NormRows {
   int32_t cols;
   uint32_t groups;  // of scale bytes
   float eps;
+  double eps_wide;  // as it was given
   Drop drop;
   bool gain_f32;
 };
@@ -134,20 +137,29 @@ __global__ void __launch_bounds__(kRowBound<T, V, VEC, WARPS>, kRowCtas<T, V, VE
     }
     const float sum = row_sum<WARPS>(squares.x + squares.y, s_sum[turn]);
     turn ^= 1;
-    float rstd;
-    if (isfinite(sum)) {
-      const float m = sum / (float)p.cols + p.eps;
+    const float m = sum / (float)p.cols + p.eps;
+    float rstd, times, more = 1.f;  // h is multiplied by `times`, and by `more`
+    if (m > 1e-30f && isfinite(m)) {
       rstd = rsqrtf(m);
-      // one step of Newton's method, as rsqrtf may be two last places off
-      if (m > 1e-30f) rstd *= fmaf(-0.5f * m * rstd, rstd, 1.5f);
+      rstd *= fmaf(-0.5f * m * rstd, rstd, 1.5f);  // one step of Newton's method, as rsqrtf may be two last places off
+      times = rstd;
     } else {
+      // the squares left fp32's range, or what they lost below it may count:
+      // up to 2^-149 each, 2^-49 of the bound above
       double wide = 0.0;
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int k = 0; k < 4; ++k) wide += (double)f[v][k].x * (double)f[v][k].x + (double)f[v][k].y * (double)f[v][k].y;
       wide = row_sum_wide<WARP>(wide, s_wide);
-      rstd = (float)(1.0 / sqrt(wide / (double)p.cols + (double)p.eps));
+      const double root = 1.0 / sqrt(wide / (double)p.cols + p.eps_wide);
+      times = rstd = (float)root;
+      if (root > (double)FLT_MAX && !isinf(root)) {
+        // fp32 has no such number, but for h in two steps; the second is at
+        // most 2^29 unless the row is zeros, which stay zeros
+        times = 0x1p127f;
+        more = (float)fmin(root * 0x1p-127, 0x1p30);
+      }
     }
     if (at.g == 0 && p.rstd) p.rstd[row] = rstd;
 #pragma unroll
@@ -156,7 +168,13 @@ __global__ void __launch_bounds__(kRowBound<T, V, VEC, WARPS>, kRowCtas<T, V, VE
       float2 w[4];
       gain.of(at, v, w);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) f[v][k] = __fmul2_rn(__fmul2_rn(f[v][k], both_of(rstd)), w[k]);
+      for (int k = 0; k < 4; ++k) f[v][k] = __fmul2_rn(f[v][k], both_of(times));
+      if (more != 1.f) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[v][k] = __fmul2_rn(f[v][k], both_of(more));
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[v][k] = __fmul2_rn(f[v][k], w[k]);
       if (p.y.data) Piece::store(static_cast<T*>(p.y.data) + row * p.y.ld + c, p.cols - c, f[v]);
       if (p.codes) store_codes<VEC>(p, row, c, f[v]);
     }
@@ -263,6 +281,7 @@ int dopt_rms_norm(const dopt_rms_norm_args* a, dopt_stream stream) {
     p.cols = (int32_t)a->cols;
     p.groups = (uint32_t)scale_groups(a->cols);
     p.eps = (float)a->eps;
+    p.eps_wide = a->eps;
     p.drop = make_drop(a->drop, threshold);
     const bool vec = a->cols % 8 == 0 && aligned_to(a->gain, 16) && rows_vec(a->x, elem) && rows_vec(a->residual, elem) && rows_vec(a->h, elem) && rows_vec(a->y, elem);
     p.gain_f32 = a->gain_dtype == DOPT_F32;
