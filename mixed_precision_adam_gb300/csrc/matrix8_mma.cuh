@@ -68,7 +68,10 @@ __device__ __forceinline__ float4 cluster_load(uint32_t at) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at) : "memory");
   return x;
 }
+// A cluster's barrier.  It, like the loads from TMEM, wants the lanes of a
+// warp together, which they need not be after a branch of their own.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 template <int CTAS>

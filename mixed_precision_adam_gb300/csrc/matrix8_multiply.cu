@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(kMulThreads, BT <= 64 ? 2 : 1) matrix8_multipl
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(taken);
+        __syncwarp();
       }
       if (!ok) {
 #pragma unroll

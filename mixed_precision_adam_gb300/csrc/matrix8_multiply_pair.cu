@@ -186,6 +186,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMulThreads)
           tmem_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(taken_by);
+          __syncwarp();  // loads from TMEM follow
         };
         // the columns that the other set shares first: the last of the first
         // set, the first of the second

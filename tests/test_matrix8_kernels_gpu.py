@@ -1,0 +1,47 @@
+"""Products in each of their kernels: which one ran, and what each has of its
+own."""
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import mixed_precision_adam_gb300 as dopt  # noqa: E402
+from kernel_nodes import kernels_of  # noqa: E402
+from matrices_harness import Codes  # noqa: E402
+from test_matrix8_gpu import check_product  # noqa: E402
+
+
+def kernel_of(m, n, k, dtype=torch.float32):
+    """(rows of a per tile or "pair", CTAs that share a tile's k) of the kernel that a product of this size takes."""
+    a, b, d = Codes(m, k), Codes(n, k), torch.zeros(m, n, dtype=dtype, device="cuda")
+    dopt.dopt_matrix8_multiply(a.m, b.m, d, stream=torch.cuda.current_stream())
+    (name, ctas, _), = kernels_of(lambda s: dopt.dopt_matrix8_multiply(a.m, b.m, d, stream=s))
+    if "matrix8_multiply_pair" in name:
+        return "pair", 1
+    for rows in (16, 32, 64, 128):
+        for split in (0, 1):
+            if f"matrix8_multiplyILi{rows}ELb{split}E" in name:
+                assert split == (ctas > 1)
+                return rows, ctas
+    raise AssertionError(name)
+
+
+# Few columns of the last tile, not by four: of a warp some lanes store four, one some, the others none.
+SPLITS = {(16, 2): (10, 16898, 3000), (16, 4): (10, 2435, 4096), (16, 8): (10, 130, 4096),
+          (32, 2): (30, 16899, 3000), (32, 4): (30, 4994, 2048), (32, 8): (20, 129, 4096),
+          (64, 2): (60, 16897, 4000), (64, 4): (60, 4993, 3000), (64, 8): (60, 131, 4096),
+          (128, 2): (100, 5890, 5000), (128, 4): (100, 2945, 4096), (128, 8): (100, 257, 4096)}
+
+
+@pytest.mark.parametrize("which", sorted(SPLITS))
+def test_parts_of_k_of_partial_columns(which):
+    """A cluster adds up its CTAs' parts of k; lanes of a warp that store differently meet again at its barriers."""
+    m, n, k = SPLITS[which]
+    assert kernel_of(m, n, k) == which
+    outputs = [("f32", False, 0), ("bf16", False, 3), ("f16", True, 1)]
+    for dtype, add, pad in outputs if n < 1000 else [outputs[m % 3]]:
+        check_product(m, n, k, dtype, add=add, pad=pad)
