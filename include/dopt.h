@@ -893,7 +893,7 @@ typedef struct {
   int32_t reserved;
   const void* x;
   const void* residual; /* added after the dropout; NULL: none               */
-  void* y;              /* may be x or residual                              */
+  void* y;              /* may be x or residual, no other part of them       */
   dopt_drop drop;
 } dopt_dropout_args;
 
@@ -920,7 +920,10 @@ typedef struct {
  * (with eps: a mean under 1e-30), is summed again in fp64, with eps as it is
  * given.  rstd is infinite where fp32 has no such number; y and the codes are
  * those of the formula all the same.  A row of zeros with eps 0 gives NaN.
- * h and y may be x or residual (the same rows), each another one.
+ * h and y may be x or residual (the same rows), each another one.  Two
+ * outputs in one array are refused, and so is an output that shares elements
+ * at different places with another array whose rows are as far apart or begin
+ * where its do; so they are in the backward pass.
  * cols <= DOPT_NORM_MAX_COLS.
  */
 typedef struct {

@@ -89,6 +89,9 @@ extern "C" int dopt_dropout(const dopt_dropout_args* a, dopt_stream stream) {
     const size_t elem = dtype_bytes(a->dtype);
     if (!aligned_to(a->x, elem) || !aligned_to(a->y, elem) || !aligned_to(a->residual, elem))
       return fail(DOPT_E_ALIGN, fn + "an array is not aligned to its elements");
+    int st = check_shared(shared_elements(a->y, 0, a->x, 0, 1, a->numel, elem), false, "y", "x", fn);
+    if (!st) st = check_shared(shared_elements(a->y, 0, a->residual, 0, 1, a->numel, elem), false, "y", "residual", fn);
+    if (st) return st;
     p.x = a->x;
     p.residual = a->residual;
     p.y = a->y;

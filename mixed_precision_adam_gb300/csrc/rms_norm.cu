@@ -4,6 +4,7 @@
 // element; in rows of 4097 to 8192 elements that are no multiple of 8, each
 // element is its own access, and it runs at a third of that.
 #include <cfloat>
+#include <initializer_list>
 
 #include "rms_norm.cuh"
 
@@ -232,6 +233,24 @@ int check_norm(int64_t rows, int64_t cols, int32_t dtype, int32_t gain_dtype, co
   return DOPT_OK;
 }
 
+// The outputs of a call (those that are there) and what they share with each
+// other and with the inputs.
+struct NamedRows {
+  const dopt_rows& r;
+  const char* name;
+};
+int check_shared_rows(std::initializer_list<NamedRows> outputs, std::initializer_list<NamedRows> inputs, int64_t rows, int64_t cols,
+                      size_t elem, const std::string& fn) {
+  for (const NamedRows* a = outputs.begin(); a != outputs.end(); ++a) {
+    const auto shared = [&](const NamedRows& b) { return shared_elements(a->r.data, a->r.ld, b.r.data, b.r.ld, rows, cols, elem); };
+    for (const NamedRows* b = a + 1; b != outputs.end(); ++b)
+      if (int st = check_shared(shared(*b), true, a->name, b->name, fn)) return st;
+    for (const NamedRows& b : inputs)
+      if (int st = check_shared(shared(b), false, a->name, b.name, fn)) return st;
+  }
+  return DOPT_OK;
+}
+
 bool rows_vec(const dopt_rows& r, size_t elem) { return !r.data || eight_vectors(r.data, r.ld, elem); }
 
 int64_t parts_of(int64_t rows, int64_t cols) { return std::min<int64_t>(rows, max_parts(cols)); }
@@ -266,6 +285,7 @@ int dopt_rms_norm(const dopt_rms_norm_args* a, dopt_stream stream) {
     if ((st = check_rows(a->y, a->cols, elem, "y", fn))) return st;
     if (a->y8 && (st = check_matrix8(*a->y8, fn + "y8: "))) return st;
     if (!aligned_to(a->rstd, 4)) return fail(DOPT_E_ALIGN, fn + "rstd not aligned to its elements");
+    if ((st = check_shared_rows({{a->h, "h"}, {a->y, "y"}}, {{a->x, "x"}, {a->residual, "residual"}}, a->rows, a->cols, elem, fn))) return st;
     p.x = RowsIn{a->x.data, a->x.ld};
     p.residual = RowsIn{a->residual.data, a->residual.ld};
     p.h = RowsOut{a->h.data, a->h.ld};
@@ -330,6 +350,8 @@ int dopt_rms_norm_backward(const dopt_rms_norm_backward_args* a, void* workspace
     if ((st = check_rows(a->dres, a->cols, elem, "dres", fn))) return st;
     if ((st = check_rows(a->dh, a->cols, elem, "dh", fn))) return st;
     if ((st = check_rows(a->dx, a->cols, elem, "dx", fn))) return st;
+    if ((st = check_shared_rows({{a->dh, "dh"}, {a->dx, "dx"}}, {{a->dy, "dy"}, {a->h, "h"}, {a->dres, "dres"}}, a->rows, a->cols, elem, fn)))
+      return st;
     if (a->dgain) {
       if (!workspace) return fail(DOPT_E_INVALID, fn + "NULL workspace");
       if (!aligned_to(workspace, 16)) return fail(DOPT_E_ALIGN, fn + "workspace not 16-byte aligned");
