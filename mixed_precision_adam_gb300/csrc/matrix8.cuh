@@ -10,6 +10,7 @@
 #include <cuda_fp8.h>
 
 #include "entry.h"
+#include "memset.h"
 #include "tensors.cuh"
 
 namespace dopt {

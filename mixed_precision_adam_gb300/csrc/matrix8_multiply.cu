@@ -372,8 +372,7 @@ extern "C" int dopt_matrix8_multiply(const dopt_matrix8* a, const dopt_matrix8* 
     const cudaStream_t s = (cudaStream_t)stream;
     if (a->cols == 0) {
       if (accumulate) return DOPT_OK;
-      const cudaError_t e = cudaMemset2DAsync(d, (size_t)ldd * elem, 0, (size_t)b->rows * elem, (size_t)a->rows, s);
-      return e == cudaSuccess ? DOPT_OK : fail(DOPT_E_CUDA, fn + cudaGetErrorString(e));
+      return check_memset(cudaMemset2DAsync(d, (size_t)ldd * elem, 0, (size_t)b->rows * elem, (size_t)a->rows, s), fn);
     }
     if ((st = check_matrix8(*a, fn + "a: "))) return st;
     if ((st = check_matrix8(*b, fn + "b: "))) return st;

@@ -336,10 +336,7 @@ int dopt_rms_norm_backward(const dopt_rms_norm_backward_args* a, void* workspace
     if (!aligned_to(a->dgain, 4) || !aligned_to(a->rstd, 4))
       return fail(DOPT_E_ALIGN, fn + "dgain or rstd not aligned to its elements");
     if (a->rows == 0) {
-      if (a->dgain && !a->accumulate) {
-        const cudaError_t e = cudaMemsetAsync(a->dgain, 0, (size_t)a->cols * sizeof(float), s);
-        if (e != cudaSuccess) return fail(DOPT_E_CUDA, fn + cudaGetErrorString(e));
-      }
+      if (a->dgain && !a->accumulate) return check_memset(cudaMemsetAsync(a->dgain, 0, (size_t)a->cols * sizeof(float), s), fn);
       return DOPT_OK;
     }
     if (!a->dy.data || !a->h.data || !a->rstd) return fail(DOPT_E_INVALID, fn + "NULL dy, h or rstd");

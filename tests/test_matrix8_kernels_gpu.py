@@ -45,3 +45,19 @@ def test_parts_of_k_of_partial_columns(which):
     outputs = [("f32", False, 0), ("bf16", False, 3), ("f16", True, 1)]
     for dtype, add, pad in outputs if n < 1000 else [outputs[m % 3]]:
         check_product(m, n, k, dtype, add=add, pad=pad)
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+def test_product_of_nothing_into_far_rows(rows):
+    """Without columns the sums are 0, also in rows more than 2^31 bytes apart, and only there."""
+    ld = 2**30 + 512
+    whole = torch.ones((rows - 1) * ld + 64, dtype=torch.bfloat16, device="cuda")
+    d = whole.as_strided((rows, 5), (ld, 1))
+    a, b = Codes(rows, 0), Codes(5, 0)
+    for add in (True, False):
+        dopt.dopt_matrix8_multiply(a.m, b.m, d, accumulate=add, stream=torch.cuda.current_stream())
+        assert bool((d == int(add)).all())
+        d.fill_(1)
+        assert bool((whole == 1).all())
+    # nothing is left for the next call to find
+    check_product(rows, 5, 40, "bf16")
