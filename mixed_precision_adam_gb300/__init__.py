@@ -891,6 +891,11 @@ def _tensor(x, name, dtypes, devices, who=""):
     return x.data_ptr(), dt
 
 
+def _must_be(x, cls, name, who=""):
+    if not isinstance(x, cls):
+        raise DoptError(E_INVALID, f"{who}{name} is not a {cls.__name__}")
+
+
 def _matrix(x, name, dtypes, devices, shape=None, who=""):
     """(pointer, elements from row to row, dtype name) of a 2-d torch tensor
     whose rows are contiguous, of `shape` unless that is None."""
@@ -955,6 +960,7 @@ class MatrixList:
                 m = e.get(name)
                 if m is None:
                     continue
+                _must_be(m, Matrix8, name, who)
                 if (m.rows, m.cols) != shape:
                     raise DoptError(E_INVALID, f"{who}{name} is {m.rows} x {m.cols}, not {shape[0]} x {shape[1]}")
                 setattr(t, name, m.c)
@@ -987,6 +993,8 @@ def dopt_matrix8_multiply(a, b, d, accumulate=False, stream=None):
     if fits:
         ptr = d.data_ptr()
     else:
+        _must_be(a, Matrix8, "a")
+        _must_be(b, Matrix8, "b")
         devices = set()
         ptr, ld, name = _matrix(d, "d", _DTYPE, devices, (a.rows, b.rows))
         dt = _dtype_codes[d.dtype] = _DTYPE[name]
@@ -1019,6 +1027,7 @@ class _Args:
 
     def _close(self, devices, dropout, keep):
         if dropout is not None:
+            _must_be(dropout, Dropout, "dropout")
             self.c.drop = dropout.c
             devices = devices | dropout.devices
         self._keep, self.gpu = (keep, dropout), _one_device(devices)
@@ -1036,8 +1045,9 @@ class DropoutArgs(_Args):
     def __init__(self, x, y, dropout, residual=None):
         d = set()
         self.c = dopt_dropout_args()
+        self.c.x, dt = _tensor(x, "x", _DTYPE, d)
         self.c.numel = x.numel()
-        self.c.x, dt = _vector(x, "x", _DTYPE, d, x.numel())
+        _vector(x, "x", _DTYPE, d, x.numel())
         self.c.y, _ = _vector(y, "y", (dt,), d, x.numel())
         if residual is not None:
             self.c.residual, _ = _vector(residual, "residual", (dt,), d, x.numel())
@@ -1073,6 +1083,7 @@ class RmsNormArgs(_Args):
                 setattr(c, name, dopt_rows(*_matrix(t, name, (dt,), d, x.shape)[:2]))
         _gain(c, gain, dt, c.cols, d)
         if y8 is not None:
+            _must_be(y8, Matrix8, "y8")
             if (y8.rows, y8.cols) != tuple(x.shape):
                 raise DoptError(E_INVALID, f"y8 is {y8.rows} x {y8.cols}, not {c.rows} x {c.cols}")
             c.y8 = ctypes.pointer(y8.c)
