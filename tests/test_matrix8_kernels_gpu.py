@@ -12,7 +12,7 @@ if not torch.cuda.is_available():
 import mixed_precision_adam_gb300 as dopt  # noqa: E402
 from kernel_nodes import kernels_of  # noqa: E402
 from matrices_harness import Codes  # noqa: E402
-from test_matrix8_gpu import check_product  # noqa: E402
+from test_matrix8_gpu import PAIRS, check_product  # noqa: E402
 
 
 def kernel_of(m, n, k, dtype=torch.float32):
@@ -61,3 +61,12 @@ def test_product_of_nothing_into_far_rows(rows):
         assert bool((whole == 1).all())
     # nothing is left for the next call to find
     check_product(rows, 5, 40, "bf16")
+
+
+@pytest.mark.parametrize("which,sizes", [(("pair", 1), PAIRS[0]), (("pair", 1), PAIRS[1]), (("pair", 1), (16384, 11008, 4096)),
+                                         ((16, 1), (3, 39000, 200)), ((32, 1), (30, 39000, 200)), ((64, 1), (60, 39000, 200)),
+                                         ((128, 1), (100, 39000, 200)), ((128, 1), (2049, 2500, 600)), ((128, 1), (700, 11000, 384))])
+def test_the_kernel_that_other_tests_are_meant_for(which, sizes):
+    """Sizes by which test_matrix8_gpu.py reaches each kernel, and the one that a large product takes."""
+    for dtype in (torch.float32, torch.bfloat16):
+        assert kernel_of(*sizes, dtype) == which
