@@ -12,6 +12,7 @@ if not torch.cuda.is_available():
 import mixed_precision_adam_gb300 as dopt  # noqa: E402
 from kernel_nodes import kernels_of  # noqa: E402
 from matrices_harness import Codes  # noqa: E402
+from oracle import matrices as O  # noqa: E402
 from test_matrix8_gpu import PAIRS, check_product  # noqa: E402
 
 
@@ -70,3 +71,33 @@ def test_the_kernel_that_other_tests_are_meant_for(which, sizes):
     """Sizes by which test_matrix8_gpu.py reaches each kernel, and the one that a large product takes."""
     for dtype in (torch.float32, torch.bfloat16):
         assert kernel_of(*sizes, dtype) == which
+
+
+# Sums along k that have no sign: what the matrix unit loses adds up.  fp32 results are summed there over 4096 of k at
+# most, so a term passes 32 additions in its step and 128 from step to step, each off by at most one last place (2 U),
+# and then additions to nearest (U): of 65 parts, and of a cluster's eight CTAs.  Summed there whole, 262144 of k and more
+# are off by 5e-5 (as measured 3.1e-6 at 16384, in proportion) to 1.7e-4 (if every step cuts off what does not fit).
+K = 262144 + 200
+PARTS_BOUND = 2 * O.U * (32 + 128) + O.U * (65 + 8)
+
+
+@pytest.mark.parametrize("which,m,n", [((16, 8), 3, 200), ((128, 8), 100, 300), ((128, 1), 100, 9800), (("pair", 1), 1000, 3900)])
+def test_sums_of_one_sign_along_a_long_k(which, m, n):
+    gen = torch.Generator("cuda").manual_seed(m + n)
+    a, b = (torch.randint(1, 64, (rows, -(-K // 16) * 16), generator=gen, device="cuda", dtype=torch.uint8)[:, :K] for rows in (m, n))
+    ma, mb = (dopt.Matrix8(x, torch.full((dopt.dopt_matrix8_scale_bytes(*x.shape),), 127, dtype=torch.uint8, device="cuda")) for x in (a, b))
+    at = torch.tensor(sorted({0, 1, m // 2, m - 1}), device="cuda")
+
+    def numbers(codes):
+        return codes.contiguous().view(torch.float8_e4m3fn).double()
+
+    want = torch.cat([numbers(a[at]) @ numbers(b[c:c + 500]).t() for c in range(0, n, 500)], 1)
+    d = torch.zeros(m, n, device="cuda")
+    dopt.dopt_matrix8_multiply(ma, mb, d, stream=torch.cuda.current_stream())
+    assert float((d[at].double() / want - 1).abs().max()) < PARTS_BOUND < 2.4e-5
+    assert kernel_of(m, n, K) == which
+    # 16-bit results: as many as 131072 of k there, so two parts and more here
+    d = d.bfloat16()
+    dopt.dopt_matrix8_multiply(ma, mb, d, stream=torch.cuda.current_stream())
+    assert kernel_of(m, n, K, torch.bfloat16) == which
+    assert float((d[at].double() / want - 1).abs().max()) < O.EPS["bf16"] + 2 * O.U * (32 + K / 32 + 8)
