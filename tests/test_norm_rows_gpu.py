@@ -53,3 +53,19 @@ def test_norm_backward_of_many_rows(cols, rows, dtype):
     _, first = run_backward(h, dy, dtype, dres=dres, drop=DROP)
     _, again = run_backward(h, dy, dtype, dres=dres, drop=DROP)
     assert np.array_equal(first, again)
+
+
+@pytest.mark.parametrize("rows", [1, 8, 64, 153, 608, 1216, 5000])
+def test_norm_backward_leaves_no_sm_without_work(rows):
+    """With dgain too: a CTA per row up to the SMs, and no fewer CTAs than those after that; never more partial sums than
+    the workspace holds."""
+    cols, sms = 1024, torch.cuda.get_device_properties(0).multi_processor_count
+    h, dy = values(rows, cols, 1, "bf16"), values(rows, cols, 2, "bf16")
+    run_backward(h, dy, "bf16", add=True)
+    x, g, r = torch.ones(rows, cols, dtype=TORCH["bf16"], device="cuda"), torch.ones(cols, device="cuda"), torch.ones(rows, device="cuda")
+    size = dopt.dopt_rms_norm_workspace_bytes(rows, cols)
+    args = dopt.RmsNormBackwardArgs(x, x, g, r, x.clone(), dgain=g.clone(), workspace=torch.empty(size, dtype=torch.uint8, device="cuda"),
+                                    workspace_bytes=size)
+    dopt.dopt_rms_norm_backward(args, stream=torch.cuda.current_stream())
+    ctas = kernels_of(lambda s: dopt.dopt_rms_norm_backward(args, stream=s))[0][2]
+    assert min(rows, sms) <= ctas <= size // (4 * cols)
