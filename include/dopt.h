@@ -879,6 +879,14 @@ int dopt_matrix8_multiply(const dopt_matrix8* a, const dopt_matrix8* b, void* d,
  * and on as there.  The same call on the gradient is the backward pass: give
  * it the same numbers (with d_step, before the step counts).  A dropped
  * element is 0 whatever it was.
+ * All dropouts read one sequence of 2^32 pairs of numbers, each from its own
+ * place on: the mask of (seed', site', t') is that of (seed, site, t) moved
+ * by (key' - key) * 0x144CBC89 pairs (mod 2^32), key = seed + site *
+ * 0x510E527F + t * 0x6A09E667.  So masks of different sites and steps are not
+ * independent: an array of 2^27 elements is 1/64 of the sequence, and some
+ * overlap (site + 19 at t - 4 is moved by 4122407 pairs, site + 13 by 39608715,
+ * t + 43 by 5865525).  A site also has the numbers that the list's step rounds
+ * the tensor of that number with at the same seed and t.
  */
 typedef struct {
   double p; /* T at most 65535; 0: no dropout                                */
