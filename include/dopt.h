@@ -905,7 +905,8 @@ typedef struct {
   dopt_drop drop;
 } dopt_dropout_args;
 
-/* y = dropout(x) + residual, rounded once; arrays aligned to their elements. */
+/* y = dropout(x) + residual; the product and the sum each rounded in fp32, and
+ * then once to dtype.  Arrays aligned to their elements. */
 int dopt_dropout(const dopt_dropout_args* args, dopt_stream stream);
 
 /* Rows of a matrix: `ld` elements from a row to the next, each aligned to
@@ -918,7 +919,7 @@ typedef struct {
 #define DOPT_NORM_MAX_COLS 16384
 
 /*
- * RMS norm of the rows of h = dropout(x) + residual (rounded to dtype):
+ * RMS norm of the rows of h = dropout(x) + residual (rounded as there):
  *   rstd = 1 / sqrt(mean(h^2) + eps);  y = h * rstd * gain,
  * as values (y), as codes (y8: blocks of rows, rows x cols), or both.  Each
  * value is read once.  h may be left out (data NULL) without residual and
