@@ -1,8 +1,10 @@
 // rms_norm.cu -- the RMS norm with dropout and the residual's addition before
 // it, values or 8-bit codes out, and the C entry points of the norm.
-// 32768 x 4096 bf16 with a residual to codes: 152 us, 6.2 TB/s of 7 bytes per
-// element; in rows of 4097 to 8192 elements that are no multiple of 8, each
-// element is its own access, and it runs at a third of that.
+// 32768 x 4096 bf16 with a residual to codes: 150 us, 6.3 TB/s of 7 bytes per
+// element (with dropout 190, bound by instructions); to values 169, 6.4 of 8,
+// with dropout too.  16-bit rows off the vector grid take an access per
+// element and run at half of that: 769 to 5501 columns 2.8 to 3.1 TB/s to
+// codes, 3.6 to 4.3 to values.
 #include <cfloat>
 #include <initializer_list>
 
